@@ -74,6 +74,7 @@ typedef enum pkvqk_status {
 #define PKVQK_FLAG_BAD_SLOT      0x1  /* slot >= num_blocks*block_size: skipped */
 #define PKVQK_FLAG_BAD_BLOCK_ID  0x2  /* block id outside [0, num_blocks): its keys read as zeros */
 #define PKVQK_FLAG_WAIT_TIMEOUT  0x4  /* a pipeline wait gave up: output invalid */
+#define PKVQK_FLAG_BAD_VALUE     0x8  /* 8-bit append: a k or v value that is not finite */
 
 /*
  * Layout of a paged cache, shared by the K and the V cache of a layer:
@@ -96,6 +97,39 @@ typedef struct pkvqk_cache_layout {
   int64_t slot_stride;
   int64_t head_stride;
 } pkvqk_cache_layout;
+
+/* Code formats of an 8-bit cache. */
+typedef enum pkvqk_q8_format {
+  PKVQK_Q8_E4M3 = 1,                 /* 1-4-3 floating point, largest value 448 */
+  PKVQK_Q8_INT8 = 2                  /* two's complement, -127 .. 127 */
+} pkvqk_q8_format;
+
+/*
+ * A layer's 8-bit K and V caches: one code a value, and one fp32 scale for
+ * each group of 16 consecutive slots of a page and kv head, K and V apart;
+ * the value is code * scale.  Codes follow `layout` (one byte an element; the
+ * strides, in elements, are multiples of 16 here); the scale of (block, slot,
+ * head) lives at
+ *     scales + block*scale_block_stride + (slot / 16)*scale_group_stride
+ *            + head*scale_head_stride
+ * (positive strides; e.g. [num_blocks, block_size / 16, num_kv_heads]).
+ * pkvqk_norm_rope_append_q8 writes powers of two from 2^-64 to 2^63; the
+ * attention calls take any positive scale in that range and move others (0,
+ * negative, NaN) to its nearest end, NaN to 2^-64.  Per key and kv head the
+ * pair takes 2*(128 + 4/16) bytes, 0.501 of a bf16 cache.
+ */
+typedef struct pkvqk_q8_cache {
+  void* k;                           /* device codes, 16-byte aligned */
+  void* v;
+  float* k_scales;                   /* device scales, 4-byte aligned */
+  float* v_scales;
+  pkvqk_cache_layout layout;
+  int32_t format;                    /* pkvqk_q8_format, of K and of V */
+  int32_t reserved;                  /* set to 0 */
+  int64_t scale_block_stride;
+  int64_t scale_group_stride;
+  int64_t scale_head_stride;
+} pkvqk_q8_cache;
 
 /* Message of the last failing call made on this thread ("" if none). */
 PKVQK_API const char* pkvqk_last_error(void);
@@ -183,6 +217,50 @@ PKVQK_API pkvqk_status pkvqk_norm_rope_append_cached(
     int32_t* status_flags, pkvqk_stream_t stream);
 
 /*
+ * pkvqk_norm_rope_append into an 8-bit cache: the same norm and rotation of q
+ * and k (angles from rope_table for positions 0 .. table_positions-1, computed
+ * for others; table_positions 0: all computed), q written to q_out (which may
+ * be q), rotated k and v quantised from fp32 with one rounding.
+ *
+ * For every group of 16 slots that the call writes, per kv head and for K and
+ * V apart, with a the largest |value| that it writes there and M = 448 (e4m3)
+ * or 127 (int8):
+ *   2^e, e the smallest integer in -64 .. 63 with a <= M*2^e (at most 63)
+ *   scale = 2^e                        where slot 0 of the group is written,
+ *         = max(2^e, stored scale)     elsewhere: the group holds earlier tokens
+ *   code  = value / scale, to the nearest code, ties to even
+ * and where the stored scale grew, the codes of the group's other slots are
+ * rescaled (code * old / new, to the nearest), so that earlier tokens keep
+ * their values.  Writing slot 0 starts a group anew: what other slots of it
+ * hold is free.  A stored scale outside 2^-64 .. 2^63 counts as 2^-64.
+ * Values beyond M*scale (infinities, or a scale at its limit) become the
+ * largest code, NaN becomes 0, and neither counts for a; PKVQK_FLAG_BAD_VALUE
+ * reports values that are not finite.
+ *
+ * Tokens of one call whose slots lie in one group must be adjacent in token
+ * order (as the consecutive tokens of a sequence are), with no other token and
+ * no padding between them; otherwise, as when two tokens share a slot, the
+ * group's contents are undefined.  Results do not depend on how a sequence's
+ * other groups are spread over calls.
+ *
+ *   q, k, v, positions, slot_mapping, gamma_q/_k, theta, eps: as
+ *   pkvqk_norm_rope_append; q_out as q (own strides); rope_table as
+ *   pkvqk_norm_rope_append_cached
+ */
+PKVQK_API pkvqk_status pkvqk_norm_rope_append_q8(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+    const void* k, int64_t k_stride_t, int64_t k_stride_h,
+    const void* v, int64_t v_stride_t, int64_t v_stride_h,
+    const int64_t* positions, const int64_t* slot_mapping,
+    const void* gamma_q, const void* gamma_k,
+    float theta, float eps,
+    int32_t num_tokens, int32_t num_q_heads,
+    const pkvqk_q8_cache* cache,
+    const void* rope_table, int32_t table_positions,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+/*
  * Schedule for pkvqk_paged_decode from host-side facts only (no device
  * read): batch, kv heads, rows per kv head (q_len * Hq/Hkv), the longest
  * sequence, the total key count and the SM count (0 = query the current
@@ -263,6 +341,27 @@ PKVQK_API size_t pkvqk_decode_workspace_bytes(int32_t batch, int32_t q_len,
 PKVQK_API pkvqk_status pkvqk_paged_decode(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,
     const void* k_cache, const void* v_cache, const pkvqk_cache_layout* layout,
+    const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens,
+    int32_t batch, int32_t q_len, int32_t num_q_heads,
+    int32_t num_splits, int32_t max_seq_len_hint, float scale,
+    void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+/*
+ * pkvqk_paged_decode over an 8-bit cache: the same definition with K_n and V_n
+ * = code * scale, the same schedules, pkvqk_choose_num_splits and
+ * pkvqk_decode_workspace_bytes.  Codes and q enter the products exactly (q is
+ * scaled by a power of two per row first), sums are fp32, softmax weights are
+ * rounded to 2^-11.  Slots at or past seq_lens[b] may hold any code and scale;
+ * an e4m3 NaN code of a visible V makes NaN of every row of its sequence and
+ * kv head.
+ * At most 16 rows per kv head (q_len*Hq/Hkv).
+ */
+PKVQK_API pkvqk_status pkvqk_paged_decode_q8(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const pkvqk_q8_cache* cache,
     const int32_t* block_tables, int32_t max_blocks_per_seq,
     const int32_t* seq_lens,
     int32_t batch, int32_t q_len, int32_t num_q_heads,

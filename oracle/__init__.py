@@ -38,3 +38,10 @@ from .reference import (  # noqa: F401
     split_page_ranges,
     lse_combine,
 )
+from .quantised import (  # noqa: F401
+    q8_append,
+    q8_bytes,
+    q8_round,
+    q8_scale_exponent,
+    q8_values,
+)

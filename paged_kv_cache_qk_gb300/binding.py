@@ -38,6 +38,10 @@ STATUS_NAMES = {0: "OK", 1: "INVALID_ARG", 2: "UNSUPPORTED", 3: "WORKSPACE_TOO_S
 FLAG_BAD_SLOT = 0x1
 FLAG_BAD_BLOCK_ID = 0x2
 FLAG_WAIT_TIMEOUT = 0x4
+FLAG_BAD_VALUE = 0x8
+
+Q8_E4M3 = 1
+Q8_INT8 = 2
 
 
 class CacheLayout(ctypes.Structure):
@@ -51,6 +55,22 @@ class CacheLayout(ctypes.Structure):
         ("block_stride", c_i64),
         ("slot_stride", c_i64),
         ("head_stride", c_i64),
+    ]
+
+
+class Q8Cache(ctypes.Structure):
+    """Mirror of ``pkvqk_q8_cache``."""
+    _fields_ = [
+        ("k", c_vp),
+        ("v", c_vp),
+        ("k_scales", c_vp),
+        ("v_scales", c_vp),
+        ("layout", CacheLayout),
+        ("format", c_i32),
+        ("reserved", c_i32),
+        ("scale_block_stride", c_i64),
+        ("scale_group_stride", c_i64),
+        ("scale_head_stride", c_i64),
     ]
 
 
@@ -122,6 +142,29 @@ pkvqk_paged_prefill_varlen = _sig("pkvqk_paged_prefill_varlen", ctypes.c_int, [
     c_i32, c_i32, c_f32,                # num_splits, max_seq_len_hint, scale
     c_vp, c_vp, c_vp, c_size, c_vp, c_vp])
 
+pkvqk_norm_rope_append_q8 = _sig("pkvqk_norm_rope_append_q8", ctypes.c_int, [
+    c_vp, c_i64, c_i64,                 # q, strides
+    c_vp, c_i64, c_i64,                 # q_out
+    c_vp, c_i64, c_i64,                 # k
+    c_vp, c_i64, c_i64,                 # v
+    c_vp, c_vp,                         # positions, slot_mapping
+    c_vp, c_vp,                         # gamma_q, gamma_k
+    c_f32, c_f32,                       # theta, eps
+    c_i32, c_i32,                       # num_tokens, num_q_heads
+    ctypes.POINTER(Q8Cache),
+    c_vp, c_i32,                        # rope_table, table_positions
+    c_vp, c_vp])                        # status_flags, stream
+_decode_q8_args = [
+    c_vp, c_i64, c_i64,                 # q, strides
+    ctypes.POINTER(Q8Cache),
+    c_vp, c_i32,                        # block_tables, max_blocks_per_seq
+    c_vp,                               # seq_lens
+    c_i32, c_i32, c_i32,                # batch, q_len, num_q_heads
+    c_i32, c_i32, c_f32,                # num_splits, max_seq_len_hint, scale
+]
+pkvqk_paged_decode_q8 = _sig("pkvqk_paged_decode_q8", ctypes.c_int,
+                             _decode_q8_args + [c_vp, c_vp, c_vp, c_size, c_vp, c_vp])
+
 EXPORTED = [
     "pkvqk_last_error", "pkvqk_abi_version", "pkvqk_norm_rope_append",
     "pkvqk_choose_num_splits", "pkvqk_decode_workspace_bytes", "pkvqk_paged_decode",
@@ -129,6 +172,7 @@ EXPORTED = [
     "pkvqk_static_workspace_capacity", "pkvqk_choose_prefill_splits",
     "pkvqk_prefill_workspace_bytes", "pkvqk_paged_prefill", "pkvqk_paged_prefill_varlen",
     "pkvqk_rope_table_bytes", "pkvqk_rope_table_build", "pkvqk_norm_rope_append_cached",
+    "pkvqk_norm_rope_append_q8", "pkvqk_paged_decode_q8",
 ]
 
 
@@ -324,5 +368,70 @@ def paged_prefill_varlen(q, cu_seqlens_q, max_q_len, k_cache, v_cache, block_tab
         _ptr(k_cache), _ptr(v_cache), ctypes.byref(lay),
         _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
         B, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
+        _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
+        _ptr(status_flags), _stream(stream)))
+
+
+# ------------------------------------------------------------- 8-bit caches
+
+def q8_cache(k_cache, v_cache, k_scales, v_scales) -> Q8Cache:
+    """The C description of an 8-bit cache.
+
+    k_cache, v_cache: [num_blocks, block_size, num_kv_heads, head_dim] views of one
+    layout, float8_e4m3fn or int8; k_scales, v_scales: fp32 [num_blocks,
+    block_size // 16, num_kv_heads] views of one layout.
+    """
+    torch = _torch()
+    formats = {torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8}
+    if k_cache.dtype not in formats or v_cache.dtype != k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be float8_e4m3fn or int8")
+    if tuple(v_cache.stride()) != tuple(k_cache.stride()) or v_cache.shape != k_cache.shape:
+        raise ValueError("k_cache and v_cache must share one layout")
+    nb, bs, hkv, _ = k_cache.shape
+    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32:
+        raise ValueError("scales must be float32")
+    if (tuple(k_scales.shape) != (nb, bs // 16, hkv) or v_scales.shape != k_scales.shape
+            or k_scales.stride() != v_scales.stride()):
+        raise ValueError("scales must be [num_blocks, block_size // 16, num_kv_heads] "
+                         "and share one layout")
+    # an axis of length 1 is never stepped along: any positive stride will do
+    s = [st if n > 1 else max(st, 1) for n, st in zip(k_scales.shape, k_scales.stride())]
+    return Q8Cache(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
+                   cache_layout(k_cache), formats[k_cache.dtype], 0, *s)
+
+
+def norm_rope_append_q8(q, k, v, positions, slot_mapping, gamma_q, gamma_k, theta, eps,
+                        k_cache, v_cache, k_scales, v_scales, *, q_out=None, rope_table=None,
+                        table_positions=0, status_flags=None, stream=None):
+    """norm_rope_append into an 8-bit cache (see q8_cache); q [T, Hq, D] is written to
+    q_out (default: in place).  rope_table as for norm_rope_append_cached."""
+    T, Hq, D = q.shape
+    q_out = q if q_out is None else q_out
+    if q_out.shape != q.shape or q_out.dtype != q.dtype:
+        raise ValueError("q_out must have q's shape and type")
+    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
+    check(pkvqk_norm_rope_append_q8(
+        _ptr(q), q.stride(0), q.stride(1),
+        _ptr(q_out), q_out.stride(0), q_out.stride(1),
+        _ptr(k), k.stride(0), k.stride(1),
+        _ptr(v), v.stride(0), v.stride(1),
+        _ptr(positions), _ptr(slot_mapping), _ptr(gamma_q), _ptr(gamma_k),
+        float(theta), float(eps), T, Hq, ctypes.byref(cache),
+        _ptr(rope_table), int(table_positions), _ptr(status_flags), _stream(stream)))
+
+
+def paged_decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, out, *,
+                    q_len=1, num_splits=1, max_seq_len_hint=0, scale=0.0, lse_out=None,
+                    workspace=None, status_flags=None, stream=None):
+    """paged_decode over an 8-bit cache (see q8_cache)."""
+    Tq, Hq, D = q.shape
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    check(pkvqk_paged_decode_q8(
+        _ptr(q), q.stride(0), q.stride(1), ctypes.byref(cache),
+        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
+        Tq // q_len, q_len, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
         _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
         _ptr(status_flags), _stream(stream)))

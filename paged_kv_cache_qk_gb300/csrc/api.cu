@@ -143,6 +143,58 @@ pkvqk_status encode_cache_map(CUtensorMap* map, const void* base, const pkvqk_ca
   return PKVQK_OK;
 }
 
+// 4-D view of an 8-bit cache: dims (inner first) = (128 dims, slot, kv head,
+// block), box = (128, tile_keys slots, heads_per_cta, 1 block), 128-byte
+// swizzle: tile_keys rows of 128 B per head.
+pkvqk_status encode_q8_map(CUtensorMap* map, const void* base, const pkvqk_cache_layout& L,
+                           int heads_per_cta, int tile_keys) {
+  PKVQK_TRY(get_encoder());
+  cuuint64_t dims[4] = {128, static_cast<cuuint64_t>(L.block_size),
+                        static_cast<cuuint64_t>(L.num_kv_heads),
+                        static_cast<cuuint64_t>(L.num_blocks)};
+  cuuint64_t strides[3] = {static_cast<cuuint64_t>(L.slot_stride),
+                           static_cast<cuuint64_t>(L.head_stride),
+                           static_cast<cuuint64_t>(L.block_stride)};
+  cuuint32_t box[4] = {128, static_cast<cuuint32_t>(tile_keys),
+                       static_cast<cuuint32_t>(heads_per_cta), 1};
+  cuuint32_t estr[4] = {1, 1, 1, 1};
+  CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void*>(base), dims,
+                        strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                        CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+  if (r != CUDA_SUCCESS)
+    return fail(PKVQK_ERR_CUDA, "cuTensorMapEncodeTiled failed (CUresult %d)", static_cast<int>(r));
+  return PKVQK_OK;
+}
+
+pkvqk_status check_q8(const pkvqk_q8_cache* c) {
+  if (c == nullptr) return fail(PKVQK_ERR_INVALID_ARG, "cache is NULL");
+  PKVQK_TRY(check_layout(&c->layout));
+  const pkvqk_cache_layout& L = c->layout;
+  if (c->format != PKVQK_Q8_E4M3 && c->format != PKVQK_Q8_INT8)
+    return fail(PKVQK_ERR_UNSUPPORTED, "format %d (PKVQK_Q8_E4M3 or PKVQK_Q8_INT8)", c->format);
+  if (L.block_stride % 16 || L.slot_stride % 16 || L.head_stride % 16)
+    return fail(PKVQK_ERR_INVALID_ARG, "strides of an 8-bit cache must be multiples of 16 bytes");
+  const int64_t st[3] = {c->scale_block_stride, c->scale_group_stride, c->scale_head_stride};
+  for (int i = 0; i < 3; ++i)
+    if (st[i] <= 0 || st[i] >= (int64_t(1) << 38))
+      return fail(PKVQK_ERR_INVALID_ARG, "scale strides must be positive");
+  return PKVQK_OK;
+}
+
+// Pointers of an 8-bit cache beyond k and v, which every call checks by name.
+pkvqk_status check_q8_scales(const pkvqk_q8_cache& c) {
+  PKVQK_TRY(check_device_ptr(c.k_scales, "k_scales"));
+  PKVQK_TRY(check_device_ptr(c.v_scales, "v_scales"));
+  if ((reinterpret_cast<uintptr_t>(c.k_scales) & 3u) || (reinterpret_cast<uintptr_t>(c.v_scales) & 3u))
+    return fail(PKVQK_ERR_INVALID_ARG, "scales not 4-byte aligned");
+  return PKVQK_OK;
+}
+
+pkvqk::ScaleView scale_view(const pkvqk_q8_cache& c) {
+  return {c.k_scales, c.v_scales, c.scale_block_stride, c.scale_group_stride, c.scale_head_stride};
+}
+
 // ---------------------------------------------------------------- SM count
 
 int sm_count_current() {
@@ -200,6 +252,7 @@ struct DecodeCall {
   int32_t* status_flags;
   cudaStream_t stream;
   bool partials_only;
+  const pkvqk_q8_cache* q8 = nullptr;          // 8-bit cache (k_cache, v_cache, layout are its)
 };
 
 pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64_t total_q);
@@ -223,6 +276,8 @@ pkvqk_status run_decode(const DecodeCall& c) {
   if (c.q_stride_t % 8 || c.q_stride_h % 8 || c.q_stride_h < 1 || c.q_stride_t < 0)
     return fail(PKVQK_ERR_INVALID_ARG, "q strides must be multiples of 8 elements");
   if (!std::isfinite(c.scale)) return fail(PKVQK_ERR_INVALID_ARG, "scale is not finite");
+  if (rows > 16 && c.q8 != nullptr)
+    return fail(PKVQK_ERR_UNSUPPORTED, "%d rows per kv head over an 8-bit cache (max 16)", rows);
   if (rows > 16) {
     // More query rows per kv head than the decode kernel's register tiles
     // hold: the tensor-core multi-query kernel computes the same rows, with
@@ -246,7 +301,8 @@ pkvqk_status run_decode(const DecodeCall& c) {
                        ? c.max_seq_len_hint
                        : static_cast<int>(std::min<int64_t>(cap_tokens, INT32_MAX));
   const int S = c.num_splits;                   // 0: balanced schedule
-  const pkvqk::DecodePlan plan = pkvqk::plan_decode(L.num_kv_heads, rows);
+  const pkvqk::DecodePlan plan = c.q8 != nullptr ? pkvqk::plan_decode_q8(L.num_kv_heads, rows)
+                                                 : pkvqk::plan_decode(L.num_kv_heads, rows);
   const int64_t nrows = static_cast<int64_t>(c.batch) * c.q_len * c.num_q_heads;
   // balanced schedule: 0.84 CTAs per SM, the share the split heuristic also
   // keeps in flight (measured on GB300 against one CTA per SM: decode call
@@ -283,10 +339,15 @@ pkvqk_status run_decode(const DecodeCall& c) {
     if (!aligned16(c.workspace)) return fail(PKVQK_ERR_INVALID_ARG, "workspace not 16-byte aligned");
   }
   if (c.status_flags != nullptr) PKVQK_TRY(check_device_ptr(c.status_flags, "status_flags"));
+  if (c.q8 != nullptr) PKVQK_TRY(check_q8_scales(*c.q8));
 
   CUtensorMap kmap, vmap;
-  PKVQK_TRY(encode_cache_map(&kmap, c.k_cache, L, plan.heads_per_cta, plan.tile_keys));
-  PKVQK_TRY(encode_cache_map(&vmap, c.v_cache, L, plan.heads_per_cta, plan.tile_keys));
+  const auto encode = [&](CUtensorMap* m, const void* base) {
+    return c.q8 != nullptr ? encode_q8_map(m, base, L, plan.heads_per_cta, plan.tile_keys)
+                           : encode_cache_map(m, base, L, plan.heads_per_cta, plan.tile_keys);
+  };
+  PKVQK_TRY(encode(&kmap, c.k_cache));
+  PKVQK_TRY(encode(&vmap, c.v_cache));
 
   const int hint_pages = (hint + L.block_size - 1) / L.block_size;
   pkvqk::DecodeArgs a;
@@ -325,7 +386,11 @@ pkvqk_status run_decode(const DecodeCall& c) {
   }
   a.status_flags = c.status_flags;
 
-  cudaError_t e = pkvqk::launch_paged_decode(plan, kmap, vmap, a, grid_ctas, c.stream);
+  cudaError_t e =
+      c.q8 != nullptr
+          ? pkvqk::launch_paged_decode_q8(plan, kmap, vmap, a, scale_view(*c.q8), c.q8->format,
+                                          grid_ctas, c.stream)
+          : pkvqk::launch_paged_decode(plan, kmap, vmap, a, grid_ctas, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   if (S == 0) {
     e = pkvqk::launch_balanced_combine(a, plan.heads_per_cta, c.stream);
@@ -554,6 +619,88 @@ pkvqk_status run_append(void* q, int64_t q_stride_t, int64_t q_stride_h, const v
   return ok();
 }
 
+pkvqk_status run_append_q8(const void* q, int64_t q_stride_t, int64_t q_stride_h, void* q_out,
+                           int64_t q_out_stride_t, int64_t q_out_stride_h, const void* k,
+                           int64_t k_stride_t, int64_t k_stride_h, const void* v,
+                           int64_t v_stride_t, int64_t v_stride_h, const int64_t* positions,
+                           const int64_t* slot_mapping, const void* gamma_q, const void* gamma_k,
+                           float theta, float eps, int32_t num_tokens, int32_t num_q_heads,
+                           const pkvqk_q8_cache* cache, const void* rope_table,
+                           int32_t table_positions, int32_t* status_flags, cudaStream_t stream) {
+  PKVQK_TRY(check_q8(cache));
+  const pkvqk_cache_layout& L = cache->layout;
+  if (table_positions < 0 || table_positions > kRopeTableMaxPositions)
+    return fail(PKVQK_ERR_INVALID_ARG, "table_positions %d (0..%d)", table_positions,
+                kRopeTableMaxPositions);
+  if (num_tokens < 0 || num_tokens > (1 << 30))
+    return fail(PKVQK_ERR_INVALID_ARG, "num_tokens %d", num_tokens);
+  if (num_q_heads < 1 || num_q_heads + L.num_kv_heads > 4096)
+    return fail(PKVQK_ERR_INVALID_ARG, "num_q_heads %d", num_q_heads);
+  if (!(theta > 0.f) || !std::isfinite(theta)) return fail(PKVQK_ERR_INVALID_ARG, "theta must be > 0");
+  if (!(eps >= 0.f) || !std::isfinite(eps)) return fail(PKVQK_ERR_INVALID_ARG, "eps must be >= 0");
+  const int64_t st[8] = {q_stride_t, q_stride_h, q_out_stride_t, q_out_stride_h,
+                         k_stride_t, k_stride_h, v_stride_t,     v_stride_h};
+  for (int i = 0; i < 8; ++i)
+    if (st[i] < 0 || (st[i] % 8) != 0)
+      return fail(PKVQK_ERR_INVALID_ARG, "q/q_out/k/v strides must be non-negative multiples of 8");
+  if (num_tokens == 0) return ok();
+  const void* al[8] = {q, q_out, k, v, gamma_q, gamma_k, cache->k, cache->v};
+  const char* nm[8] = {"q", "q_out", "k", "v", "gamma_q", "gamma_k", "k_cache", "v_cache"};
+  for (int i = 0; i < 8; ++i) {
+    PKVQK_TRY(check_device_ptr(al[i], nm[i]));
+    if (!aligned16(al[i])) return fail(PKVQK_ERR_INVALID_ARG, "%s not 16-byte aligned", nm[i]);
+  }
+  PKVQK_TRY(check_device_ptr(positions, "positions"));
+  PKVQK_TRY(check_device_ptr(slot_mapping, "slot_mapping"));
+  PKVQK_TRY(check_q8_scales(*cache));
+  if (status_flags != nullptr) PKVQK_TRY(check_device_ptr(status_flags, "status_flags"));
+  if ((reinterpret_cast<uintptr_t>(positions) & 7u) || (reinterpret_cast<uintptr_t>(slot_mapping) & 7u))
+    return fail(PKVQK_ERR_INVALID_ARG, "positions/slot_mapping not 8-byte aligned");
+  if (table_positions > 0) {
+    PKVQK_TRY(check_device_ptr(rope_table, "rope_table"));
+    if (!aligned16(rope_table)) return fail(PKVQK_ERR_INVALID_ARG, "rope_table not 16-byte aligned");
+  }
+
+  pkvqk::AppendQ8Args a = {};
+  pkvqk::NormRopeAppendArgs& n = a.base;
+  n.q = static_cast<__nv_bfloat16*>(const_cast<void*>(q));
+  n.q_stride_t = q_stride_t;
+  n.q_stride_h = q_stride_h;
+  n.k = static_cast<const __nv_bfloat16*>(k);
+  n.k_stride_t = k_stride_t;
+  n.k_stride_h = k_stride_h;
+  n.v = static_cast<const __nv_bfloat16*>(v);
+  n.v_stride_t = v_stride_t;
+  n.v_stride_h = v_stride_h;
+  n.positions = positions;
+  n.slot_mapping = slot_mapping;
+  n.gamma_q = static_cast<const __nv_bfloat16*>(gamma_q);
+  n.gamma_k = static_cast<const __nv_bfloat16*>(gamma_k);
+  n.eps = eps;
+  rope_constants(theta, n.inv_freq, n.sincos_tab);
+  n.num_tokens = num_tokens;
+  n.num_q_heads = num_q_heads;
+  n.num_kv_heads = L.num_kv_heads;
+  n.num_blocks = L.num_blocks;
+  n.block_size = L.block_size;
+  n.block_stride = L.block_stride;
+  n.slot_stride = L.slot_stride;
+  n.head_stride = L.head_stride;
+  n.status_flags = status_flags;
+  n.rope_table = table_positions > 0 ? static_cast<const float4*>(rope_table) : nullptr;
+  n.table_positions = table_positions;
+  a.q_out = static_cast<__nv_bfloat16*>(q_out);
+  a.q_out_stride_t = q_out_stride_t;
+  a.q_out_stride_h = q_out_stride_h;
+  a.k_codes = static_cast<uint8_t*>(cache->k);
+  a.v_codes = static_cast<uint8_t*>(cache->v);
+  a.scales = scale_view(*cache);
+  a.format = cache->format;
+  const cudaError_t e = pkvqk::launch_norm_rope_append_q8(a, stream);
+  if (e != cudaSuccess) return cuda_fail(e, "norm_rope_append_q8 launch");
+  return ok();
+}
+
 }  // namespace
 
 pkvqk_status pkvqk_norm_rope_append(void* q, int64_t q_stride_t, int64_t q_stride_h,
@@ -584,6 +731,19 @@ pkvqk_status pkvqk_norm_rope_append_cached(
                     v_stride_h, positions, slot_mapping, gamma_q, gamma_k, theta, eps, num_tokens,
                     num_q_heads, k_cache, v_cache, layout, rope_table, table_positions,
                     status_flags, stream);
+}
+
+pkvqk_status pkvqk_norm_rope_append_q8(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, void* q_out, int64_t q_out_stride_t,
+    int64_t q_out_stride_h, const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+    int64_t v_stride_t, int64_t v_stride_h, const int64_t* positions, const int64_t* slot_mapping,
+    const void* gamma_q, const void* gamma_k, float theta, float eps, int32_t num_tokens,
+    int32_t num_q_heads, const pkvqk_q8_cache* cache, const void* rope_table,
+    int32_t table_positions, int32_t* status_flags, pkvqk_stream_t stream) {
+  return run_append_q8(q, q_stride_t, q_stride_h, q_out, q_out_stride_t, q_out_stride_h, k,
+                       k_stride_t, k_stride_h, v, v_stride_t, v_stride_h, positions, slot_mapping,
+                       gamma_q, gamma_k, theta, eps, num_tokens, num_q_heads, cache, rope_table,
+                       table_positions, status_flags, reinterpret_cast<cudaStream_t>(stream));
 }
 
 size_t pkvqk_rope_table_bytes(int32_t max_positions) {
@@ -688,6 +848,23 @@ pkvqk_status pkvqk_paged_decode(const void* q, int64_t q_stride_t, int64_t q_str
                q_len,      num_q_heads, num_splits,       max_seq_len_hint, scale,
                out,        lse_out,     workspace,        workspace_bytes_, status_flags,
                reinterpret_cast<cudaStream_t>(stream), false};
+  return run_decode(c);
+}
+
+pkvqk_status pkvqk_paged_decode_q8(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                   const pkvqk_q8_cache* cache, const int32_t* block_tables,
+                                   int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                   int32_t batch, int32_t q_len, int32_t num_q_heads,
+                                   int32_t num_splits, int32_t max_seq_len_hint, float scale,
+                                   void* out, float* lse_out, void* workspace,
+                                   size_t workspace_bytes_, int32_t* status_flags,
+                                   pkvqk_stream_t stream) {
+  PKVQK_TRY(check_q8(cache));
+  DecodeCall c{q,          q_stride_t,  q_stride_h,       cache->k,   cache->v,
+               &cache->layout, block_tables, max_blocks_per_seq, seq_lens, batch,
+               q_len,      num_q_heads, num_splits,       max_seq_len_hint, scale,
+               out,        lse_out,     workspace,        workspace_bytes_, status_flags,
+               reinterpret_cast<cudaStream_t>(stream), false, cache};
   return run_decode(c);
 }
 

@@ -44,6 +44,33 @@ cudaError_t launch_norm_rope_append(const NormRopeAppendArgs& a, cudaStream_t st
 cudaError_t launch_rope_table_build(float4* table, int32_t positions, const double (&inv_freq)[64],
                                     const float (&sincos_tab)[51][4], cudaStream_t stream);
 
+// The quantised caches of a layer: 8-bit codes in the layout of
+// pkvqk_cache_layout (strides in bytes), one fp32 scale per group of
+// kScaleGroup consecutive slots of a page and kv head.
+constexpr int kScaleGroup = 16;
+constexpr int kFormatE4m3 = 1;
+constexpr int kFormatInt8 = 2;
+constexpr int kScaleMinExp = -64, kScaleMaxExp = 63;   // scales are 2^e in this range
+
+struct ScaleView {
+  float* k;
+  float* v;
+  int64_t block_stride, group_stride, head_stride;
+};
+
+struct AppendQ8Args {
+  NormRopeAppendArgs base;         // q is read through base.q, base.k_cache / v_cache unused
+  __nv_bfloat16* q_out;
+  int64_t q_out_stride_t, q_out_stride_h;
+  uint8_t* k_codes;
+  uint8_t* v_codes;
+  ScaleView scales;
+  int32_t format;
+  int32_t parts;                   // set by the launch: CTAs that share a window's heads
+};
+
+cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& a, cudaStream_t stream);
+
 struct DecodeArgs {
   const __nv_bfloat16* q;
   int64_t q_stride_t, q_stride_h;
@@ -81,6 +108,15 @@ DecodePlan plan_decode(int num_kv_heads, int rows);
 cudaError_t launch_paged_decode(const DecodePlan& plan, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, const DecodeArgs& a, int grid_ctas,
                                 cudaStream_t stream);
+
+// The same over an 8-bit cache (rows = q_len * group <= 16): kernel family,
+// ring geometry and launch.  The maps are 4-D views (dims, slots, kv heads,
+// blocks) of the codes with a box of tile_keys slots x heads_per_cta heads.
+DecodePlan plan_decode_q8(int num_kv_heads, int rows);
+cudaError_t launch_paged_decode_q8(const DecodePlan& plan, const CUtensorMap& kmap,
+                                   const CUtensorMap& vmap, const DecodeArgs& a,
+                                   const ScaleView& scales, int format, int grid_ctas,
+                                   cudaStream_t stream);
 
 cudaError_t launch_lse_combine(const float* ws_o, const float* ws_lse, int rows, int num_splits,
                                __nv_bfloat16* out, float* lse_out, cudaStream_t stream);

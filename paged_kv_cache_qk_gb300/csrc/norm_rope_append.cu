@@ -39,6 +39,7 @@
 #include "device_common.cuh"
 #include "kernels.h"
 #include "rope_math.cuh"
+#include "rope_rotate.cuh"
 
 namespace pkvqk {
 
@@ -66,16 +67,6 @@ struct Loaded {
   uint2 x0, x1, v0, v1;
 };
 
-// sin/cos of this lane's four frequencies 4l .. 4l+3, float-float pairs.
-struct Trig {
-  float4 ch, cl, sh, sl;
-};
-
-__device__ __forceinline__ void unpack4(const uint2& u, float* f) {
-  f[0] = bf16lo(u.x); f[1] = bf16hi(u.x);
-  f[2] = bf16lo(u.y); f[3] = bf16hi(u.y);
-}
-
 // Loads x (and for k heads the v row) of head vector h of token t.
 __device__ __forceinline__ Loaded load_vector(const NormRopeAppendArgs& a, int t, int h, int l) {
   Loaded r;
@@ -96,29 +87,6 @@ __device__ __forceinline__ Loaded load_vector(const NormRopeAppendArgs& a, int t
   return r;
 }
 
-__device__ __forceinline__ uint64_t sub2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("sub.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
-// r * (a c - b s) for c = ch + cl, s = sh + sl, two elements at once (packed
-// f32x2, each lane rounded as the scalar instruction rounds it): the products
-// a*ch and b*sh error-free (p1 = a ch rounded, its error -(p1 - a ch) from
-// one fma against -ch; q2 = b sh rounded, the error of -b sh as q2 - b sh),
-// the low parts and the error terms added last.  nch, nsh, nsl are -ch, -sh,
-// -sl (exact), so no negation is spent per element.
-__device__ __forceinline__ uint64_t rotate2(uint64_t a, uint64_t b, uint64_t ch, uint64_t nch,
-                                            uint64_t cl, uint64_t sh, uint64_t nsh, uint64_t nsl,
-                                            uint64_t r) {
-  const uint64_t p1 = mul2(a, ch);
-  const uint64_t m1 = fma2(a, nch, p1);
-  const uint64_t q2 = mul2(b, sh);
-  const uint64_t e2 = fma2(b, nsh, q2);
-  const uint64_t tail = add2(fma2(a, cl, mul2(b, nsl)), sub2(e2, m1));
-  return mul2(r, add2(sub2(p1, q2), tail));
-}
-
 // Norm + rotation + stores of one head vector; both half-warps of the warp
 // call it together (the sum-of-squares shuffles are warp-wide).
 __device__ __forceinline__ void finish_vector(const NormRopeAppendArgs& a, int t, int h, int l,
@@ -132,38 +100,8 @@ __device__ __forceinline__ void finish_vector(const NormRopeAppendArgs& a, int t
   const bool is_q = h < a.num_q_heads;
   unpack4(is_q ? gq[0] : gk[0], g0);
   unpack4(is_q ? gq[1] : gk[1], g1);
-  // x*gamma is exact in fp32; x^2 is exact, the sum rounds
-  float ss = 0.f, a0[4], a1[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    ss = fmaf(x0[j], x0[j], ss);
-    ss = fmaf(x1[j], x1[j], ss);
-    a0[j] = x0[j] * g0[j];
-    a1[j] = x1[j] * g1[j];
-  }
-#pragma unroll
-  for (int o = 8; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-  const float r = rsqrtf(fmaf(ss, 1.0f / kHeadDim, a.eps));
-
-  // rotate-half, pair (i, i + D/2) in this lane:
-  //   out_i = a_i c - a_{i+D/2} s,   out_{i+D/2} = a_{i+D/2} c + a_i s
-  const float ch[4] = {tr.ch.x, tr.ch.y, tr.ch.z, tr.ch.w};
-  const float cl[4] = {tr.cl.x, tr.cl.y, tr.cl.z, tr.cl.w};
-  const float sh[4] = {tr.sh.x, tr.sh.y, tr.sh.z, tr.sh.w};
-  const float sl[4] = {tr.sl.x, tr.sl.y, tr.sl.z, tr.sl.w};
-  const uint64_t r2 = pack2(r, r);
   float o0[4], o1[4];
-#pragma unroll
-  for (int j = 0; j < 4; j += 2) {
-    const uint64_t x0 = pack2(a0[j], a0[j + 1]), x1 = pack2(a1[j], a1[j + 1]);
-    const uint64_t c = pack2(ch[j], ch[j + 1]), nc = pack2(-ch[j], -ch[j + 1]);
-    const uint64_t c_lo = pack2(cl[j], cl[j + 1]);
-    const uint64_t s = pack2(sh[j], sh[j + 1]), ns = pack2(-sh[j], -sh[j + 1]);
-    const uint64_t s_lo = pack2(sl[j], sl[j + 1]), ns_lo = pack2(-sl[j], -sl[j + 1]);
-    // out_i = r (a_i c - a_{i+64} s);  out_{i+64} = r (a_{i+64} c - (-a_i) s)
-    unpack2(rotate2(x0, x1, c, nc, c_lo, s, ns, ns_lo, r2), o0[j], o0[j + 1]);
-    unpack2(rotate2(x1, x0, c, nc, c_lo, ns, s, s_lo, r2), o1[j], o1[j + 1]);
-  }
+  norm_rotate(x0, x1, g0, g1, a.eps, tr, o0, o1);
   const uint2 w0 = make_uint2(pack_bf16x2(o0[0], o0[1]), pack_bf16x2(o0[2], o0[3]));
   const uint2 w1 = make_uint2(pack_bf16x2(o1[0], o1[1]), pack_bf16x2(o1[2], o1[3]));
 
