@@ -357,7 +357,7 @@ PKVQK_API pkvqk_status pkvqk_paged_decode(
  * rounded to 2^-11.  Slots at or past seq_lens[b] may hold any code and scale;
  * an e4m3 NaN code of a visible V makes NaN of every row of its sequence and
  * kv head.
- * At most 16 rows per kv head (q_len*Hq/Hkv).
+ * More than 16 rows per kv head run as pkvqk_paged_prefill_q8 does.
  */
 PKVQK_API pkvqk_status pkvqk_paged_decode_q8(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,
@@ -532,6 +532,35 @@ PKVQK_API pkvqk_status pkvqk_paged_prefill_varlen(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,
     const int32_t* cu_seqlens_q, int32_t max_q_len, int64_t total_q,
     const void* k_cache, const void* v_cache, const pkvqk_cache_layout* layout,
+    const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens,
+    int32_t batch, int32_t num_q_heads,
+    int32_t num_splits, int32_t max_seq_len_hint, float scale,
+    void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+/*
+ * pkvqk_paged_prefill and pkvqk_paged_prefill_varlen over an 8-bit cache: the same
+ * definition with K_n and V_n = code * scale, the same split choice and
+ * workspace; exactness, slots past the sequence's end and NaN codes as for
+ * pkvqk_paged_decode_q8.
+ */
+PKVQK_API pkvqk_status pkvqk_paged_prefill_q8(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const pkvqk_q8_cache* cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens,
+    int32_t batch, int32_t q_len, int32_t num_q_heads,
+    int32_t num_splits, int32_t max_seq_len_hint, float scale,
+    void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+PKVQK_API pkvqk_status pkvqk_paged_prefill_varlen_q8(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const int32_t* cu_seqlens_q, int32_t max_q_len, int64_t total_q,
+    const pkvqk_q8_cache* cache,
     const int32_t* block_tables, int32_t max_blocks_per_seq,
     const int32_t* seq_lens,
     int32_t batch, int32_t num_q_heads,

@@ -164,6 +164,16 @@ _decode_q8_args = [
 ]
 pkvqk_paged_decode_q8 = _sig("pkvqk_paged_decode_q8", ctypes.c_int,
                              _decode_q8_args + [c_vp, c_vp, c_vp, c_size, c_vp, c_vp])
+pkvqk_paged_prefill_q8 = _sig("pkvqk_paged_prefill_q8", ctypes.c_int,
+                              _decode_q8_args + [c_vp, c_vp, c_vp, c_size, c_vp, c_vp])
+pkvqk_paged_prefill_varlen_q8 = _sig("pkvqk_paged_prefill_varlen_q8", ctypes.c_int, [
+    c_vp, c_i64, c_i64,                 # q, strides
+    c_vp, c_i32, c_i64,                 # cu_seqlens_q, max_q_len, total_q
+    ctypes.POINTER(Q8Cache),
+    c_vp, c_i32, c_vp,                  # block_tables, max_blocks_per_seq, seq_lens
+    c_i32, c_i32,                       # batch, num_q_heads
+    c_i32, c_i32, c_f32,                # num_splits, max_seq_len_hint, scale
+    c_vp, c_vp, c_vp, c_size, c_vp, c_vp])
 
 EXPORTED = [
     "pkvqk_last_error", "pkvqk_abi_version", "pkvqk_norm_rope_append",
@@ -172,7 +182,8 @@ EXPORTED = [
     "pkvqk_static_workspace_capacity", "pkvqk_choose_prefill_splits",
     "pkvqk_prefill_workspace_bytes", "pkvqk_paged_prefill", "pkvqk_paged_prefill_varlen",
     "pkvqk_rope_table_bytes", "pkvqk_rope_table_build", "pkvqk_norm_rope_append_cached",
-    "pkvqk_norm_rope_append_q8", "pkvqk_paged_decode_q8",
+    "pkvqk_norm_rope_append_q8", "pkvqk_paged_decode_q8", "pkvqk_paged_prefill_q8",
+    "pkvqk_paged_prefill_varlen_q8",
 ]
 
 
@@ -433,5 +444,40 @@ def paged_decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_l
         _ptr(q), q.stride(0), q.stride(1), ctypes.byref(cache),
         _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
         Tq // q_len, q_len, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
+        _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
+        _ptr(status_flags), _stream(stream)))
+
+
+def paged_prefill_q8(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, out, *,
+                     q_len, num_splits=1, max_seq_len_hint=0, scale=0.0, lse_out=None,
+                     workspace=None, status_flags=None, stream=None):
+    """paged_prefill over an 8-bit cache (see q8_cache)."""
+    Tq, Hq, D = q.shape
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    check(pkvqk_paged_prefill_q8(
+        _ptr(q), q.stride(0), q.stride(1), ctypes.byref(cache),
+        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
+        Tq // q_len, q_len, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
+        _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
+        _ptr(status_flags), _stream(stream)))
+
+
+def paged_prefill_varlen_q8(q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scales, v_scales,
+                            block_tables, seq_lens, out, *, num_splits=1, max_seq_len_hint=0,
+                            scale=0.0, lse_out=None, workspace=None, status_flags=None,
+                            stream=None):
+    """paged_prefill_varlen over an 8-bit cache (see q8_cache)."""
+    total_q, Hq, D = q.shape
+    if not out.is_contiguous():
+        raise ValueError("out must be contiguous")
+    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
+    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    check(pkvqk_paged_prefill_varlen_q8(
+        _ptr(q), q.stride(0), q.stride(1), _ptr(cu_seqlens_q), int(max_q_len), int(total_q),
+        ctypes.byref(cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
+        cu_seqlens_q.shape[0] - 1, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
         _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
         _ptr(status_flags), _stream(stream)))

@@ -276,8 +276,6 @@ pkvqk_status run_decode(const DecodeCall& c) {
   if (c.q_stride_t % 8 || c.q_stride_h % 8 || c.q_stride_h < 1 || c.q_stride_t < 0)
     return fail(PKVQK_ERR_INVALID_ARG, "q strides must be multiples of 8 elements");
   if (!std::isfinite(c.scale)) return fail(PKVQK_ERR_INVALID_ARG, "scale is not finite");
-  if (rows > 16 && c.q8 != nullptr)
-    return fail(PKVQK_ERR_UNSUPPORTED, "%d rows per kv head over an 8-bit cache (max 16)", rows);
   if (rows > 16) {
     // More query rows per kv head than the decode kernel's register tiles
     // hold: the tensor-core multi-query kernel computes the same rows, with
@@ -475,16 +473,20 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
   }
   if (c.status_flags != nullptr) PKVQK_TRY(check_device_ptr(c.status_flags, "status_flags"));
 
-  // largest power of two dividing the page size, at most 128 (the kernel's
-  // key tile): no box crosses a page
-  const int box_slots = std::min(L.block_size & -L.block_size, 128);
+  if (c.q8 != nullptr) PKVQK_TRY(check_q8_scales(*c.q8));
+
   CUtensorMap kmap, vmap;
-  PKVQK_TRY(encode_cache_map(&kmap, c.k_cache, L, 1, box_slots, 1));
-  PKVQK_TRY(encode_cache_map(&vmap, c.v_cache, L, 1, box_slots, 2));
+  if (c.q8 == nullptr) {
+    // largest power of two dividing the page size, at most 128 (the kernel's
+    // key tile): no box crosses a page
+    const int box_slots = std::min(L.block_size & -L.block_size, 128);
+    PKVQK_TRY(encode_cache_map(&kmap, c.k_cache, L, 1, box_slots, 1));
+    PKVQK_TRY(encode_cache_map(&vmap, c.v_cache, L, 1, box_slots, 2));
+  }
 
   const int hint = c.max_seq_len_hint > 0 ? c.max_seq_len_hint : static_cast<int>(cap_tokens);
   const int hint_pages = (hint + L.block_size - 1) / L.block_size;
-  pkvqk::PrefillArgs a;
+  pkvqk::PrefillArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(c.q);
   a.q_stride_t = c.q_stride_t;
   a.q_stride_h = c.q_stride_h;
@@ -511,7 +513,17 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
   a.ws_lse = S > 1 ? a.ws_o + nrows * S * 128 : nullptr;
   a.status_flags = c.status_flags;
 
-  cudaError_t e = pkvqk::launch_paged_prefill(kmap, vmap, a, c.stream);
+  if (c.q8 != nullptr) {
+    a.k_codes = static_cast<const uint8_t*>(c.k_cache);
+    a.v_codes = static_cast<const uint8_t*>(c.v_cache);
+    a.block_stride = L.block_stride;
+    a.slot_stride = L.slot_stride;
+    a.head_stride = L.head_stride;
+    a.scales = scale_view(*c.q8);
+  }
+  cudaError_t e = c.q8 != nullptr
+                      ? pkvqk::launch_paged_prefill_q8(a, c.q8->format, c.stream)
+                      : pkvqk::launch_paged_prefill(kmap, vmap, a, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged prefill launch");
   if (S > 1 && !c.partials_only) {
     e = pkvqk::launch_lse_combine(a.ws_o, a.ws_lse, static_cast<int>(nrows), S, a.out, c.lse_out,
@@ -959,6 +971,39 @@ pkvqk_status pkvqk_paged_prefill_varlen(const void* q, int64_t q_stride_t, int64
                max_q_len,  num_q_heads, num_splits,       max_seq_len_hint, scale,
                out,        lse_out,     workspace,        workspace_bytes_, status_flags,
                reinterpret_cast<cudaStream_t>(stream), false};
+  return run_prefill(c, cu_seqlens_q, total_q);
+}
+
+pkvqk_status pkvqk_paged_prefill_q8(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                    const pkvqk_q8_cache* cache, const int32_t* block_tables,
+                                    int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                    int32_t batch, int32_t q_len, int32_t num_q_heads,
+                                    int32_t num_splits, int32_t max_seq_len_hint, float scale,
+                                    void* out, float* lse_out, void* workspace,
+                                    size_t workspace_bytes_, int32_t* status_flags,
+                                    pkvqk_stream_t stream) {
+  PKVQK_TRY(check_q8(cache));
+  DecodeCall c{q,          q_stride_t,  q_stride_h,       cache->k,   cache->v,
+               &cache->layout, block_tables, max_blocks_per_seq, seq_lens, batch,
+               q_len,      num_q_heads, num_splits,       max_seq_len_hint, scale,
+               out,        lse_out,     workspace,        workspace_bytes_, status_flags,
+               reinterpret_cast<cudaStream_t>(stream), false, cache};
+  return run_prefill(c, nullptr, static_cast<int64_t>(batch) * q_len);
+}
+
+pkvqk_status pkvqk_paged_prefill_varlen_q8(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const int32_t* cu_seqlens_q,
+    int32_t max_q_len, int64_t total_q, const pkvqk_q8_cache* cache, const int32_t* block_tables,
+    int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t batch, int32_t num_q_heads,
+    int32_t num_splits, int32_t max_seq_len_hint, float scale, void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes_, int32_t* status_flags, pkvqk_stream_t stream) {
+  PKVQK_TRY(check_q8(cache));
+  if (cu_seqlens_q == nullptr) return fail(PKVQK_ERR_INVALID_ARG, "cu_seqlens_q is NULL");
+  DecodeCall c{q,          q_stride_t,  q_stride_h,       cache->k,   cache->v,
+               &cache->layout, block_tables, max_blocks_per_seq, seq_lens, batch,
+               max_q_len,  num_q_heads, num_splits,       max_seq_len_hint, scale,
+               out,        lse_out,     workspace,        workspace_bytes_, status_flags,
+               reinterpret_cast<cudaStream_t>(stream), false, cache};
   return run_prefill(c, cu_seqlens_q, total_q);
 }
 

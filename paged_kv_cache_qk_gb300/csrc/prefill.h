@@ -7,6 +7,8 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "kernels.h"
+
 namespace pkvqk {
 
 // Packed (token, q head) rows of one kv head that one CTA covers.
@@ -43,6 +45,11 @@ struct PrefillArgs {
   // descending)
   int32_t mt_major;
   int32_t group_shift;             // set by launch_paged_prefill: log2(group), or -1
+  // 8-bit caches only (the bf16 form reads its cache through kmap and vmap)
+  const uint8_t* k_codes;
+  const uint8_t* v_codes;
+  int64_t block_stride, slot_stride, head_stride;
+  ScaleView scales;
 };
 
 // Shared-memory bytes one CTA of the kernel takes (one CTA per SM).
@@ -53,5 +60,8 @@ int prefill_smem_bytes();
 // The q and out row-tile maps are built here (where the layouts allow them).
 cudaError_t launch_paged_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const PrefillArgs& a, cudaStream_t stream);
+
+// The same over an 8-bit cache of the given format.
+cudaError_t launch_paged_prefill_q8(const PrefillArgs& a, int format, cudaStream_t stream);
 
 }  // namespace pkvqk

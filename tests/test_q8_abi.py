@@ -51,15 +51,28 @@ def _decode(lib, cache, B=4, q_len=1, Hq=16, S=1, ws=0, maxp=16, qs=(2048, 128),
         S, 256, scale, FAKE, None, FAKE, ws, None, None)
 
 
+def _prefill(lib, cache, B=4, q_len=32, Hq=16, S=1, ws=0, maxp=16, qs=(2048, 128), scale=0.0):
+    return lib.pkvqk_paged_prefill_q8(
+        FAKE, *qs, None if cache is None else ctypes.byref(cache), FAKE, maxp, FAKE, B, q_len, Hq,
+        S, 256, scale, FAKE, None, FAKE, ws, None, None)
+
+
+def _varlen(lib, cache, B=4, q_len=32, Hq=16, S=1, ws=0, maxp=16, qs=(2048, 128), scale=0.0,
+            cu=FAKE, total=64):
+    return lib.pkvqk_paged_prefill_varlen_q8(
+        FAKE, *qs, cu, q_len, total, None if cache is None else ctypes.byref(cache), FAKE, maxp,
+        FAKE, B, Hq, S, 256, scale, FAKE, None, FAKE, ws, None, None)
+
+
 @pytest.mark.parametrize("bad,status,word", BAD_CACHES, ids=lambda x: str(x))
 def test_caches_are_refused(lib, bad, status, word):
-    for call in (_append, _decode):
+    for call in (_append, _decode, _prefill, _varlen):
         assert call(lib, _cache(lib, **bad)) == getattr(lib, "PKVQK_ERR_" + status)
         assert word in lib.pkvqk_last_error().decode()
 
 
 def test_null_cache(lib):
-    for call in (_append, _decode):
+    for call in (_append, _decode, _prefill, _varlen):
         assert call(lib, None) == lib.PKVQK_ERR_INVALID_ARG
 
 
@@ -80,6 +93,23 @@ def test_decode_arguments(lib):
     assert _decode(lib, c, S=4, ws=100) == lib.PKVQK_ERR_WORKSPACE_TOO_SMALL
     assert _decode(lib, c, S=0, ws=100) == lib.PKVQK_ERR_WORKSPACE_TOO_SMALL
     assert _decode(lib, c, B=0) == lib.PKVQK_OK
+
+
+@pytest.mark.parametrize("call", [_prefill, _varlen])
+def test_prefill_arguments(lib, call):
+    c = _cache(lib)
+    for kw in (dict(B=-1), dict(q_len=0), dict(q_len=16385), dict(Hq=12), dict(S=257), dict(S=0),
+               dict(maxp=0), dict(qs=(2048, 100)), dict(scale=float("inf"))):
+        assert call(lib, c, **kw) == lib.PKVQK_ERR_INVALID_ARG, kw
+    assert call(lib, c, S=4, ws=100) == lib.PKVQK_ERR_WORKSPACE_TOO_SMALL
+    assert call(lib, c, B=0) == lib.PKVQK_OK
+
+
+def test_varlen_arguments(lib):
+    c = _cache(lib)
+    assert _varlen(lib, c, cu=None) == lib.PKVQK_ERR_INVALID_ARG
+    assert _varlen(lib, c, total=-1) == lib.PKVQK_ERR_INVALID_ARG
+    assert _varlen(lib, c, total=0) == lib.PKVQK_OK
 
 
 def test_binding_refuses_mismatched_tensors(lib):
