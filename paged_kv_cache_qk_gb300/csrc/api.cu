@@ -476,10 +476,13 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
   if (c.q8 != nullptr) PKVQK_TRY(check_q8_scales(*c.q8));
 
   CUtensorMap kmap, vmap;
-  if (c.q8 == nullptr) {
-    // largest power of two dividing the page size, at most 128 (the kernel's
-    // key tile): no box crosses a page
-    const int box_slots = std::min(L.block_size & -L.block_size, 128);
+  // largest power of two dividing the page size, at most 128 (the kernel's key
+  // tile): no box crosses a page
+  const int box_slots = std::min(L.block_size & -L.block_size, 128);
+  if (c.q8 != nullptr) {
+    PKVQK_TRY(encode_q8_map(&kmap, c.k_cache, L, 1, box_slots));
+    PKVQK_TRY(encode_q8_map(&vmap, c.v_cache, L, 1, box_slots));
+  } else {
     PKVQK_TRY(encode_cache_map(&kmap, c.k_cache, L, 1, box_slots, 1));
     PKVQK_TRY(encode_cache_map(&vmap, c.v_cache, L, 1, box_slots, 2));
   }
@@ -514,15 +517,13 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
   a.status_flags = c.status_flags;
 
   if (c.q8 != nullptr) {
-    a.k_codes = static_cast<const uint8_t*>(c.k_cache);
-    a.v_codes = static_cast<const uint8_t*>(c.v_cache);
-    a.block_stride = L.block_stride;
-    a.slot_stride = L.slot_stride;
-    a.head_stride = L.head_stride;
     a.scales = scale_view(*c.q8);
+    a.groups_per_page = static_cast<uint32_t>(L.block_size / pkvqk::kScaleGroup);
+    a.groups_per_page_inv = static_cast<uint32_t>(
+        ((uint64_t(1) << 32) + a.groups_per_page - 1) / a.groups_per_page);
   }
   cudaError_t e = c.q8 != nullptr
-                      ? pkvqk::launch_paged_prefill_q8(a, c.q8->format, c.stream)
+                      ? pkvqk::launch_paged_prefill_q8(kmap, vmap, a, c.q8->format, c.stream)
                       : pkvqk::launch_paged_prefill(kmap, vmap, a, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged prefill launch");
   if (S > 1 && !c.partials_only) {

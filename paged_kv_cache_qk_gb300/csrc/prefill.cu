@@ -55,7 +55,7 @@ bool encode_rows_map(CUtensorMap* map, const void* base, long long tokens, int h
 
 }  // namespace
 
-int prefill_smem_bytes() { return kSmemBytes; }
+int prefill_smem_bytes() { return kSmemBytes<0>; }
 
 namespace {
 
@@ -64,7 +64,7 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap,
                           const PrefillArgs& args, cudaStream_t stream) {
   static std::atomic<uint64_t> smem_set{0};
   const auto kern = paged_prefill_kernel<kFormat>;
-  const cudaError_t e = set_smem_limit_once(kern, kSmemBytes, smem_set);
+  const cudaError_t e = set_smem_limit_once(kern, kSmemBytes<kFormat>, smem_set);
   if (e != cudaSuccess) return e;
   PrefillArgs a = args;
   CUtensorMap qmap, omap;
@@ -83,7 +83,7 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap,
                 ? 1 : 0;
   const long long gx = static_cast<long long>(a.m_tiles) * a.num_kv_heads * a.num_splits;
   return launch_pdl(kern, dim3(static_cast<unsigned>(gx), a.batch),
-                    dim3(kPrefillThreads<kFormat>), kSmemBytes, stream, kmap, vmap, qmap, omap, a);
+                    dim3(kThreads), kSmemBytes<kFormat>, stream, kmap, vmap, qmap, omap, a);
 }
 
 }  // namespace
@@ -93,11 +93,10 @@ cudaError_t launch_paged_prefill(const CUtensorMap& kmap, const CUtensorMap& vma
   return launch_format<0>(kmap, vmap, args, stream);
 }
 
-cudaError_t launch_paged_prefill_q8(const PrefillArgs& args, int format, cudaStream_t stream) {
-  CUtensorMap none;
-  std::memset(&none, 0, sizeof(none));
-  return format == kFormatE4m3 ? launch_format<kFormatE4m3>(none, none, args, stream)
-                               : launch_format<kFormatInt8>(none, none, args, stream);
+cudaError_t launch_paged_prefill_q8(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                    const PrefillArgs& args, int format, cudaStream_t stream) {
+  return format == kFormatE4m3 ? launch_format<kFormatE4m3>(kmap, vmap, args, stream)
+                               : launch_format<kFormatInt8>(kmap, vmap, args, stream);
 }
 
 }  // namespace pkvqk

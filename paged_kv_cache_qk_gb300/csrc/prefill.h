@@ -45,11 +45,10 @@ struct PrefillArgs {
   // descending)
   int32_t mt_major;
   int32_t group_shift;             // set by launch_paged_prefill: log2(group), or -1
-  // 8-bit caches only (the bf16 form reads its cache through kmap and vmap)
-  const uint8_t* k_codes;
-  const uint8_t* v_codes;
-  int64_t block_stride, slot_stride, head_stride;
+  // 8-bit caches only
   ScaleView scales;
+  uint32_t groups_per_page;        // block_size / 16, 1 .. 16, and
+  uint32_t groups_per_page_inv;    // ceil(2^32 / it): exact quotients up to 2^28 groups
 };
 
 // Shared-memory bytes one CTA of the kernel takes (one CTA per SM).
@@ -61,7 +60,9 @@ int prefill_smem_bytes();
 cudaError_t launch_paged_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const PrefillArgs& a, cudaStream_t stream);
 
-// The same over an 8-bit cache of the given format.
-cudaError_t launch_paged_prefill_q8(const PrefillArgs& a, int format, cudaStream_t stream);
+// The same over an 8-bit cache of the given format; 4-D maps of its codes with a
+// box of (128 dims, b slots, 1 head, 1 block), b as above.
+cudaError_t launch_paged_prefill_q8(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                    const PrefillArgs& a, int format, cudaStream_t stream);
 
 }  // namespace pkvqk

@@ -50,9 +50,9 @@
 // sees S_x(i+1).
 //
 // Over an 8-bit cache (kFormat != 0) the operands are f16 instead of bf16: codes
-// are exact in it, three converter warps (16, 18, 19) fill the K and V stages
-// from global memory in place of the producer, the softmax warps rewrite Q as
-// f16 first, and scales enter at the softmax (half_tile).
+// are exact in it, the producer warp brings codes and scales, the softmax warps
+// convert the codes between their tiles, Q is brought in as f16 before the
+// roles begin, and scales enter at the softmax (half_tile).
 //
 // Shared memory (1024-byte aligned, 128-byte swizzle everywhere, the layout
 // the MMA descriptors describe):
@@ -91,11 +91,7 @@ constexpr int kDataBytes = kOffV + kStages * kTile;
 constexpr int kSoftmaxWarps = 16;             // 8 per row tile, two per lane quadrant
 constexpr int kProducerWarp = kSoftmaxWarps;
 constexpr int kMmaWarp = kSoftmaxWarps + 1;
-// kFormat 0 (bf16 cache): warps 16 and 17 only.  8-bit formats: warps 16, 18 and
-// 19 convert codes into the f16 stages, which the bf16 form fills by TMA.
-constexpr int kConverterWarps = 3;
-template <int kFormat>
-constexpr int kPrefillThreads = (kSoftmaxWarps + (kFormat == 0 ? 2 : 1 + kConverterWarps)) * 32;
+constexpr int kThreads = (kSoftmaxWarps + 2) * 32;
 constexpr uint32_t kTmemCols = 512;
 constexpr uint32_t kColS = 0;                  // + x * kN
 constexpr uint32_t kColO = 256;                // + x * kN
@@ -118,8 +114,9 @@ struct Bars {
   uint64_t xch[2][4];                            // warp pair (tile, lane quadrant) swaps
   uint64_t q_full[2];                            // Q tile x landed (TMA)
   uint64_t o_staged[2];                          // tile x's output rows staged for TMA
-  uint64_t q_ready[2];                           // 8-bit: Q tile x rewritten as f16
   uint64_t scales_full[kScaleSlots];             // 8-bit: a tile's scales are in shared memory
+  uint64_t raw_k_full, raw_k_empty;              // 8-bit: K codes landed / read
+  uint64_t raw_v_full[kStages];                  // 8-bit: V codes landed
   uint32_t tmem_base;
   int32_t abort;
 };
@@ -130,7 +127,12 @@ constexpr int kSlotBytes = 2 * 2 * 2 * kM * 4;
 // 8-bit: [slot][group] (scale of K, log2 of the scale of V, its inverse, unused)
 constexpr int kOffScales = kOffSlots + kSlotBytes;
 constexpr int kScaleBytes = kScaleSlots * kGroupsPerTile * 16;
-constexpr int kSmemBytes = kOffScales + kScaleBytes + 1024;   // + alignment slack
+constexpr int kOffRowScale = kOffScales + kScaleBytes;        // 8-bit: [row] of both Q tiles
+constexpr int kOffRaw = (kOffRowScale + 2 * kM * 4 + 1023) / 1024 * 1024;   // 8-bit: K codes
+constexpr int kRawBytes = kN * kHeadDim;
+template <int kFormat>
+constexpr int kSmemBytes =
+    (kFormat == 0 ? kOffScales : kOffRaw + kRawBytes) + 1024;   // + alignment slack
 
 // x / group for x >= 0: a shift where the group is a power of two (the
 // usual case), else the division.
@@ -365,118 +367,227 @@ __device__ void drain_copies(Bars* bars, int issued) {
   }
 }
 
-// ------------------------------------------------- converters (8-bit caches)
+// ------------------------------------------------------- 8-bit caches
 //
-// Three warps turn codes into the f16 operand stages: both K and V as two
-// swizzled halves of 64 dims, [128 keys][64 f16].  The 16-slot groups of a key
-// tile are dealt round robin (K and V offset against each other, so that each
-// warp has five or six of the sixteen); a warp loads all its groups of one
-// tensor (16 bytes a lane, 8 rows x 64 bytes an instruction: two rows of four
-// chunks per quarter-warp land in different banks of the swizzled stage), then
-// waits for the stage to be free, converts and stores.  Loads therefore run
-// ahead of the MMAs by the wait.  Keys that no row of the CTA sees, and pages
-// outside the cache, become zeros: what their slots hold never reaches an MMA.
-// The first warp also writes the tile's scales.
+// Codes come in by TMA, K's into a staging tile, V's into the first half of their
+// stage, and the softmax warps turn them into the f16 operands while they would
+// wait for the tensor core: tile A's eight warps convert K(i + 2) after P_A(i),
+// tile B's convert V(i + 1) after P_B(i) (or do nothing else, where there is no
+// tile B), one 16-slot group a warp: four reads of 16 bytes a lane, eight stores.
+// A group of V becomes f16 in place: its codes lie where its first half of dims
+// goes, so a warp only overwrites what it has read.
+// Lane group lane / 4 reads row order[lane / 4] of 8 rows so that the two rows of
+// a quarter-warp differ in bits 0 and 2: the reads (four adjacent chunks a row)
+// and the stores (every other chunk) are then both free of bank conflicts under
+// the 128-byte swizzle.
+//
+// Measured on 19 x 512 tokens after 16384 (the bf16 kernel: 874 us), warps of
+// their own for the conversion: three loading from global memory 1926-2463 us,
+// four or seven in a launch of 24 warps at 80 registers 1694-1743 us (the softmax
+// then spills), three converting out of TMA slots 1703 us: a lone warp beside
+// four softmax warps issues an instruction every ~5 cycles, and conversion, waits
+// and hand-over are ~5000 of them a key tile.
+
+// This warp's 16 keys (group g of the tile) of codes at `raw` into the stage;
+// keys from `left` on become zeros (slots that no row sees may hold NaN codes).
+// between(): after the reads, before the first store.
+template <int kFormat, typename Between>
+__device__ __forceinline__ void convert_group(const uint8_t* raw, uint8_t* stage, int g, int left,
+                                              Between&& between) {
+  const int lane = threadIdx.x & 31, c4 = lane & 3;
+  const int row = (0x63724150 >> (4 * (lane >> 2))) & 7;    // order 0 5 1 4 2 7 3 6
+  const uint8_t* from = raw + g * kScaleGroup * 128;
+  uint4 v[4];
+#pragma unroll
+  for (int u = 0; u < 4; ++u)                  // rows 8 (u / 2) .., chunks 4 (u % 2) ..
+    v[u] = *reinterpret_cast<const uint4*>(from + (u >> 1) * 1024 + swz128(row, 4 * (u & 1) + c4));
+  if (left < kScaleGroup) {
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      if ((u >> 1) * 8 + row >= left) v[u] = make_uint4(0u, 0u, 0u, 0u);
+  }
+  __syncwarp();
+  between();
+  uint8_t* to = stage + g * kScaleGroup * 128;
+#pragma unroll
+  for (int u = 0; u < 4; ++u) {
+    uint32_t f[8];
+    codes_adjacent<kFormat>(v[u].x, f[0], f[1]);
+    codes_adjacent<kFormat>(v[u].y, f[2], f[3]);
+    codes_adjacent<kFormat>(v[u].z, f[4], f[5]);
+    codes_adjacent<kFormat>(v[u].w, f[6], f[7]);
+    uint8_t* t = to + (u >> 1) * 1024 + (u & 1) * kHalf;
+    *reinterpret_cast<uint4*>(t + swz128(row, 2 * c4)) = make_uint4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<uint4*>(t + swz128(row, 2 * c4 + 1)) = make_uint4(f[4], f[5], f[6], f[7]);
+  }
+  tc5::fence_smem_for_async();
+  __syncwarp();
+}
+
+// K (tile A's warps) and V (tile B's) of key tile i; false: a wait gave up.
 template <int kFormat>
-__device__ void convert_tiles(const PrefillArgs& a, const Work& w, uint8_t* smem, Bars* bars,
-                              int cw) {
-  const int lane = threadIdx.x & 31;
-  const int bs = a.block_size;
+__device__ __forceinline__ bool convert_k(const Work& w, uint8_t* smem, Bars* bars, int i) {
+  const int s = i & 1, g = (threadIdx.x >> 5) & 7;
+  if (i >= 2 && !warp_wait(&bars->empty_k[s], ((i >> 1) - 1) & 1)) return false;
+  if (!warp_wait(&bars->raw_k_full, i & 1)) return false;
+  convert_group<kFormat>(smem + kOffRaw, smem + kOffK + s * kTile, g,
+                         w.key_end - (w.k0 + i * kN + g * kScaleGroup), [&] {
+                           if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->raw_k_empty);
+                         });
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->full_k[s]);
+  return true;
+}
+
+template <int kFormat>
+__device__ __forceinline__ bool convert_v(const Work& w, uint8_t* smem, Bars* bars, int i) {
+  const int s = i & 1, g = (threadIdx.x >> 5) & 7;
+  uint8_t* stage = smem + kOffV + s * kTile;
+  if (!warp_wait(&bars->raw_v_full[s], (i >> 1) & 1)) return false;
+  convert_group<kFormat>(stage, stage, g, w.key_end - (w.k0 + i * kN + g * kScaleGroup), [] {});
+  if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->full_v[s]);
+  return true;
+}
+
+template <int kFormat>
+__device__ __forceinline__ void convert_all_v(const PrefillArgs& a, const Work& w, uint8_t* smem,
+                                              Bars* bars) {
+  for (int i = 0; i < w.ntiles; ++i)
+    if (!convert_v<kFormat>(w, smem, bars, i)) {
+      bars->abort = 1;
+      report(a.status_flags, kFlagTimeout);
+      return;
+    }
+}
+
+// Page of the group that holds key `key` (a multiple of 16): page, slot in it.
+__device__ __forceinline__ int group_page(const PrefillArgs& a, int key, int* slot) {
+  const uint32_t gi = static_cast<uint32_t>(key) / kScaleGroup;
+  const uint32_t page = a.groups_per_page == 1 ? gi : __umulhi(gi, a.groups_per_page_inv);
+  *slot = static_cast<int>(gi - page * a.groups_per_page) * kScaleGroup;
+  return static_cast<int>(page);
+}
+
+// 4-D tiled TMA load without an L2 hint (see tma_load_5d_keep).
+__device__ __forceinline__ void tma_load_4d_keep(void* dst, const CUtensorMap* map, uint64_t* bar,
+                                                 int c1, int c2, int c3) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+      " [%0], [%1, {%2, %3, %4, %5}], [%6];" ::"r"(smem_addr(dst)),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(0), "r"(c1), "r"(c2), "r"(c3),
+      "r"(smem_addr(bar))
+      : "memory");
+}
+
+// The producer warp over an 8-bit cache: codes and scales of every key tile, lane
+// l the tile's group l % 8 (block ids read one tile ahead).
+__device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMap* kmap,
+                           const CUtensorMap* vmap, uint8_t* smem, Bars* bars) {
+  const int lane = threadIdx.x & 31, gl = lane & (kGroupsPerTile - 1);
+  const int tb = 1 << box_shift(a.block_size);
+  const bool issues = lane < kGroupsPerTile && (lane * kScaleGroup) % tb == 0;   // one box each
   const int32_t* bt = a.block_tables + static_cast<long long>(w.b) * a.max_blocks_per_seq;
-  const int gl = lane & (kGroupsPerTile - 1);   // the group whose page this lane looks up
-  auto group_key = [&](int i) { return w.k0 + i * kN + gl * kScaleGroup; };
-  auto page_id = [&](int i) {
-    const int key = group_key(i);
-    return key < w.key_end ? __ldg(bt + key / bs) : -1;
-  };
   float4* scales = reinterpret_cast<float4*>(smem + kOffScales);
-  int id_next = w.ntiles > 0 ? page_id(0) : -1;
+  auto block_id = [&](int i, int* slot) {
+    const int key = w.k0 + i * kN + gl * kScaleGroup;
+    *slot = 0;
+    return i < w.ntiles && key < w.key_end ? __ldg(bt + group_page(a, key, slot)) : -1;
+  };
+  int slot, k_sent = 0, v_sent = 0;
+  int id = block_id(0, &slot);
+  bool ok = true;
   for (int i = 0; i < w.ntiles; ++i) {
     const int s = i & 1;
-    const uint32_t rel = ((i >> 1) - 1) & 1;         // release of tile i - 2
-    const int key = group_key(i);
-    const int blk = id_next;
-    const bool seen = key < w.key_end;
-    const bool bad = seen && (blk < 0 || static_cast<long long>(blk) >= a.num_blocks);
-    if (bad && cw == 0) report(a.status_flags, kFlagBadBlock);
-    if (i + 1 < w.ntiles) id_next = page_id(i + 1);
-    const int slot = key - (key / bs) * bs;
-    // code offset of the group's first row, < 0: zeros
-    const long long off = seen && !bad ? blk * a.block_stride + slot * a.slot_stride +
-                                             w.g * a.head_stride
-                                       : -1ll;
+    const bool good = id >= 0 && static_cast<long long>(id) < a.num_blocks;
+    if (!good && w.k0 + i * kN + gl * kScaleGroup < w.key_end)
+      report(a.status_flags, kFlagBadBlock);
+    const int c3 = good ? id : static_cast<int>(a.num_blocks);   // past the extent: zeros
     float ks = 1.f, vs = 1.f;
-    if (cw == 0 && off >= 0) {
-      const long long so = blk * a.scales.block_stride +
+    if (good) {
+      const long long so = id * a.scales.block_stride +
                            (slot / kScaleGroup) * a.scales.group_stride +
                            w.g * a.scales.head_stride;
-      ks = usable_scale(__ldg(a.scales.k + so));
-      vs = usable_scale(__ldg(a.scales.v + so));
+      ks = __ldg(a.scales.k + so);
+      vs = __ldg(a.scales.v + so);
     }
-#pragma unroll 1
-    for (int kv = 0; kv < 2; ++kv) {
-      const uint8_t* codes = kv == 0 ? a.k_codes : a.v_codes;
-      const int first = kv == 0 ? cw : (cw + 1) % kConverterWarps;
-      constexpr int kMost = (kGroupsPerTile + kConverterWarps - 1) / kConverterWarps;
-      uint4 v[kMost][4];
+    // K(i - 1) has been read (and with it, the softmax of tile i - 4 is over: tile
+    // A's warps convert K(i - 1) after their P(i - 3) and after S_B(i - 3))
+    ok = i == 0 || warp_wait(&bars->raw_k_empty, (i - 1) & 1);
+    if (!ok) break;
+    if (lane == 0) mbar_arrive_expect_tx(&bars->raw_k_full, kRawBytes);
+    __syncwarp();
+    if (issues)
+      tma_load_4d_keep(smem + kOffRaw + lane * kScaleGroup * kHeadDim, kmap, &bars->raw_k_full,
+                       slot, w.g, c3);
+    k_sent = i + 1;
+    ok = i < 2 || warp_wait(&bars->empty_v[s], ((i >> 1) - 1) & 1);   // PV(i - 2) is over
+    if (!ok) break;
+    if (lane == 0) mbar_arrive_expect_tx(&bars->raw_v_full[s], kRawBytes);
+    __syncwarp();
+    if (issues)
+      tma_load_4d_keep(smem + kOffV + s * kTile + lane * kScaleGroup * kHeadDim, vmap,
+                       &bars->raw_v_full[s], slot, w.g, c3);
+    v_sent = i + 1;
+    id = block_id(i + 1, &slot);
+    ks = usable_scale(ks);
+    vs = usable_scale(vs);
+    if (lane < kGroupsPerTile)
+      scales[(i & (kScaleSlots - 1)) * kGroupsPerTile + lane] =
+          make_float4(ks, log2f(vs), __frcp_rn(vs), 0.f);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->scales_full[i & (kScaleSlots - 1)]);
+  }
+  if (!ok && lane == 0) {
+    bars->abort = 1;
+    report(a.status_flags, kFlagTimeout);
+    // the copies in flight land before the CTA leaves
+    if (k_sent > 0) mbar_wait(&bars->raw_k_full, (k_sent - 1) & 1);
+    for (int i = v_sent < 2 ? 0 : v_sent - 2; i < v_sent; ++i)
+      mbar_wait(&bars->raw_v_full[i & 1], (i >> 1) & 1);
+  }
+  __syncwarp();
+}
+
+// Q rows as f16 in both tiles' shared memory, before the warps take their roles:
+// thread i brings 64 dims (half i / 256) of row i % 256, scaled by the power of
+// two of its row's largest magnitude (so it reads the other half too); the
+// inverse goes to the row's slot.
+__device__ __forceinline__ void q_rows_to_f16(const PrefillArgs& a, const Work& w,
+                                              uint8_t* smem) {
+  const int row = threadIdx.x % (2 * kM), dh = threadIdx.x / (2 * kM);
+  const int rg = w.mt * 2 * kM + row;
+  const int t = div_group(a, rg);
+  const bool live = rg < w.rows && w.q0 + t >= 0 && w.q0 + t < a.total_q;
+  const uint4* src = reinterpret_cast<const uint4*>(
+      a.q + (live ? w.q0 + t : 0) * a.q_stride_t +
+      static_cast<long long>(w.g * a.group + (live ? rg - t * a.group : 0)) * a.q_stride_h);
+  uint4 v[8];
+  float amax = 0.f;
 #pragma unroll
-      for (int j = 0; j < kMost; ++j) {
-        const int grp = first + j * kConverterWarps;
-        const long long o = __shfl_sync(0xffffffffu, off, grp & (kGroupsPerTile - 1));
+  for (int h = 0; h < 2; ++h) {                // the other half first
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          const int r = (u >> 1) * 8 + (lane >> 2);
-          const bool live = grp < kGroupsPerTile && o >= 0 &&
-                            w.k0 + i * kN + grp * kScaleGroup + r < w.key_end;
-          v[j][u] = make_uint4(0u, 0u, 0u, 0u);
-          if (live)
-            v[j][u] = __ldg(reinterpret_cast<const uint4*>(
-                codes + o + r * a.slot_stride + (u & 1) * 64 + (lane & 3) * 16));
-        }
-      }
-      bool ok = true;
-      if (i >= 2) ok = warp_wait(kv == 0 ? &bars->empty_k[s] : &bars->empty_v[s], rel);
-      if (!ok) {
-        if (lane == 0) {
-          bars->abort = 1;
-          report(a.status_flags, kFlagTimeout);
-        }
-        return;
-      }
-      if (kv == 0 && cw == 0) {
-        // slot i % 4 was last read for tile i - 4: S(i - 2), whose end the wait
-        // above saw, was issued after the softmax of tile i - 3
-        if (lane < kGroupsPerTile)
-          scales[(i & (kScaleSlots - 1)) * kGroupsPerTile + lane] =
-              make_float4(ks, log2f(vs), __frcp_rn(vs), 0.f);
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&bars->scales_full[i & (kScaleSlots - 1)]);
-      }
-      uint8_t* tile = smem + (kv == 0 ? kOffK : kOffV) + s * kTile;
+    for (int c = 0; c < 8; ++c)
+      v[c] = live ? __ldg(src + (dh ^ h ^ 1) * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
-      for (int j = 0; j < kMost; ++j) {
-        const int grp = first + j * kConverterWarps;
-        if (grp >= kGroupsPerTile) break;
+    for (int c = 0; c < 8; ++c) {
+      float f[8];
+      unpack8(v[c], f);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
-          uint32_t f[8];
-          codes_adjacent<kFormat>(v[j][u].x, f[0], f[1]);
-          codes_adjacent<kFormat>(v[j][u].y, f[2], f[3]);
-          codes_adjacent<kFormat>(v[j][u].z, f[4], f[5]);
-          codes_adjacent<kFormat>(v[j][u].w, f[6], f[7]);
-          const int r = grp * kScaleGroup + (u >> 1) * 8 + (lane >> 2);
-          uint8_t* half = tile + (u & 1) * kHalf;
-          *reinterpret_cast<uint4*>(half + swz128(r, (lane & 3) * 2)) =
-              make_uint4(f[0], f[1], f[2], f[3]);
-          *reinterpret_cast<uint4*>(half + swz128(r, (lane & 3) * 2 + 1)) =
-              make_uint4(f[4], f[5], f[6], f[7]);
-        }
-      }
-      tc5::fence_smem_for_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(kv == 0 ? &bars->full_k[s] : &bars->full_v[s]);
+      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
     }
   }
+  float inverse;
+  const float up = q_row_scale(amax, inverse);
+  uint8_t* dst = smem + kOffQ + (row / kM) * kTile + dh * kHalf;
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    float f[8];
+    unpack8(v[c], f);
+    *reinterpret_cast<uint4*>(dst + swz128(row % kM, c)) =
+        make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
+                   pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
+  }
+  if (dh == 0) reinterpret_cast<float*>(smem + kOffRowScale)[row] = inverse;
+  tc5::fence_smem_for_async();
 }
 
 // ------------------------------------------------------------ MMA issue
@@ -531,11 +642,9 @@ __device__ void issue_mmas(const PrefillArgs& a, const Work& w, uint8_t* smem, B
     if (x == last) tc5::commit(&bars->empty_v[s]);
   };
   bool ok = true;
-  // Q tile A by TMA (issued at set-up), tile B after K(0); 8-bit: rewritten as f16
-  // by the softmax warps
+  // Q tile A by TMA (issued at set-up), tile B after K(0); 8-bit: in place already
   const auto wait_q = [&](int x) {
-    if (kFormat != 0) return mbar_wait(&bars->q_ready[x], 0);
-    return !a.q_tma || mbar_wait(&bars->q_full[x], 0);
+    return kFormat != 0 || !a.q_tma || mbar_wait(&bars->q_full[x], 0);
   };
   if (n > 0) ok = wait_q(0);
   if (ok && n > 0) ok = mbar_wait(&bars->full_k[0], 0);
@@ -871,55 +980,6 @@ __device__ __forceinline__ void write_rows(const PrefillArgs& a, const Work& w, 
   }
 }
 
-// 8-bit caches: this thread's half (64 dims) of its Q row becomes f16 in place,
-// scaled by the row's power of two (both halves swap their largest magnitude);
-// returns the inverse of that power.
-__device__ __forceinline__ float q_half_row_to_f16(const PrefillArgs& a, const Work& w,
-                                                   uint8_t* smem, Bars* bars, int x, int half,
-                                                   int r, float* slots, uint64_t* xbar,
-                                                   uint32_t& uses, bool& ok) {
-  uint8_t* row = smem + kOffQ + x * kTile + half * kHalf;
-  uint4 v[8];
-  if (a.q_tma) {
-    ok = warp_wait(&bars->q_full[x], 0) && ok;
-#pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = *reinterpret_cast<const uint4*>(row + swz128(r, c));
-  } else {
-    const int rg = w.mt * 2 * kM + x * kM + r;
-    const int t = div_group(a, rg);
-    const bool live = rg < w.rows && w.q0 + t >= 0 && w.q0 + t < a.total_q;
-    const uint4* src = reinterpret_cast<const uint4*>(
-        a.q + (live ? w.q0 + t : 0) * a.q_stride_t +
-        static_cast<long long>(w.g * a.group + (live ? rg - t * a.group : 0)) * a.q_stride_h +
-        half * 64);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) v[c] = live ? __ldg(src + c) : make_uint4(0u, 0u, 0u, 0u);
-  }
-  float amax = 0.f;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float f[8];
-    unpack8(v[c], f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-  }
-  amax = fmaxf(amax, pair_swap(amax, slots, xbar, uses, half, r, ok));
-  float inverse;
-  const float up = q_row_scale(amax, inverse);
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float f[8];
-    unpack8(v[c], f);
-    *reinterpret_cast<uint4*>(row + swz128(r, c)) =
-        make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
-                   pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
-  }
-  tc5::fence_smem_for_async();
-  __syncwarp();
-  if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->q_ready[x]);
-  return inverse;
-}
-
 template <int kFormat>
 __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem, Bars* bars,
                              const CUtensorMap* omap, float* xslots, uint32_t tmem, int x,
@@ -939,8 +999,7 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
   uint64_t* xbar = &bars->xch[x][wq];
   uint32_t uses = 0;
   bool ok = true;
-  if (kFormat != 0 && w.ntiles > 0)
-    sl2 *= q_half_row_to_f16(a, w, smem, bars, x, half, r, slots, xbar, uses, ok);
+  if (kFormat != 0) sl2 *= reinterpret_cast<const float*>(smem + kOffRowScale)[x * kM + r];
 
   // decided once: interior tiles end at or before every row's limit (the
   // warp's smallest), and only the last tile can reach past key_end (tile A
@@ -954,6 +1013,10 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
 
   float m_ref = -INFINITY;                     // reference max (log2 units), integer once set
   float l = 0.f;                               // this half's sum of P
+  if (kFormat != 0 && n > 0) {                 // the first K tiles, the first V tile
+    ok = x == 0 ? convert_k<kFormat>(w, smem, bars, 0) : convert_v<kFormat>(w, smem, bars, 0);
+    if (x == 0 && n > 1) ok = ok && convert_k<kFormat>(w, smem, bars, 1);
+  }
   for (int i = 0; i < n && ok; ++i) {
     // 8-bit: this half's four groups of scales
     const float4* scales = nullptr;
@@ -1032,6 +1095,13 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
     tc5::fence_before_sync();
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->p_full[x]);
+    if (kFormat != 0) {
+      if (x == 0) {
+        if (i + 2 < n) ok = convert_k<kFormat>(w, smem, bars, i + 2);
+      } else if (i + 1 < n) {
+        ok = convert_v<kFormat>(w, smem, bars, i + 1);
+      }
+    }
   }
   // O_x is complete once the last PV has finished
   if (ok && w.ntiles > 0) {
@@ -1074,11 +1144,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   if (w.mt * 2 * kM >= w.rows) return;
 
   if (threadIdx.x == kProducerWarp * 32) {
-    if (kFormat == 0) {
-      prefetch_tensormap(&kmap);
-      prefetch_tensormap(&vmap);
-    }
-    constexpr int kFillers = kFormat == 0 ? 1 : kConverterWarps;
+    prefetch_tensormap(&kmap);
+    prefetch_tensormap(&vmap);
+    constexpr int kFillers = kFormat == 0 ? 1 : kSoftmaxWarps / 2;
     for (int s = 0; s < kStages; ++s) {
       mbar_init(&bars->full_k[s], kFillers);
       mbar_init(&bars->full_v[s], kFillers);
@@ -1096,15 +1164,17 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     mbar_init(&bars->q_full[1], 1);
     mbar_init(&bars->drain, 1);
     if (kFormat != 0) {
-      for (int x = 0; x < 2; ++x) mbar_init(&bars->q_ready[x], kSoftmaxWarps / 2);
       for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bars->scales_full[s], 1);
+      mbar_init(&bars->raw_k_full, 1);
+      mbar_init(&bars->raw_k_empty, kSoftmaxWarps / 2);
+      for (int s = 0; s < kStages; ++s) mbar_init(&bars->raw_v_full[s], 1);
     }
     bars->abort = 0;
     issued = 0;
     fence_barrier_init();
     // Q by TMA: one box per (row tile, 64-dim half), rows past q or
     // before it read as zeros, rows of a following sequence are masked
-    if (a.q_tma && w.ntiles > 0) {
+    if (kFormat == 0 && a.q_tma && w.ntiles > 0) {
       prefetch_tensormap(&qmap);
       // tile A now; tile B after K(0), so that S_A(0) waits for two boxes less
       mbar_arrive_expect_tx(&bars->q_full[0], kTile);
@@ -1112,18 +1182,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       for (int dh = 0; dh < 2; ++dh)
         tma_load_rows(smem + kOffQ + dh * kHalf, &qmap, &bars->q_full[0], dh * 64,
                       w.g * a.group, tok);
-      if (kFormat != 0 && w.has_b) {           // no K boxes to let through first
-        mbar_arrive_expect_tx(&bars->q_full[1], kTile);
-        const int tok_b = static_cast<int>(w.q0 + div_group(a, w.mt * 2 * kM + kM));
-        for (int dh = 0; dh < 2; ++dh)
-          tma_load_rows(smem + kOffQ + kTile + dh * kHalf, &qmap, &bars->q_full[1], dh * 64,
-                        w.g * a.group, tok_b);
-      }
     }
   }
   if (warp == kMmaWarp) tc5::tmem_alloc(&bars->tmem_base, kTmemCols);
 
-  if (kFormat == 0 && warp < kSoftmaxWarps && !a.q_tma) {
+  if (kFormat != 0) {
+    if (warp < kSoftmaxWarps && w.ntiles > 0) q_rows_to_f16(a, w, smem);
+  } else if (warp < kSoftmaxWarps && !a.q_tma) {
     // Q tiles: thread i loads 64 dims (half i / 256) of row i % 128 of tile
     // (i / 128) % 2 (row = (token, q head of the group)), one swizzled half
     const int row = threadIdx.x % (2 * kM), dh = threadIdx.x / (2 * kM);
@@ -1156,20 +1221,23 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     if (x == 0 || w.has_b)
       softmax_rows<kFormat>(a, w, smem, bars, &omap, reinterpret_cast<float*>(smem + kOffSlots),
                             tmem, x, half);
-  } else if (warp != kMmaWarp) {
-    int n = 0;
-    if constexpr (kFormat == 0)
+    else if (kFormat != 0)                     // no tile B: V is all its warps do
+      convert_all_v<kFormat>(a, w, smem, bars);
+  } else if (warp == kProducerWarp) {
+    if constexpr (kFormat == 0) {
+      int n = 0;
       produce(a, w, &kmap, &vmap, &qmap, smem, bars, &n);
-    else
-      convert_tiles<kFormat>(a, w, smem, bars, warp == kProducerWarp ? 0 : warp - kMmaWarp);
-    if (threadIdx.x == kProducerWarp * 32) {
-      issued = n;
-      // the Q copies have landed before the CTA can leave (done long ago
-      // unless the MMA thread gave up)
-      if (a.q_tma && w.ntiles > 0) {
-        mbar_wait(&bars->q_full[0], 0);
-        if (w.has_b) mbar_wait(&bars->q_full[1], 0);
+      if (threadIdx.x == kProducerWarp * 32) {
+        issued = n;
+        // the Q copies have landed before the CTA can leave (done long ago
+        // unless the MMA thread gave up)
+        if (a.q_tma && w.ntiles > 0) {
+          mbar_wait(&bars->q_full[0], 0);
+          if (w.has_b) mbar_wait(&bars->q_full[1], 0);
+        }
       }
+    } else {
+      produce_q8(a, w, &kmap, &vmap, smem, bars);
     }
   } else {
     if ((threadIdx.x & 31) == 0) issue_mmas<kFormat>(a, w, smem, bars, tmem);
