@@ -479,7 +479,9 @@ __device__ __forceinline__ void tma_load_4d_keep(void* dst, const CUtensorMap* m
 }
 
 // The producer warp over an 8-bit cache: codes and scales of every key tile, lane
-// l the tile's group l % 8 (block ids read one tile ahead).
+// l the tile's group l % 8 (block ids read one tile ahead).  K runs a tile ahead
+// of V -- K(0) V(0) K(1) K(2) V(1) K(3) V(2) .. -- so that it does not wait behind
+// V for a stage that only PV_B frees.
 __device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMap* kmap,
                            const CUtensorMap* vmap, uint8_t* smem, Bars* bars) {
   const int lane = threadIdx.x & 31, gl = lane & (kGroupsPerTile - 1);
@@ -492,11 +494,21 @@ __device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMa
     *slot = 0;
     return i < w.ntiles && key < w.key_end ? __ldg(bt + group_page(a, key, slot)) : -1;
   };
+  auto send_v = [&](int i, int slot, int c3) {
+    const int s = i & 1;
+    if (i >= 2 && !warp_wait(&bars->empty_v[s], ((i >> 1) - 1) & 1)) return false;   // PV(i - 2)
+    if (lane == 0) mbar_arrive_expect_tx(&bars->raw_v_full[s], kRawBytes);
+    __syncwarp();
+    if (issues)
+      tma_load_4d_keep(smem + kOffV + s * kTile + lane * kScaleGroup * kHeadDim, vmap,
+                       &bars->raw_v_full[s], slot, w.g, c3);
+    return true;
+  };
   int slot, k_sent = 0, v_sent = 0;
   int id = block_id(0, &slot);
+  int v_slot = 0, v_c3 = 0;                    // of tile i - 1
   bool ok = true;
   for (int i = 0; i < w.ntiles; ++i) {
-    const int s = i & 1;
     const bool good = id >= 0 && static_cast<long long>(id) < a.num_blocks;
     if (!good && w.k0 + i * kN + gl * kScaleGroup < w.key_end)
       report(a.status_flags, kFlagBadBlock);
@@ -509,8 +521,6 @@ __device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMa
       ks = __ldg(a.scales.k + so);
       vs = __ldg(a.scales.v + so);
     }
-    // K(i - 1) has been read (and with it, the softmax of tile i - 4 is over: tile
-    // A's warps convert K(i - 1) after their P(i - 3) and after S_B(i - 3))
     ok = i == 0 || warp_wait(&bars->raw_k_empty, (i - 1) & 1);
     if (!ok) break;
     if (lane == 0) mbar_arrive_expect_tx(&bars->raw_k_full, kRawBytes);
@@ -519,15 +529,11 @@ __device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMa
       tma_load_4d_keep(smem + kOffRaw + lane * kScaleGroup * kHeadDim, kmap, &bars->raw_k_full,
                        slot, w.g, c3);
     k_sent = i + 1;
-    ok = i < 2 || warp_wait(&bars->empty_v[s], ((i >> 1) - 1) & 1);   // PV(i - 2) is over
-    if (!ok) break;
-    if (lane == 0) mbar_arrive_expect_tx(&bars->raw_v_full[s], kRawBytes);
-    __syncwarp();
-    if (issues)
-      tma_load_4d_keep(smem + kOffV + s * kTile + lane * kScaleGroup * kHeadDim, vmap,
-                       &bars->raw_v_full[s], slot, w.g, c3);
-    v_sent = i + 1;
+    const int k_slot = slot;
     id = block_id(i + 1, &slot);
+    // Slot i % 4 was last read for tile i - 4.  K(i - 1) has been read: tile A's
+    // warps do so after their P(i - 3) and after S_B(i - 3), which was issued after
+    // P_B(i - 4).
     ks = usable_scale(ks);
     vs = usable_scale(vs);
     if (lane < kGroupsPerTile)
@@ -535,6 +541,18 @@ __device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMa
           make_float4(ks, log2f(vs), __frcp_rn(vs), 0.f);
     __syncwarp();
     if (lane == 0) mbar_arrive(&bars->scales_full[i & (kScaleSlots - 1)]);
+    if (i != 1) {
+      const int j = i == 0 ? 0 : i - 1;
+      ok = send_v(j, i == 0 ? k_slot : v_slot, i == 0 ? c3 : v_c3);
+      if (!ok) break;
+      v_sent = j + 1;
+    }
+    v_slot = k_slot;
+    v_c3 = c3;
+  }
+  if (ok && w.ntiles > 1) {
+    ok = send_v(w.ntiles - 1, v_slot, v_c3);
+    if (ok) v_sent = w.ntiles;
   }
   if (!ok && lane == 0) {
     bars->abort = 1;
