@@ -13,6 +13,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import struct
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(_HERE, "libpkvqk.so")
@@ -384,6 +385,63 @@ def paged_prefill_varlen(q, cu_seqlens_q, max_q_len, k_cache, v_cache, block_tab
 
 
 # ------------------------------------------------------------- 8-bit caches
+#
+# These calls are a few microseconds of kernel at decode sizes, so the host side
+# is kept short: the cache's description is packed in one go, strides are read
+# once a tensor, and the current stream is asked for by its handle.
+
+_Q8_PACK = struct.Struct("=4Qq4i3q2i3q")       # pkvqk_q8_cache, no padding
+assert _Q8_PACK.size == ctypes.sizeof(Q8Cache)
+_q8 = {}                                       # torch names, filled on first use
+
+
+def _q8_names():
+    torch = _torch()
+    _q8.update(formats={torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8},
+               bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32, i64=torch.int64,
+               raw_stream=torch._C._cuda_getCurrentRawStream)
+    return _q8
+
+
+def _fast(name, args):
+    """The entry point with the cache passed as packed bytes."""
+    f = _lib[name]
+    f.restype = ctypes.c_int
+    f.argtypes = [ctypes.c_char_p if a is ctypes.POINTER(Q8Cache) else a for a in args]
+    return f
+
+
+_append_q8 = _fast("pkvqk_norm_rope_append_q8", pkvqk_norm_rope_append_q8.argtypes)
+_paged_decode_q8 = _fast("pkvqk_paged_decode_q8", pkvqk_paged_decode_q8.argtypes)
+_paged_prefill_q8 = _fast("pkvqk_paged_prefill_q8", pkvqk_paged_prefill_q8.argtypes)
+_paged_prefill_varlen_q8 = _fast("pkvqk_paged_prefill_varlen_q8",
+                                 pkvqk_paged_prefill_varlen_q8.argtypes)
+
+
+def _pack_q8(t, k_cache, v_cache, k_scales, v_scales):
+    shape, st = k_cache.shape, k_cache.stride()
+    fmt = t["formats"].get(k_cache.dtype)
+    if fmt is None or v_cache.dtype is not k_cache.dtype:
+        raise ValueError("k_cache and v_cache must both be float8_e4m3fn or int8")
+    if v_cache.stride() != st or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must share one layout")
+    nb, bs, hkv, d = shape
+    if st[3] != 1:
+        raise ValueError("head_dim must be the contiguous axis")
+    if k_scales.dtype is not t["f32"] or v_scales.dtype is not t["f32"]:
+        raise ValueError("scales must be float32")
+    ss = k_scales.stride()
+    if k_scales.shape != (nb, bs // 16, hkv) or v_scales.shape != k_scales.shape \
+            or v_scales.stride() != ss:
+        raise ValueError("scales must be [num_blocks, block_size // 16, num_kv_heads] "
+                         "and share one layout")
+    # an axis of length 1 is never stepped along: any positive stride will do
+    return _Q8_PACK.pack(
+        k_cache.data_ptr(), v_cache.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(),
+        nb, bs, hkv, d, 0, st[0], st[1], st[2], fmt, 0,
+        ss[0] if nb > 1 else ss[0] or 1, ss[1] if bs > 16 else ss[1] or 1,
+        ss[2] if hkv > 1 else ss[2] or 1)
+
 
 def q8_cache(k_cache, v_cache, k_scales, v_scales) -> Q8Cache:
     """The C description of an 8-bit cache.
@@ -392,23 +450,49 @@ def q8_cache(k_cache, v_cache, k_scales, v_scales) -> Q8Cache:
     layout, float8_e4m3fn or int8; k_scales, v_scales: fp32 [num_blocks,
     block_size // 16, num_kv_heads] views of one layout.
     """
-    torch = _torch()
-    formats = {torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8}
-    if k_cache.dtype not in formats or v_cache.dtype != k_cache.dtype:
-        raise ValueError("k_cache and v_cache must both be float8_e4m3fn or int8")
-    if tuple(v_cache.stride()) != tuple(k_cache.stride()) or v_cache.shape != k_cache.shape:
-        raise ValueError("k_cache and v_cache must share one layout")
-    nb, bs, hkv, _ = k_cache.shape
-    if k_scales.dtype != torch.float32 or v_scales.dtype != torch.float32:
-        raise ValueError("scales must be float32")
-    if (tuple(k_scales.shape) != (nb, bs // 16, hkv) or v_scales.shape != k_scales.shape
-            or k_scales.stride() != v_scales.stride()):
-        raise ValueError("scales must be [num_blocks, block_size // 16, num_kv_heads] "
-                         "and share one layout")
-    # an axis of length 1 is never stepped along: any positive stride will do
-    s = [st if n > 1 else max(st, 1) for n, st in zip(k_scales.shape, k_scales.stride())]
-    return Q8Cache(_ptr(k_cache), _ptr(v_cache), _ptr(k_scales), _ptr(v_scales),
-                   cache_layout(k_cache), formats[k_cache.dtype], 0, *s)
+    return Q8Cache.from_buffer_copy(_pack_q8(_q8 or _q8_names(), k_cache, v_cache, k_scales,
+                                             v_scales))
+
+
+def _heads(t, x, name):
+    """(tokens, heads, token stride, head stride) of a [tokens, heads, head_dim] view."""
+    n, h, _ = x.shape
+    s0, s1, s2 = x.stride()
+    if x.dtype is not t["bf16"] or s2 != 1:
+        raise ValueError(f"{name} must be bfloat16 with head_dim the contiguous axis")
+    return n, h, s0, s1
+
+
+def _ints(x, dtype, n, name):
+    if x.dtype is not dtype or not x.is_contiguous() or x.numel() != n:
+        raise ValueError(f"{name} must be {n} contiguous {dtype} values")
+    return x.data_ptr()
+
+
+def _results(t, out, lse_out, rows, heads):
+    """Pointers of out [rows, heads, head_dim] and lse_out [rows, heads] (or None)."""
+    if out.dtype is not t["bf16"] or not out.is_contiguous() or out.numel() != rows * heads * 128:
+        raise ValueError("out must be contiguous bfloat16, one value per value of q")
+    if lse_out is None:
+        return out.data_ptr(), 0
+    if lse_out.dtype is not t["f32"] or not lse_out.is_contiguous() \
+            or lse_out.numel() != rows * heads:
+        raise ValueError("lse_out must be contiguous float32, one value per row and head")
+    return out.data_ptr(), lse_out.data_ptr()
+
+
+def _table(t, block_tables, batch):
+    if block_tables.dtype is not t["i32"] or block_tables.shape[0] != batch \
+            or not block_tables.is_contiguous():
+        raise ValueError("block_tables must be contiguous int32 [batch, max_blocks_per_seq]")
+    return block_tables.data_ptr(), block_tables.shape[1]
+
+
+def _raw_stream(t, stream, x):
+    if stream is not None:
+        return stream.cuda_stream
+    index = x.get_device()
+    return t["raw_stream"](index) if index >= 0 else 0   # a host tensor is refused below
 
 
 def norm_rope_append_q8(q, k, v, positions, slot_mapping, gamma_q, gamma_k, theta, eps,
@@ -416,53 +500,57 @@ def norm_rope_append_q8(q, k, v, positions, slot_mapping, gamma_q, gamma_k, thet
                         table_positions=0, status_flags=None, stream=None):
     """norm_rope_append into an 8-bit cache (see q8_cache); q [T, Hq, D] is written to
     q_out (default: in place).  rope_table as for norm_rope_append_cached."""
-    T, Hq, D = q.shape
+    t = _q8 or _q8_names()
     q_out = q if q_out is None else q_out
-    if q_out.shape != q.shape or q_out.dtype != q.dtype:
-        raise ValueError("q_out must have q's shape and type")
-    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
-    check(pkvqk_norm_rope_append_q8(
-        _ptr(q), q.stride(0), q.stride(1),
-        _ptr(q_out), q_out.stride(0), q_out.stride(1),
-        _ptr(k), k.stride(0), k.stride(1),
-        _ptr(v), v.stride(0), v.stride(1),
-        _ptr(positions), _ptr(slot_mapping), _ptr(gamma_q), _ptr(gamma_k),
-        float(theta), float(eps), T, Hq, ctypes.byref(cache),
-        _ptr(rope_table), int(table_positions), _ptr(status_flags), _stream(stream)))
+    T, Hq, qs, qh = _heads(t, q, "q")
+    To, Ho, os_, oh = _heads(t, q_out, "q_out")
+    Tk, Hk, ks, kh = _heads(t, k, "k")
+    Tv, Hv, vs, vh = _heads(t, v, "v")
+    if (To, Ho) != (T, Hq) or Tk != T or Tv != T or Hk != Hv or Hk != k_cache.shape[2]:
+        raise ValueError("q, q_out, k and v must agree in tokens, and k, v and the cache in heads")
+    if gamma_q.dtype is not t["bf16"] or gamma_k.dtype is not t["bf16"]:
+        raise ValueError("gamma_q and gamma_k must be bfloat16")
+    check(_append_q8(
+        q.data_ptr(), qs, qh, q_out.data_ptr(), os_, oh, k.data_ptr(), ks, kh,
+        v.data_ptr(), vs, vh, _ints(positions, t["i64"], T, "positions"),
+        _ints(slot_mapping, t["i64"], T, "slot_mapping"), gamma_q.data_ptr(), gamma_k.data_ptr(),
+        theta, eps, T, Hq, _pack_q8(t, k_cache, v_cache, k_scales, v_scales),
+        _ptr(rope_table), table_positions, _ptr(status_flags), _raw_stream(t, stream, q)))
+
+
+def _attend_q8(f, q, caches, block_tables, seq_lens, out, q_len, num_splits, max_seq_len_hint,
+               scale, lse_out, workspace, status_flags, stream):
+    t = _q8 or _q8_names()
+    rows, Hq, qs, qh = _heads(t, q, "q")
+    batch = seq_lens.shape[0]
+    if q_len * batch != rows:
+        raise ValueError("q must hold q_len rows for each sequence of seq_lens")
+    table, width = _table(t, block_tables, batch)
+    o, lse = _results(t, out, lse_out, rows, Hq)
+    check(f(
+        q.data_ptr(), qs, qh, _pack_q8(t, *caches), table, width,
+        _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, q_len, Hq, num_splits,
+        max_seq_len_hint, scale, o, lse, _ptr(workspace),
+        0 if workspace is None else workspace.nbytes, _ptr(status_flags),
+        _raw_stream(t, stream, q)))
 
 
 def paged_decode_q8(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, out, *,
                     q_len=1, num_splits=1, max_seq_len_hint=0, scale=0.0, lse_out=None,
                     workspace=None, status_flags=None, stream=None):
     """paged_decode over an 8-bit cache (see q8_cache)."""
-    Tq, Hq, D = q.shape
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    check(pkvqk_paged_decode_q8(
-        _ptr(q), q.stride(0), q.stride(1), ctypes.byref(cache),
-        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
-        Tq // q_len, q_len, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
-        _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
-        _ptr(status_flags), _stream(stream)))
+    _attend_q8(_paged_decode_q8, q, (k_cache, v_cache, k_scales, v_scales), block_tables,
+               seq_lens, out, q_len, num_splits, max_seq_len_hint, scale, lse_out, workspace,
+               status_flags, stream)
 
 
 def paged_prefill_q8(q, k_cache, v_cache, k_scales, v_scales, block_tables, seq_lens, out, *,
                      q_len, num_splits=1, max_seq_len_hint=0, scale=0.0, lse_out=None,
                      workspace=None, status_flags=None, stream=None):
     """paged_prefill over an 8-bit cache (see q8_cache)."""
-    Tq, Hq, D = q.shape
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    check(pkvqk_paged_prefill_q8(
-        _ptr(q), q.stride(0), q.stride(1), ctypes.byref(cache),
-        _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
-        Tq // q_len, q_len, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
-        _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
-        _ptr(status_flags), _stream(stream)))
+    _attend_q8(_paged_prefill_q8, q, (k_cache, v_cache, k_scales, v_scales), block_tables,
+               seq_lens, out, q_len, num_splits, max_seq_len_hint, scale, lse_out, workspace,
+               status_flags, stream)
 
 
 def paged_prefill_varlen_q8(q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scales, v_scales,
@@ -470,14 +558,14 @@ def paged_prefill_varlen_q8(q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scal
                             scale=0.0, lse_out=None, workspace=None, status_flags=None,
                             stream=None):
     """paged_prefill_varlen over an 8-bit cache (see q8_cache)."""
-    total_q, Hq, D = q.shape
-    if not out.is_contiguous():
-        raise ValueError("out must be contiguous")
-    cache = q8_cache(k_cache, v_cache, k_scales, v_scales)
-    ws_bytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    check(pkvqk_paged_prefill_varlen_q8(
-        _ptr(q), q.stride(0), q.stride(1), _ptr(cu_seqlens_q), int(max_q_len), int(total_q),
-        ctypes.byref(cache), _ptr(block_tables), block_tables.shape[1], _ptr(seq_lens),
-        cu_seqlens_q.shape[0] - 1, Hq, int(num_splits), int(max_seq_len_hint), float(scale),
-        _ptr(out), _ptr(lse_out), _ptr(workspace), ws_bytes,
-        _ptr(status_flags), _stream(stream)))
+    t = _q8 or _q8_names()
+    total_q, Hq, qs, qh = _heads(t, q, "q")
+    batch = seq_lens.shape[0]
+    table, width = _table(t, block_tables, batch)
+    o, lse = _results(t, out, lse_out, total_q, Hq)
+    check(_paged_prefill_varlen_q8(
+        q.data_ptr(), qs, qh, _ints(cu_seqlens_q, t["i32"], batch + 1, "cu_seqlens_q"), max_q_len,
+        total_q, _pack_q8(t, k_cache, v_cache, k_scales, v_scales), table, width,
+        _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, Hq, num_splits, max_seq_len_hint,
+        scale, o, lse, _ptr(workspace), 0 if workspace is None else workspace.nbytes,
+        _ptr(status_flags), _raw_stream(t, stream, q)))

@@ -123,3 +123,61 @@ def test_binding_refuses_mismatched_tensors(lib):
                  (k.transpose(2, 3), k.transpose(2, 3), s, s)):
         with pytest.raises(ValueError):
             lib.q8_cache(*args)
+
+
+def _cpu_call(**change):
+    """Arguments of an append and a decode on host tensors, some of them replaced."""
+    bf, i32, i64 = torch.bfloat16, torch.int32, torch.int64
+    a = dict(q=torch.zeros(4, 4, 128, dtype=bf), k=torch.zeros(4, 2, 128, dtype=bf),
+             v=torch.zeros(4, 2, 128, dtype=bf), pos=torch.zeros(4, dtype=i64),
+             slots=torch.zeros(4, dtype=i64), g=torch.zeros(128, dtype=bf),
+             kc=torch.zeros(4, 16, 2, 128, dtype=torch.int8), s=torch.zeros(4, 1, 2),
+             table=torch.zeros(4, 4, dtype=i32), lens=torch.zeros(4, dtype=i32),
+             out=torch.zeros(4, 4, 128, dtype=bf), lse=torch.zeros(4, 4), q_out=None)
+    a.update(change)
+    return a
+
+
+def _cpu_append(lib, **change):
+    a = _cpu_call(**change)
+    lib.norm_rope_append_q8(a["q"], a["k"], a["v"], a["pos"], a["slots"], a["g"], a["g"], 1e6,
+                            1e-6, a["kc"], a["kc"].clone(), a["s"], a["s"].clone(),
+                            q_out=a["q_out"])
+
+
+def _cpu_decode(lib, **change):
+    a = _cpu_call(**change)
+    for f, kw in ((lib.paged_decode_q8, {}), (lib.paged_prefill_q8, dict(q_len=1))):
+        f(a["q"], a["kc"], a["kc"].clone(), a["s"], a["s"].clone(), a["table"], a["lens"],
+          a["out"], lse_out=a["lse"], **kw)
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=torch.zeros(4, 4, 128)), dict(k=torch.zeros(4, 3, 128, dtype=torch.bfloat16)),
+    dict(k=torch.zeros(4, 2, 256, dtype=torch.bfloat16)[..., ::2]),
+    dict(v=torch.zeros(3, 2, 128, dtype=torch.bfloat16)),
+    dict(pos=torch.zeros(4, dtype=torch.int32)), dict(slots=torch.zeros(3, dtype=torch.int64)),
+    dict(slots=torch.zeros(8, dtype=torch.int64)[::2]), dict(g=torch.zeros(128)),
+    dict(q_out=torch.zeros(4, 5, 128, dtype=torch.bfloat16))], ids=lambda c: next(iter(c)))
+def test_append_binding_refuses(lib, change):
+    with pytest.raises(ValueError):
+        _cpu_append(lib, **change)
+
+
+@pytest.mark.parametrize("change", [
+    dict(q=torch.zeros(4, 4, 128)), dict(q=torch.zeros(5, 4, 128, dtype=torch.bfloat16)),
+    dict(table=torch.zeros(4, 4, dtype=torch.int64)),
+    dict(table=torch.zeros(3, 4, dtype=torch.int32)), dict(lens=torch.zeros(4)),
+    dict(out=torch.zeros(4, 4, 128)), dict(out=torch.zeros(4, 3, 128, dtype=torch.bfloat16)),
+    dict(lse=torch.zeros(4, 5)), dict(lse=torch.zeros(4, 4, dtype=torch.float64))],
+    ids=lambda c: next(iter(c)))
+def test_attention_binding_refuses(lib, change):
+    with pytest.raises(ValueError):
+        _cpu_decode(lib, **change)
+
+
+def test_host_tensors_are_refused(lib):
+    """Well-formed, but on the host: the library's residency check."""
+    for call in (_cpu_append, _cpu_decode):
+        with pytest.raises(lib.PkvqkError):
+            call(lib)
