@@ -19,10 +19,13 @@
 // a window of 16 consecutive tokens (one per half-warp, lane l holding elements
 // 4l.. and 64+4l.. as in the bf16 append) and, of the q and kv heads, a
 // contiguous share.  Tokens of one group are adjacent in token order (a run);
-// the window in which a run starts owns all of it, so it may reach up to 15
-// tokens into the next window (second pass) and every group is written by one
-// CTA, without atomics.  A token's rotary angles are read (table) or computed
-// once per CTA and serve all its heads.
+// the window in which a run starts owns all of it, so every group is written by
+// one CTA, without atomics.  Its runs are taken in chunks of whole runs, at most
+// 16 tokens each: one chunk where groups and windows are aligned or shifted against
+// each other alike (it then reaches into the next window), two at most where runs
+// of different sequences meet.  A token's rotary angles are read (table) or
+// computed once per CTA and chunk and serve all its heads; the next head's values
+// load while a head is being quantised.
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
@@ -36,16 +39,13 @@ namespace {
 
 constexpr int kWindow = 16;                    // tokens per CTA, one per half-warp
 constexpr int kThreads = kWindow * 16;
+// Many tokens: four CTAs share an SM at 64 registers and a head vector's share of
+// a window is cut so that three waves of them come (measured on 4 x 2048 tokens, 16
+// q and 8 kv heads: 42.8 us; two waves 44.6, four 47.7; three CTAs an SM 46.7-50.8,
+// two at 108 registers 57.2).  Few: two, without spills (64 tokens 5.1 us against 5.9).
+constexpr int kManyTokens = 1024;
+constexpr int kManyCtas = 4, kManyWaves = 3, kFewCtas = 2;
 static_assert(kWindow == kScaleGroup, "a run spans at most two windows");
-
-// A run as one of its tokens sees it: window-relative tokens [s, e) of one
-// group, the slots they write, s < 0 where the token is not this CTA's.
-struct Run {
-  int s, e;
-  uint32_t slots;
-  __device__ bool active() const { return s >= 0; }
-  __device__ bool fresh() const { return (slots & 1u) != 0; }
-};
 
 template <int kFormat>
 __device__ __forceinline__ int scale_exponent(float amax) {
@@ -89,311 +89,366 @@ __device__ __forceinline__ void decode4(uint32_t w, float (&f)[4]) {
   }
 }
 
-// Finite part of |y|, and whether anything was not finite.
-__device__ __forceinline__ float finite_abs(float y, bool& bad) {
-  const float a = fabsf(y);
-  const bool fin = a <= 3.402823466e38f;       // false for NaN too
-  bad |= !fin;
-  return fin ? a : 0.f;
+// max(a, |b|, |c|) for a >= 0, NaN if any is.
+__device__ __forceinline__ float max_abs3(float a, float b, float c) {
+  float d;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
+// The largest |y| of eight values; where that is not finite, NaN in y becomes 0
+// (which is how it is stored), infinities do not count, and the result is of the
+// finite ones.
+__device__ __forceinline__ float max_finite(float (&y)[8], bool& bad) {
+  float m = max_abs3(max_abs3(0.f, y[0], y[1]), y[2], y[3]);
+  m = max_abs3(max_abs3(m, y[4], y[5]), y[6], y[7]);
+  if (!(m <= 3.402823466e38f)) {
+    bad = true;
+    m = 0.f;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      y[e] = y[e] == y[e] ? y[e] : 0.f;
+      const float v = fabsf(y[e]);
+      m = fmaxf(m, v <= 3.402823466e38f ? v : 0.f);
+    }
+  }
+  return m;
 }
 
 __device__ __forceinline__ uint32_t half_mask() {
   return 0xffffu << (threadIdx.x & 16);
 }
 
-// Where a token's codes and its group's scale live.
+// Where a token's codes and its group's scale live: offsets for head 0.
 struct Place {
-  int64_t code, scale;                         // element offsets for head 0
-  int64_t group_code;                          // code offset of the group's slot 0
+  int64_t code, scale;
 };
 
 __device__ __forceinline__ Place place(const AppendQ8Args& a, int64_t slot) {
   const int64_t blk = slot / a.base.block_size;
   const int in = static_cast<int>(slot - blk * a.base.block_size);
   Place p;
-  p.group_code = blk * a.base.block_stride +
-                 static_cast<int64_t>(in & ~(kScaleGroup - 1)) * a.base.slot_stride;
-  p.code = p.group_code + static_cast<int64_t>(in & (kScaleGroup - 1)) * a.base.slot_stride;
+  p.code = blk * a.base.block_stride + in * a.base.slot_stride;
   p.scale = blk * a.scales.block_stride + (in / kScaleGroup) * a.scales.group_stride;
   return p;
 }
 
-// The rest of a group follows its scale from `old` to `now`: the slots that the
-// run does not write, by the half-warp of the run's first token (8 bytes a
-// lane, eight slots in flight).
-template <int kFormat>
-__device__ __forceinline__ void rescale_group(uint8_t* codes, int64_t slot_stride, uint32_t written,
-                                              float ratio, int l) {
+// A group whose scale grew: its other slots' codes follow it.
+struct Grown {
+  uint8_t* codes;                              // the group's slot 0
+  uint32_t written;                            // slots that the call writes: left alone
+  float ratio;                                 // old scale / new scale
+};
+constexpr int kMostGrown = kWindow;            // per head: one a run
+
+struct Smem {
+  // cos hi, cos lo, sin hi, sin lo of the half-warps' tokens, 64 frequencies each
+  alignas(16) float trig[4][kWindow][kHeadDim / 2];
+  alignas(16) float knots[kSinCosKnots][4];
+  alignas(16) float amax[2][kWindow];          // [parity][half-warp]
+  alignas(16) Grown grown[3][kMostGrown];
+  int num_grown[3];
+  alignas(16) int64_t slot[2 * kWindow + 1];   // of tokens window - 1 .. window + 31, -1: none
+};
+
+// The half-warp's angles of position pos into its part of shared memory: from the
+// table, or computed (four frequencies a lane).
+__device__ __forceinline__ void put_angles(const NormRopeAppendArgs& n, Smem& sm, int64_t pos,
+                                           bool computed, int hw, int l) {
+  __syncwarp();                                // reads of the token before
+  if (!computed) {
+    // float4 f of the row: component f % 4 of lane f / 4
+    const float4* row = n.rope_table + pos * (kHeadDim / 2);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int f = i * 16 + l;
+      *reinterpret_cast<float4*>(&sm.trig[f & 3][hw][(f >> 2) * 4]) = __ldg(row + f);
+    }
+  } else {
 #pragma unroll 1
-  for (int b = 0; b < kScaleGroup; b += 8) {
-    uint2 w[8];
+    for (int f = l; f < kHeadDim / 2; f += 16) {
+      FF x, sn, cs;
+      const int quadrant = reduce_angle(static_cast<double>(pos), n.inv_freq[f], &x);
+      sincos_ff(x, quadrant, sm.knots, &sn, &cs);
+      sm.trig[0][hw][f] = cs.hi;
+      sm.trig[1][hw][f] = cs.lo;
+      sm.trig[2][hw][f] = sn.hi;
+      sm.trig[3][hw][f] = sn.lo;
+    }
+  }
+  __syncwarp();
+}
+
+// Read where they are used (and not kept over the heads: the registers let four
+// CTAs share an SM).
+__device__ __forceinline__ float4 lds_f4(const float* p) {
+  float4 v;
+  asm volatile("ld.shared.v4.f32 {%0,%1,%2,%3}, [%4];"
+               : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+               : "r"(smem_addr(p)));
+  return v;
+}
+__device__ __forceinline__ Trig angles(const Smem& sm, int hw, int l) {
+  Trig t;
+  t.ch = lds_f4(&sm.trig[0][hw][4 * l]);
+  t.cl = lds_f4(&sm.trig[1][hw][4 * l]);
+  t.sh = lds_f4(&sm.trig[2][hw][4 * l]);
+  t.sl = lds_f4(&sm.trig[3][hw][4 * l]);
+  return t;
+}
+
+__device__ __forceinline__ void gains(const __nv_bfloat16* g, int l, float (&g0)[4],
+                                      float (&g1)[4]) {
+  unpack4(__ldg(reinterpret_cast<const uint2*>(g + 4 * l)), g0);
+  unpack4(__ldg(reinterpret_cast<const uint2*>(g + 64 + 4 * l)), g1);
+}
+
+// The codes of grown groups, half-warp hw slot hw of each (8 bytes a lane, four
+// groups in flight).
+template <int kFormat>
+__device__ __forceinline__ void rescale(const Grown* list, int count, int64_t slot_stride, int hw,
+                                        int l) {
+#pragma unroll 1
+  for (int g = 0; g < count; g += 4) {
+    uint2 w[4];
 #pragma unroll
-    for (int j = 0; j < 8; ++j)
-      if (!((written >> (b + j)) & 1u))
-        w[j] = *reinterpret_cast<const uint2*>(codes + (b + j) * slot_stride + 8 * l);
+    for (int i = 0; i < 4; ++i)
+      if (g + i < count && !((list[g + i].written >> hw) & 1u))
+        w[i] = *reinterpret_cast<const uint2*>(list[g + i].codes + hw * slot_stride + 8 * l);
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      if ((written >> (b + j)) & 1u) continue;
-      float f[4], g[4];
-      decode4<kFormat>(w[j].x, f);
-      decode4<kFormat>(w[j].y, g);
-      *reinterpret_cast<uint2*>(codes + (b + j) * slot_stride + 8 * l) =
-          make_uint2(encode4<kFormat>(f[0] * ratio, f[1] * ratio, f[2] * ratio, f[3] * ratio),
-                     encode4<kFormat>(g[0] * ratio, g[1] * ratio, g[2] * ratio, g[3] * ratio));
+    for (int i = 0; i < 4; ++i) {
+      if (g + i >= count || ((list[g + i].written >> hw) & 1u)) continue;
+      const float r = list[g + i].ratio;
+      float x[4], y[4];
+      decode4<kFormat>(w[i].x, x);
+      decode4<kFormat>(w[i].y, y);
+      *reinterpret_cast<uint2*>(list[g + i].codes + hw * slot_stride + 8 * l) =
+          make_uint2(encode4<kFormat>(x[0] * r, x[1] * r, x[2] * r, x[3] * r),
+                     encode4<kFormat>(y[0] * r, y[1] * r, y[2] * r, y[3] * r));
     }
   }
 }
 
-struct Smem {
-  // cos hi, cos lo, sin hi, sin lo; read as float4
-  alignas(16) float trig[4][2 * kWindow][kHeadDim / 2];
-  alignas(16) float knots[kSinCosKnots][4];
-  alignas(16) float amax[2][2][2 * kWindow];   // [parity][K, V][token]
-  alignas(16) int64_t slot[2 * kWindow + 1];   // of tokens window - 1 .. window + 31, -1: none
-};
-
+// The scale of a group from its run's maximum m; *prev: the stored one as it counts.
 template <int kFormat>
-__global__ void __launch_bounds__(kThreads)
-norm_rope_append_q8_kernel(const __grid_constant__ AppendQ8Args a) {
-  __shared__ __align__(16) Smem sm;
+__device__ __forceinline__ float group_scale(float m, float stored, uint32_t written,
+                                             float* prev) {
+  const float lo = __int_as_float((127 + kScaleMinExp) << 23);
+  const float hi = __int_as_float((127 + kScaleMaxExp) << 23);
+  const float want = __int_as_float((127 + scale_exponent<kFormat>(m)) << 23);
+  *prev = stored >= lo && stored <= hi ? stored : lo;
+  return (written & 1u) ? want : fmaxf(want, *prev);
+}
+
+// The lane's eight values as codes (dims 4l.. at `code`, 64 + 4l.. 64 bytes on);
+// returns 1 / scale, exact for a power of two.
+template <int kFormat>
+__device__ __forceinline__ float write_codes(const float (&y)[8], float scale, uint8_t* code) {
+  const float inv = __frcp_rn(scale);
+  const uint64_t inv2 = pack2(inv, inv);
+  float z[8];
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(y[e], y[e + 1]), inv2), z[e], z[e + 1]);
+  *reinterpret_cast<uint32_t*>(code) = encode4<kFormat>(z[0], z[1], z[2], z[3]);
+  *reinterpret_cast<uint32_t*>(code + 64) = encode4<kFormat>(z[4], z[5], z[6], z[7]);
+  return inv;
+}
+
+// K (kIsK) or V of kv heads [h0, h1): the runs that start in the window.
+template <int kFormat, bool kIsK>
+__device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bool computed,
+                                             int h0, int h1) {
   const NormRopeAppendArgs& n = a.base;
   const int tid = threadIdx.x, lane = tid & 31, l = tid & 15, hw = tid >> 4;
+  const int t0 = blockIdx.x * kWindow;
+  // V: tokens window .. window + 31 with a slot; B: those that start a run
+  const int64_t my = sm.slot[lane + 1], before = sm.slot[lane];
+  const uint32_t V = __ballot_sync(0xffffffffu, my >= 0);
+  const uint32_t B = __ballot_sync(
+      0xffffffffu, my >= 0 && (before < 0 || before / kScaleGroup != my / kScaleGroup));
+  auto run_end = [&](int s) {
+    const uint32_t after = (B | ~V) & ~((2u << s) - 1u);
+    return after != 0u ? __ffs(after) - 1 : 2 * kWindow;
+  };
+  // head k of all chunks: maxima in buffer k % 2; grown groups in list k % 3,
+  // rescaled at the next head's barrier and emptied at the one after
+  int k = 0, list = 0;
+  bool bad = false;
+  uint32_t todo = B & 0xffffu;                 // runs that start in the window
+#pragma unroll 1
+  while (todo != 0u) {                         // uniform over the CTA
+    // chunk [b, b + len): whole runs, at most 16 tokens; half-warp hw has b + hw
+    const int b = __ffs(todo) - 1;
+    int len = 0;
+    while (todo != 0u) {
+      const int e = run_end(__ffs(todo) - 1);
+      if (len > 0 && e - b > kWindow) break;
+      len = min(e - b, kWindow);
+      todo &= todo - 1u;
+    }
+    const int j = b + hw;
+    const bool active = hw < len && ((V >> j) & 1u);
+    const int rs = active ? 31 - __clz(B & ((2u << j) - 1u)) : j;
+    const int re = active ? min(run_end(j), b + len) : j;
+    const bool first = active && j == rs;
+    uint32_t written = 0u;                     // slots of the group that the run writes
+    if (rs + l < re) written = 1u << (sm.slot[rs + l + 1] & (kScaleGroup - 1));
+    written = __reduce_or_sync(half_mask(), written);
+    const int peer = rs + l < re ? rs + l - b : -1;   // half-warp whose maximum this lane takes
+    const int64_t tok = active ? t0 + j : 0;
+    if (kIsK) put_angles(n, sm, active ? n.positions[tok] : 0, computed, hw, l);
+    // of head h: this lane's values, code chunk and scale
+    const int64_t stride_h = kIsK ? n.k_stride_h : n.v_stride_h;
+    const __nv_bfloat16* src =
+        (kIsK ? n.k + tok * n.k_stride_t : n.v + tok * n.v_stride_t) + h0 * stride_h + 4 * l;
+    uint8_t* code;
+    float* scale;
+    {
+      const Place at = place(a, active ? sm.slot[j + 1] : 0);
+      code = (kIsK ? a.k_codes : a.v_codes) + at.code + h0 * n.head_stride + 4 * l;
+      scale = (kIsK ? a.scales.k : a.scales.v) + at.scale + h0 * a.scales.head_stride;
+    }
+    const int offset = active ? static_cast<int>(sm.slot[j + 1] & (kScaleGroup - 1)) : 0;
+    uint2 x0w = make_uint2(0u, 0u), x1w = x0w;
+    float next_scale = 0.f;
+    if (active) {
+      x0w = __ldg(reinterpret_cast<const uint2*>(src));
+      x1w = __ldg(reinterpret_cast<const uint2*>(src + 64));
+      if (!(written & 1u)) next_scale = *scale;
+    }
+#pragma unroll 1
+    for (int h = h0; h < h1; ++h, ++k) {
+      float x0[4], x1[4], y[8];
+      unpack4(x0w, x0);
+      unpack4(x1w, x1);
+      const float stored = next_scale;
+      src += stride_h;
+      if (active && h + 1 < h1) {              // the next head's
+        x0w = __ldg(reinterpret_cast<const uint2*>(src));
+        x1w = __ldg(reinterpret_cast<const uint2*>(src + 64));
+        if (!(written & 1u)) next_scale = scale[a.scales.head_stride];
+      }
+      if (kIsK) {
+        float o0[4], o1[4], g0[4], g1[4];
+        gains(n.gamma_k, l, g0, g1);
+        norm_rotate(x0, x1, g0, g1, n.eps, angles(sm, hw, l), o0, o1);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = o0[e];
+          y[4 + e] = o1[e];
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          y[e] = x0[e];
+          y[4 + e] = x1[e];
+        }
+      }
+      float m = max_finite(y, bad);
+      m = __uint_as_float(__reduce_max_sync(half_mask(), __float_as_uint(m)));
+      if (l == 0) sm.amax[k & 1][hw] = m;
+      __syncthreads();
+      rescale<kFormat>(sm.grown[list], sm.num_grown[list], n.slot_stride, hw, l);
+      list = list == 2 ? 0 : list + 1;
+      if (tid == 0) sm.num_grown[list == 2 ? 0 : list + 1] = 0;
+      m = peer >= 0 ? sm.amax[k & 1][peer] : 0.f;
+      m = __uint_as_float(__reduce_max_sync(half_mask(), __float_as_uint(m)));
+      if (active) {
+        float prev;
+        const float now = group_scale<kFormat>(m, stored, written, &prev);
+        const float inv = write_codes<kFormat>(y, now, code);
+        if (first && l == 0) {
+          *scale = now;
+          if (!(written & 1u) && now > prev)
+            sm.grown[list][atomicAdd(&sm.num_grown[list], 1)] = {
+                code - offset * n.slot_stride, written, prev * inv};
+        }
+      }
+      code += n.head_stride;
+      scale += a.scales.head_stride;
+    }
+  }
+  __syncthreads();
+  rescale<kFormat>(sm.grown[list], sm.num_grown[list], n.slot_stride, hw, l);
+  __syncthreads();
+  if (tid < 3) sm.num_grown[tid] = 0;          // for the next tensor (it has a barrier before use)
+  if (bad) report(n.status_flags, kFlagBadValue);   // inactive half-warps hold zeros
+}
+
+template <int kFormat, int kMinCtas>
+__global__ void __launch_bounds__(kThreads, kMinCtas)
+norm_rope_append_q8_kernel(const __grid_constant__ AppendQ8Args a) {
+  __shared__ Smem sm;
+  const NormRopeAppendArgs& n = a.base;
+  const int tid = threadIdx.x, l = tid & 15, hw = tid >> 4;
   const int t0 = blockIdx.x * kWindow;         // first token of the window
-  const int items = n.num_q_heads + n.num_kv_heads;   // kv heads first, then q heads
+  // head vectors of this part: K of the kv heads, V of them, q heads
+  const int hkv = n.num_kv_heads, items = n.num_q_heads + 2 * hkv;
   const int i0 = static_cast<int>(static_cast<int64_t>(blockIdx.y) * items / a.parts);
   const int i1 = static_cast<int>(static_cast<int64_t>(blockIdx.y + 1) * items / a.parts);
 
   pdl_launch_dependents();
   pdl_wait();
 
+  // slots of the window and the next one; are their positions in the table?
+  bool outside = false;
   if (tid < 2 * kWindow + 1) {
     const int64_t t = static_cast<int64_t>(t0) - 1 + tid;
-    int64_t slot = t >= 0 && t < n.num_tokens ? n.slot_mapping[t] : -1;
+    const bool live = t >= 0 && t < n.num_tokens;
+    int64_t slot = live ? n.slot_mapping[t] : -1;
     if (slot >= n.num_blocks * n.block_size) {
       report(n.status_flags, kFlagBadSlot);
       slot = -1;
     }
     sm.slot[tid] = slot < 0 ? -1 : slot;
-  }
-  __syncthreads();
-  // starts and validity of tokens window .. window + 31
-  const int64_t my = sm.slot[lane + 1], before = sm.slot[lane];
-  const bool valid = my >= 0;
-  const uint32_t V = __ballot_sync(0xffffffffu, valid);
-  const uint32_t B = __ballot_sync(
-      0xffffffffu, valid && (before < 0 || before / kScaleGroup != my / kScaleGroup));
-  auto run_of = [&](int j) {
-    Run r{-1, -1, 0u};
-    const uint32_t upto = B & ((2u << j) - 1u);
-    if (((V >> j) & 1u) && upto != 0u) {
-      const int s = 31 - __clz(upto);
-      if (s < kWindow) {
-        const uint32_t after = (B | ~V) & ~((2u << s) - 1u);
-        r.s = s;
-        r.e = after != 0u ? __ffs(after) - 1 : 2 * kWindow;
-      }
+    if (tid < 3) sm.num_grown[tid] = 0;
+    if (tid > 0) {
+      const int64_t pos = live ? n.positions[t] : 0;
+      outside = !(pos >= 0 && pos < n.table_positions);
     }
-    return r;
-  };
-  auto slots_of = [&](Run& r) {                // the half-warp together
-    uint32_t m = 0u;
-    for (int j = r.s + l; r.active() && j < r.e; j += 16)
-      m |= 1u << (sm.slot[j + 1] & (kScaleGroup - 1));
-    r.slots = __reduce_or_sync(half_mask(), m);
-  };
-  Run run[2] = {run_of(hw), run_of(kWindow + hw)};
-  slots_of(run[0]);
-  slots_of(run[1]);
-  const bool second = run_of(kWindow).active();        // uniform over the CTA
-
-  // angles: from the table where every token of the window (and of runs that
-  // reach past it) is in it, else computed, four lanes' frequencies a thread
-  const int tok[2] = {t0 + hw, t0 + kWindow + hw};
-  int64_t pos[2];
-  bool outside = false;
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    pos[p] = (p == 0 || run[p].active()) && tok[p] < n.num_tokens ? n.positions[tok[p]] : 0;
-    outside |= (p == 0 || run[p].active()) && !(pos[p] >= 0 && pos[p] < n.table_positions);
   }
   const bool computed = __syncthreads_or(outside) != 0;
   if (computed) {
     for (int e = tid; e < kSinCosKnots * 4; e += kThreads)
       (&sm.knots[0][0])[e] = (&n.sincos_tab[0][0])[e];
     __syncthreads();
-#pragma unroll 1
-    for (int p = 0; p < (second ? 2 : 1); ++p)
-#pragma unroll 1
-      for (int f = l; f < kHeadDim / 2; f += 16) {
-        FF x, sn, cs;
-        const int quadrant = reduce_angle(static_cast<double>(pos[p]), n.inv_freq[f], &x);
-        sincos_ff(x, quadrant, sm.knots, &sn, &cs);
-        const int j = p * kWindow + hw;
-        sm.trig[0][j][f] = cs.hi;
-        sm.trig[1][j][f] = cs.lo;
-        sm.trig[2][j][f] = sn.hi;
-        sm.trig[3][j][f] = sn.lo;
-      }
-    __syncwarp();                              // a half-warp reads its own tokens only
   }
-  auto trig_of = [&](int p) {
-    Trig t;
-    if (computed) {
-      const int j = p * kWindow + hw;
-      t.ch = *reinterpret_cast<const float4*>(&sm.trig[0][j][4 * l]);
-      t.cl = *reinterpret_cast<const float4*>(&sm.trig[1][j][4 * l]);
-      t.sh = *reinterpret_cast<const float4*>(&sm.trig[2][j][4 * l]);
-      t.sl = *reinterpret_cast<const float4*>(&sm.trig[3][j][4 * l]);
-    } else {
-      const float4* row = n.rope_table + (pos[p] * (kHeadDim / 8) + l) * 4;
-      t.ch = __ldg(row);
-      t.cl = __ldg(row + 1);
-      t.sh = __ldg(row + 2);
-      t.sl = __ldg(row + 3);
-    }
-    return t;
-  };
-  const Trig tr = trig_of(0);
-  auto gains = [&](const __nv_bfloat16* g, float (&g0)[4], float (&g1)[4]) {
-    unpack4(__ldg(reinterpret_cast<const uint2*>(g + 4 * l)), g0);
-    unpack4(__ldg(reinterpret_cast<const uint2*>(g + 64 + 4 * l)), g1);
-  };
-
-  // ---- kv heads of this part
-  const int kv1 = min(i1, n.num_kv_heads);
-  if (i0 < kv1) {
-    float g0[4], g1[4];
-    gains(n.gamma_k, g0, g1);
-    Place at[2];
-#pragma unroll
-    for (int p = 0; p < 2; ++p)
-      at[p] = place(a, run[p].active() ? sm.slot[p * kWindow + hw + 1] : 0);
-    int parity = 0;
-    bool bad = false;
-#pragma unroll 1
-    for (int h = i0; h < kv1; ++h, parity ^= 1) {
-      float y[2][2][8];                        // [pass][K, V]
-      float old[2][2];                         // scales before this call
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        if (p == 1 && !second) break;
-        uint2 k0, k1, v0, v1;
-        k0 = k1 = v0 = v1 = make_uint2(0u, 0u);
-        old[p][0] = old[p][1] = 0.f;
-        if (run[p].active()) {
-          const __nv_bfloat16* ks = n.k + tok[p] * n.k_stride_t + h * n.k_stride_h;
-          const __nv_bfloat16* vs = n.v + tok[p] * n.v_stride_t + h * n.v_stride_h;
-          k0 = __ldg(reinterpret_cast<const uint2*>(ks + 4 * l));
-          k1 = __ldg(reinterpret_cast<const uint2*>(ks + 64 + 4 * l));
-          v0 = __ldg(reinterpret_cast<const uint2*>(vs + 4 * l));
-          v1 = __ldg(reinterpret_cast<const uint2*>(vs + 64 + 4 * l));
-          if (!run[p].fresh()) {
-            const int64_t so = at[p].scale + h * a.scales.head_stride;
-            old[p][0] = a.scales.k[so];
-            old[p][1] = a.scales.v[so];
-          }
-        }
-        float x0[4], x1[4], o0[4], o1[4];
-        unpack4(k0, x0);
-        unpack4(k1, x1);
-        norm_rotate(x0, x1, g0, g1, n.eps, p == 0 ? tr : trig_of(1), o0, o1);
-        float w0[4], w1[4];
-        unpack4(v0, w0);
-        unpack4(v1, w1);
-        float mk = 0.f, mv = 0.f;
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          y[p][0][j] = o0[j];
-          y[p][0][4 + j] = o1[j];
-          y[p][1][j] = w0[j];
-          y[p][1][4 + j] = w1[j];
-        }
-        bool nonfinite = false;
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          mk = fmaxf(mk, finite_abs(y[p][0][j], nonfinite));
-          mv = fmaxf(mv, finite_abs(y[p][1][j], nonfinite));
-        }
-        if (nonfinite) {                       // NaN is stored as 0
-          bad |= run[p].active();
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            y[p][0][j] = y[p][0][j] == y[p][0][j] ? y[p][0][j] : 0.f;
-            y[p][1][j] = y[p][1][j] == y[p][1][j] ? y[p][1][j] : 0.f;
-          }
-        }
-        const uint32_t uk = __reduce_max_sync(half_mask(), __float_as_uint(mk));
-        const uint32_t uv = __reduce_max_sync(half_mask(), __float_as_uint(mv));
-        if (l == 0) {
-          sm.amax[parity][0][p * kWindow + hw] = __uint_as_float(uk);
-          sm.amax[parity][1][p * kWindow + hw] = __uint_as_float(uv);
-        }
-      }
-      __syncthreads();
-#pragma unroll
-      for (int p = 0; p < 2; ++p) {
-        if (p == 1 && !second) break;
-        const Run& r = run[p];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          float m = 0.f;
-          for (int j = r.s + l; r.active() && j < r.e; j += 16) m = fmaxf(m, sm.amax[parity][x][j]);
-          m = __uint_as_float(__reduce_max_sync(half_mask(), __float_as_uint(m)));
-          if (!r.active()) continue;
-          const float lo = __int_as_float((127 + kScaleMinExp) << 23);
-          const float hi = __int_as_float((127 + kScaleMaxExp) << 23);
-          const float want = __int_as_float((127 + scale_exponent<kFormat>(m)) << 23);
-          const float prev = old[p][x] >= lo && old[p][x] <= hi ? old[p][x] : lo;
-          const float now = r.fresh() ? want : fmaxf(want, prev);
-          const float inv = __frcp_rn(now);    // exact: a power of two
-          const float* yy = y[p][x];
-          uint8_t* codes = (x == 0 ? a.k_codes : a.v_codes) + h * n.head_stride;
-          *reinterpret_cast<uint32_t*>(codes + at[p].code + 4 * l) =
-              encode4<kFormat>(yy[0] * inv, yy[1] * inv, yy[2] * inv, yy[3] * inv);
-          *reinterpret_cast<uint32_t*>(codes + at[p].code + 64 + 4 * l) =
-              encode4<kFormat>(yy[4] * inv, yy[5] * inv, yy[6] * inv, yy[7] * inv);
-          if (p == 0 && r.s == hw) {           // the run's first token
-            if (l == 0) (x == 0 ? a.scales.k : a.scales.v)[at[p].scale + h * a.scales.head_stride] = now;
-            if (!r.fresh() && now > prev)
-              rescale_group<kFormat>(codes + at[p].group_code, n.slot_stride, r.slots, prev * inv,
-                                     l);
-          }
-        }
-      }
-    }
-    if (bad) report(n.status_flags, kFlagBadValue);
-  }
+  if (i0 < hkv) append_heads<kFormat, true>(a, sm, computed, i0, min(i1, hkv));
+  if (i0 < 2 * hkv && i1 > hkv)
+    append_heads<kFormat, false>(a, sm, computed, max(i0 - hkv, 0), min(i1 - hkv, hkv));
 
   // ---- q heads of this part
-  const int q0 = max(i0 - n.num_kv_heads, 0), q1 = i1 - n.num_kv_heads;
+  const int q0 = max(i0 - 2 * hkv, 0), q1 = i1 - 2 * hkv;
   if (q0 >= q1) return;
+  const bool live = t0 + hw < n.num_tokens;
+  const int64_t tok = live ? t0 + hw : 0;
+  put_angles(n, sm, live ? n.positions[tok] : 0, computed, hw, l);
   float g0[4], g1[4];
-  gains(n.gamma_q, g0, g1);
-  const bool live = tok[0] < n.num_tokens;
-  const __nv_bfloat16* src = n.q + (live ? tok[0] : 0) * n.q_stride_t;
-  __nv_bfloat16* dst = a.q_out + (live ? tok[0] : 0) * a.q_out_stride_t;
+  gains(n.gamma_q, l, g0, g1);
+  const __nv_bfloat16* src = n.q + tok * n.q_stride_t;
+  __nv_bfloat16* dst = a.q_out + tok * a.q_out_stride_t;
   constexpr int kAhead = 4;                    // vectors whose loads go first
 #pragma unroll 1
   for (int h = q0; h < q1; h += kAhead) {
     uint2 in[kAhead][2];
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      in[j][0] = in[j][1] = make_uint2(0u, 0u);
-      if (live && h + j < q1) {
-        const __nv_bfloat16* s = src + (h + j) * n.q_stride_h;
-        in[j][0] = *reinterpret_cast<const uint2*>(s + 4 * l);
-        in[j][1] = *reinterpret_cast<const uint2*>(s + 64 + 4 * l);
+    for (int i = 0; i < kAhead; ++i) {
+      in[i][0] = in[i][1] = make_uint2(0u, 0u);
+      if (live && h + i < q1) {
+        const __nv_bfloat16* x = src + (h + i) * n.q_stride_h;
+        in[i][0] = *reinterpret_cast<const uint2*>(x + 4 * l);
+        in[i][1] = *reinterpret_cast<const uint2*>(x + 64 + 4 * l);
       }
     }
 #pragma unroll
-    for (int j = 0; j < kAhead; ++j) {
-      if (h + j >= q1) break;
+    for (int i = 0; i < kAhead; ++i) {
+      if (h + i >= q1) break;
       float x0[4], x1[4], o0[4], o1[4];
-      unpack4(in[j][0], x0);
-      unpack4(in[j][1], x1);
-      norm_rotate(x0, x1, g0, g1, n.eps, tr, o0, o1);
+      unpack4(in[i][0], x0);
+      unpack4(in[i][1], x1);
+      norm_rotate(x0, x1, g0, g1, n.eps, angles(sm, hw, l), o0, o1);
       if (live) {
-        __nv_bfloat16* d = dst + (h + j) * a.q_out_stride_h;
+        __nv_bfloat16* d = dst + (h + i) * a.q_out_stride_h;
         *reinterpret_cast<uint2*>(d + 4 * l) =
             make_uint2(pack_bf16x2(o0[0], o0[1]), pack_bf16x2(o0[2], o0[3]));
         *reinterpret_cast<uint2*>(d + 64 + 4 * l) =
@@ -409,13 +464,19 @@ cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& args, cudaStream_t st
   if (args.base.num_tokens == 0) return cudaSuccess;
   AppendQ8Args a = args;
   const int windows = (a.base.num_tokens + kWindow - 1) / kWindow;
-  const int items = a.base.num_q_heads + a.base.num_kv_heads;
-  // enough parts for six CTAs on each of 152 SMs, at most one head each
-  const int want = (6 * 152 + windows - 1) / windows;
+  const int items = a.base.num_q_heads + 2 * a.base.num_kv_heads;
+  // enough parts for the wanted CTAs on 152 SMs, at most one head vector each
+  const bool many = a.base.num_tokens >= kManyTokens;
+  const int ctas = 152 * (many ? kManyCtas * kManyWaves : 3 * kFewCtas);
+  const int want = (ctas + windows - 1) / windows;
   a.parts = want < 1 ? 1 : (want > items ? items : want);
   const dim3 grid(windows, a.parts);
-  return launch_pdl(a.format == kFormatE4m3 ? norm_rope_append_q8_kernel<kFormatE4m3>
-                                            : norm_rope_append_q8_kernel<kFormatInt8>,
+  if (a.format == kFormatE4m3)
+    return launch_pdl(many ? norm_rope_append_q8_kernel<kFormatE4m3, kManyCtas>
+                           : norm_rope_append_q8_kernel<kFormatE4m3, kFewCtas>,
+                      grid, dim3(kThreads), 0, stream, a);
+  return launch_pdl(many ? norm_rope_append_q8_kernel<kFormatInt8, kManyCtas>
+                         : norm_rope_append_q8_kernel<kFormatInt8, kFewCtas>,
                     grid, dim3(kThreads), 0, stream, a);
 }
 

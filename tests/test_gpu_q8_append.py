@@ -226,3 +226,65 @@ def test_append_on_a_side_stream_captured_and_replayed(lib):
     g.replay()
     torch.cuda.synchronize()
     assert not torch.equal(c.k.view(torch.uint8), d.k.view(torch.uint8))
+
+
+# calls of 1024 tokens and more run on the kernel's narrower form: whole groups, runs that start inside a group and end in the next window,
+# many short sequences (several runs a window), padding between them
+MANY = [
+    (16, 8, [1024, 37, 200], 16, [0, 5, 16]),
+    (32, 4, [700, 700], 256, [3, 255]),
+    (14, 2, [9] * 130, 48, [7] * 130),
+    (4, 4, [1, 2, 16, 17, 31, 33] * 12, 16, [0, 15, 8, 1, 30, 2] * 12),
+]
+
+
+@pytest.mark.parametrize("fmt", CLASSES)
+@pytest.mark.parametrize("case", MANY, ids=lambda c: f"Hq{c[0]}-Hkv{c[1]}-B{len(c[2])}-bs{c[3]}")
+def test_append_of_many_tokens(lib, fmt, case):
+    Hq, Hkv, new, bs, priors = case
+    lens = [c + n for c, n in zip(priors, new)]
+    nb = sum(-(-n // bs) for n in lens) + 2
+    p = workloads.make_problem("q8", Hq, Hkv, 128, bs, lens, new, nb, 70, "cuda")
+    assert p.T >= 1024
+    p.v = (p.v.float() * torch.randn(p.T, Hkv, 1, device="cuda").exp2()).bfloat16()   # grows
+    n = max(lens)
+    for table_positions in (n, n // 2):      # all angles from the table, some computed
+        c = Q8(p, fmt, 7, unused=None)
+        before = _before(c)
+        flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+        q_out = torch.full_like(p.q, float("nan"))
+        _run(lib, p, c, q_out=q_out, table=_table(lib, p, n), n=table_positions, flags=flags)
+        torch.cuda.synchronize()
+        assert flags.item() == 0
+        _check(p, c, before, q_out, what=f"{fmt} {case[:2]} table {table_positions}")
+    # without a table, the same bits
+    d = Q8(p, fmt, 7, unused=None)
+    q2 = p.q.clone()
+    lib.norm_rope_append_q8(q2, p.k, p.v, p.positions, p.slot_mapping, p.gamma_q, p.gamma_k,
+                            p.theta, p.eps, *d.args())
+    torch.cuda.synchronize()
+    assert torch.equal(q2, q_out)
+    for x, y in zip(c.args(), d.args()):
+        assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
+def test_append_of_many_tokens_padding_bad_slots_and_non_finite_values(lib):
+    p = workloads.make_problem("q8", 8, 2, 128, 16, [40] * 60, 20, 200, 71, "cuda")
+    c = Q8(p, "e4m3", 8, unused=None)
+    slots = p.slot_mapping.clone()
+    slots[0:20] = -1                         # a padded sequence
+    slots[-1] = p.num_blocks * 16 + 3        # too large
+    p.v[100, 0, 3] = float("inf")
+    p.v[101, 1, 0] = float("nan")
+    before = _before(c)
+    flags = torch.zeros(1, dtype=torch.int32, device="cuda")
+    q_out = torch.empty_like(p.q)
+    _run(lib, p, c, slots=slots, q_out=q_out, table=_table(lib, p, 40), n=40, flags=flags)
+    torch.cuda.synchronize()
+    assert flags.item() == lib.FLAG_BAD_SLOT | lib.FLAG_BAD_VALUE
+    q, k, v = _exact(p)
+    s = slots.cpu().numpy()
+    check_appended(k, s, *before["k"], code_bytes(c.k), c.ks.cpu().numpy(), "e4m3", "k")
+    check_appended(np.nan_to_num(v, nan=0.0, posinf=np.inf), s, *before["v"], code_bytes(c.v),
+                   c.vs.cpu().numpy(), "e4m3", "v")
+    assert bf16_ulp_distance(bits(q_out), oracle.f64_to_bf16_bits(q)).max() <= 1
