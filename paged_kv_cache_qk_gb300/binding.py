@@ -470,13 +470,14 @@ def _ints(x, dtype, n, name):
 
 
 def _results(t, out, lse_out, rows, heads):
-    """Pointers of out [rows, heads, head_dim] and lse_out [rows, heads] (or None)."""
-    if out.dtype is not t["bf16"] or not out.is_contiguous() or out.numel() != rows * heads * 128:
+    """Pointers of out [rows, heads, head_dim] and lse_out [rows, heads] (or None); both
+    may hold more rows, which are left as they are."""
+    if out.dtype is not t["bf16"] or not out.is_contiguous() or out.numel() < rows * heads * 128:
         raise ValueError("out must be contiguous bfloat16, one value per value of q")
     if lse_out is None:
         return out.data_ptr(), 0
     if lse_out.dtype is not t["f32"] or not lse_out.is_contiguous() \
-            or lse_out.numel() != rows * heads:
+            or lse_out.numel() < rows * heads:
         raise ValueError("lse_out must be contiguous float32, one value per row and head")
     return out.data_ptr(), lse_out.data_ptr()
 

@@ -26,11 +26,17 @@
 //    takes it unrounded in fp32.
 //  * the running reference m is raised only when a score passes it by 2^4, found
 //    by a warp vote, so the usual tile has no shuffles and rescales nothing.
-// One warp per kv head; the producer warp issues one TMA box for K and one for V
-// per 16-key tile into the ring.  Scales are read by the consumer warps, one tile
-// per lane, 32 tiles ahead.
+//  * two tiles go through a warp at once, so that one's loads and conversions fill
+//    the latencies of the other's products (a tile alone takes a warp ~1050 cycles,
+//    a pair ~1850; 64 sequences of mixed lengths, 4 kv heads: 68.9 -> 59.5 us).
+// One warp per kv head at 8 heads a CTA, else two: they take the pairs in turn and
+// merge at the end of a segment through shared memory.  The producer warp issues
+// one TMA box for K and one for V per 16-key tile into the ring.  Scales are read
+// by the consumer warps, one tile per lane, 32 tiles ahead.
 #include "decode_schedule.cuh"
 #include "q8_common.cuh"
+
+#include <type_traits>
 
 namespace pkvqk {
 
@@ -48,8 +54,13 @@ struct GeometryQ8 {
   static constexpr int kStageBytes = 2 * HPC * kHeadTileBytes;
   static constexpr int kRaw = kBudgetKb * 1024 / kStageBytes;
   static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
-  static constexpr int kSmemBytes = kStages * kStageBytes + 1024;
-  static constexpr int kThreads = (HPC + 1) * 32;
+  static constexpr int kSplit = HPC == 8 ? 1 : 2;     // consumer warps per head
+  static constexpr int kConsumers = HPC * kSplit;
+  // one n-tile of a warp's result, per head: O, then (l, mu, top) of two rows a lane
+  static constexpr int kMergeBytes = kSplit > 1 ? 32 * (32 + 6) * 4 : 0;
+  static constexpr int kOffMerge = kStages * kStageBytes;
+  static constexpr int kSmemBytes = kOffMerge + HPC * kMergeBytes + 1024;
+  static constexpr int kThreads = (kConsumers + 1) * 32;
 };
 
 // ----------------------------------------------------------------- producer
@@ -164,12 +175,13 @@ __device__ __forceinline__ float2 tile_scales(const DecodeArgs& a, const ScaleVi
 
 template <int HPC, int NT, int kFormat>
 __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan* plan,
-                           const uint8_t* stages, uint64_t* full, uint64_t* empty,
-                           volatile int* abort_flag) {
+                           uint8_t* stages, uint64_t* full, uint64_t* empty, uint64_t* merge_full,
+                           uint64_t* merge_empty, volatile int* abort_flag) {
   using Geo = GeometryQ8<HPC>;
   constexpr int STAGES = Geo::kStages;
+  constexpr int kSplit = Geo::kSplit;
   const int lane = threadIdx.x & 31;
-  const int hh = threadIdx.x >> 5;
+  const int hh = (threadIdx.x >> 5) % HPC, part = (threadIdx.x >> 5) / HPC;
   const int g = lane >> 2, c = lane & 3;
   const int R = a.q_len * a.group;
   const int krow = (g >> 1) | ((g & 1) << 2);  // key row of lane group g
@@ -186,9 +198,10 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
   SegmentSource src;
   src.init(a, plan, kTK);
   Segment seg;
-  int it = 0;
+  int it0 = 0;                                 // ring position of the segment's first tile
+  uint32_t merges = 0;
   bool aborted = false;
-  while (!aborted && src.next(seg)) {
+  for (; !aborted && src.next(seg); it0 += seg.ntiles) {
     const int kvh = seg.hg * HPC + hh;
     float2 next = tile_scales(a, sv, seg, kvh, lane);
 
@@ -261,76 +274,107 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
     }
 
     float ks_l = 1.f, lv_l = 0.f, iv_l = 1.f;
-    for (int i = 0; i < seg.ntiles; ++i, ++it) {
-      if ((i & 31) == 0) {                     // the next 32 tiles' scales
-        ks_l = usable_scale(next.x);
-        const float vs = usable_scale(next.y);
-        lv_l = log2f(vs);
-        iv_l = __frcp_rn(vs);
-        next = tile_scales(a, sv, seg, kvh, i + 32 + lane);
+    // U tiles (i .. i + U - 1 of the segment) at once; false: a wait gave up
+    auto tiles = [&](auto count, int i) {
+      constexpr int U = decltype(count)::value;
+      const int it = it0 + i;
+      float ks[U], lv[U], iv[U];
+      uint32_t kt[U];                          // shared-memory address of the K tile
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        ks[u] = __shfl_sync(0xffffffffu, ks_l, (i + u) & 31);
+        lv[u] = __shfl_sync(0xffffffffu, lv_l, (i + u) & 31);
+        iv[u] = __shfl_sync(0xffffffffu, iv_l, (i + u) & 31);
       }
-      const float ks = __shfl_sync(0xffffffffu, ks_l, i & 31);
-      const float lv = __shfl_sync(0xffffffffu, lv_l, i & 31);
-      const float iv = __shfl_sync(0xffffffffu, iv_l, i & 31);
-
-      const int s = it % STAGES;
-      if (!mbar_wait(&full[s], (it / STAGES) & 1)) {
-        *abort_flag = 1;
-        report(a.status_flags, kFlagTimeout);
-        aborted = true;
-        break;
+#pragma unroll
+      for (int u = 0; u < U; ++u) {
+        const int s = (it + u) % STAGES;
+        if (!mbar_wait(&full[s], ((it + u) / STAGES) & 1)) return false;
+        kt[u] = smem_addr(stages + s * Geo::kStageBytes + hh * kHeadTileBytes);
       }
-      const uint32_t kt = smem_addr(stages + s * Geo::kStageBytes + hh * kHeadTileBytes);
-      const uint32_t vt = kt + HPC * kHeadTileBytes;
+      constexpr uint32_t kToV = HPC * kHeadTileBytes;
       const int key0 = seg.k0 + i * kTK;
 
       // slots past the sequence's end may hold anything; P' is 0 there, but an
       // e4m3 code can be NaN, so their V rows are zeroed (this warp's own)
-      if (kFormat == kFormatE4m3 && key0 + kTK > seg.seq_len) {
-        const int r0 = max(0, seg.seq_len - key0);
-        for (int e = r0 * 8 + lane; e < kTK * 8; e += 32)
-          asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(vt + e * 16), "r"(0)
-                       : "memory");
+      if (kFormat == kFormatE4m3 && key0 + U * kTK > seg.seq_len) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+          const int r0 = min(max(0, seg.seq_len - key0 - u * kTK), kTK);
+          for (int e = r0 * 8 + lane; e < kTK * 8; e += 32)
+            asm volatile("st.shared.v4.b32 [%0], {%1,%1,%1,%1};" ::"r"(kt[u] + kToV + e * 16),
+                         "r"(0)
+                         : "memory");
+        }
         __syncwarp();
         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");   // before the next TMA write
       }
 
-      // S^T (16 keys x 8 rows) = K Q^T over 8 steps of 16 dims
-      float sc[NT][4];
+      // S^T (16 keys x 8 rows) = K Q^T over 8 steps of 16 dims; with one n-tile the
+      // two halves of the dims in chains of their own
+      constexpr int kChains = NT == 1 ? 2 : 1;
+      float sc[U][NT][4];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.f;
+      for (int u = 0; u < U; ++u) {
+        float chain[kChains][NT][4];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint4 ka = lds128(kt + koff[j]), kb = lds128(kt + koff[j] + 8 * 128);
-        const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
-#pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          uint32_t a0, a1, a2, a3;
-          codes_adjacent<kFormat>(wa[w], a0, a2);
-          codes_adjacent<kFormat>(wb[w], a1, a3);
+        for (int j = 0; j < kChains; ++j)
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
-            mma_f16(sc[nt], a0, a1, a2, a3, qb[nt][j * 4 + w][0], qb[nt][j * 4 + w][1]);
+            chain[j][nt][0] = chain[j][nt][1] = chain[j][nt][2] = chain[j][nt][3] = 0.f;
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const uint4 ka = lds128(kt[u] + koff[j]), kb = lds128(kt[u] + koff[j] + 8 * 128);
+          const uint32_t wa[4] = {ka.x, ka.y, ka.z, ka.w}, wb[4] = {kb.x, kb.y, kb.z, kb.w};
+#pragma unroll
+          for (int w = 0; w < 4; ++w) {
+            uint32_t a0, a1, a2, a3;
+            codes_adjacent<kFormat>(wa[w], a0, a2);
+            codes_adjacent<kFormat>(wb[w], a1, a3);
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt)
+              mma_f16(chain[j % kChains][nt], a0, a1, a2, a3, qb[nt][j * 4 + w][0], qb[nt][j * 4 + w][1]);
+          }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[u][nt][e] = kChains == 2 ? chain[0][nt][e] + chain[kChains - 1][nt][e]
+                                        : chain[0][nt][e];
       }
 
       // x = s + log2 sv (log2 units); elements 0, 1: key krow, 2, 3: key krow + 8
       bool above = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          sc[nt][e] = fmaf(sc[nt][e], rf[nt][e & 1] * ks, lv);
-          if (key0 + kTK > lim_all && key0 + krow + (e >> 1) * 8 >= lim[nt][e & 1])
-            sc[nt][e] = -INFINITY;
-          above |= sc[nt][e] > top[nt][e & 1];
-        }
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e)
+            sc[u][nt][e] = fmaf(sc[u][nt][e], rf[nt][e & 1] * ks[u], lv[u]);
+      if (key0 + U * kTK > lim_all) {          // some row does not see all these keys
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+              if (key0 + u * kTK + krow + (e >> 1) * 8 >= lim[nt][e & 1]) sc[u][nt][e] = -INFINITY;
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) above |= sc[u][nt][e] > top[nt][e & 1];
       if (__any_sync(0xffffffffu, above)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(sc[nt][e], sc[nt][2 + e]);
+            float m = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
+            if (U == 2) m = fmaxf(m, fmaxf(sc[U - 1][nt][e], sc[U - 1][nt][2 + e]));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -348,39 +392,130 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
             }
           }
       }
-      uint32_t pb[NT][2];
+      uint32_t pb[U][NT][2];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) {
-        float p[4];
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) p[e] = exp2f(sc[nt][e] - mu[nt][e & 1]);
-        l[nt][0] = fmaf(p[0] + p[2], iv, l[nt][0]);
-        l[nt][1] = fmaf(p[1] + p[3], iv, l[nt][1]);
-        pb[nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
-        pb[nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
-      }
+        for (int nt = 0; nt < NT; ++nt) {
+          float p[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) p[e] = ex2_sfu(sc[u][nt][e] - mu[nt][e & 1]);
+          l[nt][0] = fmaf(p[0] + p[2], iv[u], l[nt][0]);
+          l[nt][1] = fmaf(p[1] + p[3], iv[u], l[nt][1]);
+          pb[u][nt][0] = transpose8x8(pack_f16x2(p[0], p[1]));
+          pb[u][nt][1] = transpose8x8(pack_f16x2(p[2], p[3]));
+        }
 
       // O^T (128 dims x 8 rows) += V^T P^T; dims 2g, 2g + 1 of a 16-dim block sit
       // in operand rows g, g + 8
 #pragma unroll
-      for (int i4 = 0; i4 < 4; ++i4) {
-        uint32_t v0, v1, v2, v3;
-        ldsm_x4_trans(vt + voff[i4], v0, v1, v2, v3);
-        uint32_t a0, a1, a2, a3;
-        codes_alternate<kFormat>(v0, a0, a1);
-        codes_alternate<kFormat>(v1, a2, a3);
+      for (int u = 0; u < U; ++u)
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma_f16(o[nt][2 * i4], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-        codes_alternate<kFormat>(v2, a0, a1);
-        codes_alternate<kFormat>(v3, a2, a3);
+        for (int i4 = 0; i4 < 4; ++i4) {
+          uint32_t v0, v1, v2, v3;
+          ldsm_x4_trans(kt[u] + kToV + voff[i4], v0, v1, v2, v3);
+          uint32_t a0, a1, a2, a3;
+          codes_alternate<kFormat>(v0, a0, a1);
+          codes_alternate<kFormat>(v1, a2, a3);
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-          mma_f16(o[nt][2 * i4 + 1], a0, a1, a2, a3, pb[nt][0], pb[nt][1]);
-      }
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(o[nt][2 * i4], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
+          codes_alternate<kFormat>(v2, a0, a1);
+          codes_alternate<kFormat>(v3, a2, a3);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+            mma_f16(o[nt][2 * i4 + 1], a0, a1, a2, a3, pb[u][nt][0], pb[u][nt][1]);
+        }
       __syncwarp();
-      if (lane == 0) mbar_arrive(&empty[s]);
+      if (lane == 0) {
+#pragma unroll
+        for (int u = 0; u < U; ++u) mbar_arrive(&empty[(it + u) % STAGES]);
+      }
+      return true;
+    };
+    int i = 0;
+    while (i < seg.ntiles && !aborted) {
+      if ((i & 31) == 0) {                     // the next 32 tiles' scales
+        ks_l = usable_scale(next.x);
+        const float vs = usable_scale(next.y);
+        lv_l = log2f(vs);
+        iv_l = __frcp_rn(vs);
+        next = tile_scales(a, sv, seg, kvh, i + 32 + lane);
+      }
+      // pairs, except with 16 rows and nine warps a CTA, which get 168 registers
+      constexpr int kAtOnce = HPC >= 4 && NT == 2 ? 1 : 2;
+      const int n = min(seg.ntiles - i, kAtOnce);
+      if (kSplit > 1 && ((i / kAtOnce) % kSplit) != part) {   // the other warp's
+        i += n;
+        continue;
+      }
+      const bool ok = n == kAtOnce ? tiles(std::integral_constant<int, kAtOnce>{}, i)
+                                   : tiles(std::integral_constant<int, 1>{}, i);
+      if (!ok) {
+        *abort_flag = 1;
+        report(a.status_flags, kFlagTimeout);
+        aborted = true;
+      }
+      i += n;
     }
 
+    // two warps of a head: the second hands its rows over, one n-tile at a time
+    if constexpr (kSplit > 1) {
+      if (aborted) break;
+      float4* mo = reinterpret_cast<float4*>(stages + Geo::kOffMerge + hh * Geo::kMergeBytes);
+      float* ml = reinterpret_cast<float*>(mo + 8 * 32);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt, ++merges) {
+        bool ok = true;
+        if (part == 1) {
+          if (merges > 0) ok = mbar_wait(&merge_empty[hh], (merges - 1) & 1);
+          if (ok) {
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt)
+              mo[mt * 32 + lane] = make_float4(o[nt][mt][0], o[nt][mt][1], o[nt][mt][2], o[nt][mt][3]);
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              ml[(3 * e) * 32 + lane] = l[nt][e];
+              ml[(3 * e + 1) * 32 + lane] = mu[nt][e];
+              ml[(3 * e + 2) * 32 + lane] = top[nt][e];
+            }
+          }
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&merge_full[hh]);
+        } else {
+          ok = mbar_wait(&merge_full[hh], merges & 1);
+          if (ok) {
+            float w[2][2];                     // [row][this warp, the other]
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+              const float mu1 = ml[(3 * e + 1) * 32 + lane];
+              const bool has0 = top[nt][e] != -INFINITY, has1 = ml[(3 * e + 2) * 32 + lane] != -INFINITY;
+              const float m = has0 ? (has1 ? fmaxf(mu[nt][e], mu1) : mu[nt][e]) : mu1;
+              w[e][0] = has0 ? exp2f(mu[nt][e] - m) : 0.f;
+              w[e][1] = has1 ? exp2f(mu1 - m) : 0.f;
+              l[nt][e] = l[nt][e] * w[e][0] + ml[(3 * e) * 32 + lane] * w[e][1];
+              mu[nt][e] = m;
+            }
+#pragma unroll
+            for (int mt = 0; mt < 8; ++mt) {
+              const float4 x = mo[mt * 32 + lane];
+              o[nt][mt][0] = o[nt][mt][0] * w[0][0] + x.x * w[0][1];
+              o[nt][mt][1] = o[nt][mt][1] * w[1][0] + x.y * w[1][1];
+              o[nt][mt][2] = o[nt][mt][2] * w[0][0] + x.z * w[0][1];
+              o[nt][mt][3] = o[nt][mt][3] * w[1][0] + x.w * w[1][1];
+            }
+          }
+          __syncwarp();
+          if (lane == 0 && ok) mbar_arrive(&merge_empty[hh]);
+        }
+        if (!ok) {
+          *abort_flag = 1;
+          report(a.status_flags, kFlagTimeout);
+          aborted = true;
+        }
+      }
+      if (aborted || part == 1) continue;
+    }
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -458,19 +593,25 @@ paged_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
   __shared__ int issued;
   __shared__ Plan plan;
   __shared__ long long wsum[32];
+  __shared__ uint64_t merge_full[HPC], merge_empty[HPC];
+  constexpr int kProducer = Geo::kConsumers;   // warp index of the producer
   uint8_t* stages = align1024(smem_raw);
 
   const int warp = threadIdx.x >> 5;
   if (threadIdx.x == 0) {
     for (int s = 0; s < STAGES; ++s) {
       mbar_init(&full[s], 1);
-      mbar_init(&empty[s], HPC);
+      mbar_init(&empty[s], HPC);               // one warp of each head reads a stage
+    }
+    for (int h = 0; h < HPC; ++h) {
+      mbar_init(&merge_full[h], 1);
+      mbar_init(&merge_empty[h], 1);
     }
     abort_flag = 0;
     issued = 0;
     fence_barrier_init();
   }
-  if (warp == HPC) prefetch_before_wait_q8<HPC>(&kmap, &vmap, a);
+  if (warp == kProducer) prefetch_before_wait_q8<HPC>(&kmap, &vmap, a);
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
@@ -479,12 +620,13 @@ paged_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
     make_plan(a, &plan, wsum);
     write_empty_units(a, HPC);
   }
-  if (warp == HPC)
+  if (warp == kProducer)
     produce_q8<HPC>(&kmap, &vmap, a, &plan, stages, full, empty, &abort_flag, &issued);
   else
-    consume_q8<HPC, NT, kFormat>(a, sv, &plan, stages, full, empty, &abort_flag);
+    consume_q8<HPC, NT, kFormat>(a, sv, &plan, stages, full, empty, merge_full, merge_empty,
+                                 &abort_flag);
   __syncthreads();
-  if (abort_flag && threadIdx.x == HPC * 32) drain<STAGES>(full, issued);
+  if (abort_flag && threadIdx.x == kProducer * 32) drain<STAGES>(full, issued);
 }
 
 template <int HPC, int NT, int kFormat>

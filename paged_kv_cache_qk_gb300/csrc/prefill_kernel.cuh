@@ -115,7 +115,7 @@ struct Bars {
   uint64_t q_full[2];                            // Q tile x landed (TMA)
   uint64_t o_staged[2];                          // tile x's output rows staged for TMA
   uint64_t scales_full[kScaleSlots];             // 8-bit: a tile's scales are in shared memory
-  uint64_t raw_k_full, raw_k_empty;              // 8-bit: K codes landed / read
+  uint64_t raw_k_full, raw_k_empty, raw_k1_full; // 8-bit: K codes landed / read
   uint64_t raw_v_full[kStages];                  // 8-bit: V codes landed
   uint32_t tmem_base;
   int32_t abort;
@@ -424,15 +424,22 @@ __device__ __forceinline__ void convert_group(const uint8_t* raw, uint8_t* stage
   __syncwarp();
 }
 
-// K (tile A's warps) and V (tile B's) of key tile i; false: a wait gave up.
-template <int kFormat>
+// K (tile A's warps) and V (tile B's) of key tile i; false: a wait gave up.  K(1) is
+// there from the start, in its stage as V is (the staging tile holds K(0) then):
+// the staging tile's use u is K(0), K(2), K(3) ..
+__device__ __forceinline__ int staging_use(int i) { return i == 0 ? 0 : i - 1; }
+
+template <int kFormat, bool kStaged = true>
 __device__ __forceinline__ bool convert_k(const Work& w, uint8_t* smem, Bars* bars, int i) {
   const int s = i & 1, g = (threadIdx.x >> 5) & 7;
+  uint8_t* stage = smem + kOffK + s * kTile;
   if (i >= 2 && !warp_wait(&bars->empty_k[s], ((i >> 1) - 1) & 1)) return false;
-  if (!warp_wait(&bars->raw_k_full, i & 1)) return false;
-  convert_group<kFormat>(smem + kOffRaw, smem + kOffK + s * kTile, g,
+  if (!warp_wait(kStaged ? &bars->raw_k_full : &bars->raw_k1_full,
+                 kStaged ? staging_use(i) & 1 : 0))
+    return false;
+  convert_group<kFormat>(kStaged ? smem + kOffRaw : stage, stage, g,
                          w.key_end - (w.k0 + i * kN + g * kScaleGroup), [&] {
-                           if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->raw_k_empty);
+                           if (kStaged && (threadIdx.x & 31) == 0) mbar_arrive(&bars->raw_k_empty);
                          });
   if ((threadIdx.x & 31) == 0) mbar_arrive(&bars->full_k[s]);
   return true;
@@ -480,39 +487,53 @@ __device__ __forceinline__ void tma_load_4d_keep(void* dst, const CUtensorMap* m
 
 // The producer warp over an 8-bit cache: codes and scales of every key tile, lane
 // l the tile's group l % 8 (block ids read one tile ahead).  K runs a tile ahead
-// of V -- K(0) V(0) K(1) K(2) V(1) K(3) V(2) .. -- so that it does not wait behind
-// V for a stage that only PV_B frees.
-__device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMap* kmap,
-                           const CUtensorMap* vmap, uint8_t* smem, Bars* bars) {
-  const int lane = threadIdx.x & 31, gl = lane & (kGroupsPerTile - 1);
-  const int tb = 1 << box_shift(a.block_size);
-  const bool issues = lane < kGroupsPerTile && (lane * kScaleGroup) % tb == 0;   // one box each
-  const int32_t* bt = a.block_tables + static_cast<long long>(w.b) * a.max_blocks_per_seq;
-  float4* scales = reinterpret_cast<float4*>(smem + kOffScales);
-  auto block_id = [&](int i, int* slot) {
-    const int key = w.k0 + i * kN + gl * kScaleGroup;
-    *slot = 0;
-    return i < w.ntiles && key < w.key_end ? __ldg(bt + group_page(a, key, slot)) : -1;
-  };
-  auto send_v = [&](int i, int slot, int c3) {
+// of V -- K(0) V(0) K(1) before the CTA's roles begin, then K(2) V(1) K(3) V(2) .. --
+// so that it does not wait behind V for a stage that only PV_B frees.
+struct ProducerQ8 {
+  const PrefillArgs& a;
+  const Work& w;
+  const CUtensorMap* kmap;
+  const CUtensorMap* vmap;
+  uint8_t* smem;
+  Bars* bars;
+  int lane, id, slot;                          // block id and slot of the next tile's group
+  int v_slot, v_c3;                            // of the tile whose V is due
+  int k_sent, v_sent;
+
+  __device__ __forceinline__ int group_key(int i) const {
+    return w.k0 + i * kN + (lane & (kGroupsPerTile - 1)) * kScaleGroup;
+  }
+  __device__ __forceinline__ void look_up(int i) {
+    const int key = group_key(i);
+    id = -1;
+    slot = 0;
+    if (i < w.ntiles && key < w.key_end) {
+      const int page = group_page(a, key, &slot);
+      id = __ldg(a.block_tables + static_cast<long long>(w.b) * a.max_blocks_per_seq + page);
+    }
+  }
+  // one box per lane that starts one
+  __device__ __forceinline__ void send(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int at,
+                                       int c3) {
+    if (lane == 0) mbar_arrive_expect_tx(bar, kRawBytes);
+    __syncwarp();
+    const int tb = 1 << box_shift(a.block_size);
+    if (lane < kGroupsPerTile && (lane * kScaleGroup) % tb == 0)
+      tma_load_4d_keep(dst + lane * kScaleGroup * kHeadDim, map, bar, at, w.g, c3);
+  }
+  __device__ __forceinline__ bool send_v(int i) {
     const int s = i & 1;
     if (i >= 2 && !warp_wait(&bars->empty_v[s], ((i >> 1) - 1) & 1)) return false;   // PV(i - 2)
-    if (lane == 0) mbar_arrive_expect_tx(&bars->raw_v_full[s], kRawBytes);
-    __syncwarp();
-    if (issues)
-      tma_load_4d_keep(smem + kOffV + s * kTile + lane * kScaleGroup * kHeadDim, vmap,
-                       &bars->raw_v_full[s], slot, w.g, c3);
+    send(smem + kOffV + s * kTile, vmap, &bars->raw_v_full[s], v_slot, v_c3);
+    v_sent = i + 1;
     return true;
-  };
-  int slot, k_sent = 0, v_sent = 0;
-  int id = block_id(0, &slot);
-  int v_slot = 0, v_c3 = 0;                    // of tile i - 1
-  bool ok = true;
-  for (int i = 0; i < w.ntiles; ++i) {
+  }
+  // K(i) and the tile's scales; leaves its slot and block for V
+  __device__ __forceinline__ bool send_k(int i) {
     const bool good = id >= 0 && static_cast<long long>(id) < a.num_blocks;
-    if (!good && w.k0 + i * kN + gl * kScaleGroup < w.key_end)
-      report(a.status_flags, kFlagBadBlock);
+    if (!good && group_key(i) < w.key_end) report(a.status_flags, kFlagBadBlock);
     const int c3 = good ? id : static_cast<int>(a.num_blocks);   // past the extent: zeros
+    const int at = slot;
     float ks = 1.f, vs = 1.f;
     if (good) {
       const long long so = id * a.scales.block_stride +
@@ -521,49 +542,65 @@ __device__ void produce_q8(const PrefillArgs& a, const Work& w, const CUtensorMa
       ks = __ldg(a.scales.k + so);
       vs = __ldg(a.scales.v + so);
     }
-    ok = i == 0 || warp_wait(&bars->raw_k_empty, (i - 1) & 1);
-    if (!ok) break;
-    if (lane == 0) mbar_arrive_expect_tx(&bars->raw_k_full, kRawBytes);
-    __syncwarp();
-    if (issues)
-      tma_load_4d_keep(smem + kOffRaw + lane * kScaleGroup * kHeadDim, kmap, &bars->raw_k_full,
-                       slot, w.g, c3);
+    if (i == 1) {
+      send(smem + kOffK + kTile, kmap, &bars->raw_k1_full, at, c3);
+    } else {
+      if (i >= 2 && !warp_wait(&bars->raw_k_empty, (staging_use(i) - 1) & 1)) return false;
+      send(smem + kOffRaw, kmap, &bars->raw_k_full, at, c3);
+    }
     k_sent = i + 1;
-    const int k_slot = slot;
-    id = block_id(i + 1, &slot);
+    look_up(i + 1);
     // Slot i % 4 was last read for tile i - 4.  K(i - 1) has been read: tile A's
     // warps do so after their P(i - 3) and after S_B(i - 3), which was issued after
     // P_B(i - 4).
     ks = usable_scale(ks);
     vs = usable_scale(vs);
+    const int ring = i & (kScaleSlots - 1);
     if (lane < kGroupsPerTile)
-      scales[(i & (kScaleSlots - 1)) * kGroupsPerTile + lane] =
+      reinterpret_cast<float4*>(smem + kOffScales)[ring * kGroupsPerTile + lane] =
           make_float4(ks, log2f(vs), __frcp_rn(vs), 0.f);
     __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->scales_full[i & (kScaleSlots - 1)]);
-    if (i != 1) {
-      const int j = i == 0 ? 0 : i - 1;
-      ok = send_v(j, i == 0 ? k_slot : v_slot, i == 0 ? c3 : v_c3);
-      if (!ok) break;
-      v_sent = j + 1;
-    }
-    v_slot = k_slot;
+    if (lane == 0) mbar_arrive(&bars->scales_full[ring]);
+    v_slot = at;
     v_c3 = c3;
+    return true;
   }
-  if (ok && w.ntiles > 1) {
-    ok = send_v(w.ntiles - 1, v_slot, v_c3);
-    if (ok) v_sent = w.ntiles;
+
+  __device__ __forceinline__ void begin() {
+    lane = threadIdx.x & 31;
+    k_sent = v_sent = 0;
+    look_up(0);
+    if (w.ntiles == 0) return;
+    send_k(0);
+    send_v(0);
+    if (w.ntiles > 1) send_k(1);
   }
-  if (!ok && lane == 0) {
-    bars->abort = 1;
-    report(a.status_flags, kFlagTimeout);
-    // the copies in flight land before the CTA leaves
-    if (k_sent > 0) mbar_wait(&bars->raw_k_full, (k_sent - 1) & 1);
-    for (int i = v_sent < 2 ? 0 : v_sent - 2; i < v_sent; ++i)
-      mbar_wait(&bars->raw_v_full[i & 1], (i >> 1) & 1);
+  __device__ __forceinline__ void rest() {
+    const int n = w.ntiles;
+    bool ok = true;
+    for (int i = 2; i < n && ok; ++i) {
+      const int s = v_slot, c3 = v_c3;         // tile i - 1's
+      ok = send_k(i);
+      const int ks = v_slot, kc3 = v_c3;
+      v_slot = s;
+      v_c3 = c3;
+      ok = ok && send_v(i - 1);
+      v_slot = ks;
+      v_c3 = kc3;
+    }
+    if (ok && n > 1) ok = send_v(n - 1);
+    if (!ok && lane == 0) {
+      bars->abort = 1;
+      report(a.status_flags, kFlagTimeout);
+      // the copies in flight land before the CTA leaves
+      if (k_sent > 1) mbar_wait(&bars->raw_k1_full, 0);
+      if (k_sent != 0) mbar_wait(&bars->raw_k_full, staging_use(k_sent == 2 ? 0 : k_sent - 1) & 1);
+      for (int i = v_sent < 2 ? 0 : v_sent - 2; i < v_sent; ++i)
+        mbar_wait(&bars->raw_v_full[i & 1], (i >> 1) & 1);
+    }
+    __syncwarp();
   }
-  __syncwarp();
-}
+};
 
 // Q rows as f16 in both tiles' shared memory, before the warps take their roles:
 // thread i brings 64 dims (half i / 256) of row i % 256, scaled by the power of
@@ -578,20 +615,20 @@ __device__ __forceinline__ void q_rows_to_f16(const PrefillArgs& a, const Work& 
   const uint4* src = reinterpret_cast<const uint4*>(
       a.q + (live ? w.q0 + t : 0) * a.q_stride_t +
       static_cast<long long>(w.g * a.group + (live ? rg - t * a.group : 0)) * a.q_stride_h);
-  uint4 v[8];
+  uint4 v[8], other[8];
+#pragma unroll
+  for (int c = 0; c < 8; ++c) {
+    v[c] = live ? __ldg(src + dh * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
+    other[c] = live ? __ldg(src + (dh ^ 1) * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
+  }
   float amax = 0.f;
 #pragma unroll
-  for (int h = 0; h < 2; ++h) {                // the other half first
+  for (int c = 0; c < 8; ++c) {
+    float f[8], g[8];
+    unpack8(v[c], f);
+    unpack8(other[c], g);
 #pragma unroll
-    for (int c = 0; c < 8; ++c)
-      v[c] = live ? __ldg(src + (dh ^ h ^ 1) * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll
-    for (int c = 0; c < 8; ++c) {
-      float f[8];
-      unpack8(v[c], f);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-    }
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(f[e]), fabsf(g[e])));
   }
   float inverse;
   const float up = q_row_scale(amax, inverse);
@@ -740,28 +777,39 @@ __device__ __forceinline__ float pow2_int(float d) {
   return d < -126.f ? 0.f : __int_as_float((127 + static_cast<int>(d)) << 23);
 }
 
-// Multiply the bf16 pairs in kWords columns at taddr by the power of two f
-// (exact unless a value drops below the normal range).
+// Multiply the P pairs in kWords columns at taddr by the power of two f (exact
+// unless a value drops below the normal range).  8-bit: eight columns at a time,
+// as the scores of a chunk are in registers meanwhile.
 template <int kFormat, int kWords>
 __device__ __forceinline__ void scale_p(uint32_t taddr, float f) {
   tc5::wait_st();                              // this thread's P stores to these columns
-  float w[32];
-  if (kWords == 16) tc5::tmem_ld16(taddr, w);
-  else tc5::tmem_ld32(taddr, w);
-  tc5::wait_ld();
-  uint32_t p[kWords];
+  if constexpr (kFormat == 0) {
+    float w[32];
+    if (kWords == 16) tc5::tmem_ld16(taddr, w);
+    else tc5::tmem_ld32(taddr, w);
+    tc5::wait_ld();
+    uint32_t p[kWords];
 #pragma unroll
-  for (int j = 0; j < kWords; ++j) {
-    const uint32_t u = __float_as_uint(w[j]);
-    if (kFormat == 0) {
+    for (int j = 0; j < kWords; ++j) {
+      const uint32_t u = __float_as_uint(w[j]);
       p[j] = pack_bf16x2(bf16lo(u) * f, bf16hi(u) * f);
-    } else {
-      const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&u));
-      p[j] = pack_f16x2(q.x * f, q.y * f);
+    }
+    if (kWords == 16) tc5::tmem_st16(taddr, p);
+    else tc5::tmem_st32u(taddr, p);
+  } else {
+#pragma unroll 1
+    for (int c = 0; c < kWords; c += 8) {
+      uint32_t p[8];
+      tc5::tmem_ld8(taddr + c, p);
+      tc5::wait_ld();
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float2 q = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
+        p[j] = pack_f16x2(q.x * f, q.y * f);
+      }
+      tc5::tmem_st8(taddr + c, p);
     }
   }
-  if (kWords == 16) tc5::tmem_st16(taddr, p);
-  else tc5::tmem_st32u(taddr, p);
 }
 
 // This thread's 64 keys of one key tile: S from scol (two 32-column chunks),
@@ -821,33 +869,47 @@ __device__ __forceinline__ float half_tile(uint32_t scol, uint32_t pcol, int kba
     }
     if (c == 1) publish(m_ref);
     const float u = (m_ref == -INFINITY) ? 0.f : m_ref;
-    const float f0 = kFormat == 0 ? sl2 : sl2 * g0.x, f1 = kFormat == 0 ? sl2 : sl2 * g1.x;
-    const float h0 = kFormat == 0 ? -u : g0.y - u, h1 = kFormat == 0 ? -u : g1.y - u;
-    const uint64_t scale2[2] = {pack2(f0, f0), pack2(f1, f1)};
-    const uint64_t shift2[2] = {pack2(h0, h0), pack2(h1, h1)};
-    uint64_t acc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = pack2(0.f, 0.f);
-    uint32_t pk[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      float x0, x1;
-      unpack2(fma2(pack2(v[2 * q], v[2 * q + 1]), scale2[q >> 3], shift2[q >> 3]), x0, x1);
-      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);   // masked: 2^-inf = 0
-      const int j = kFormat == 0 ? q & 3 : ((q >> 3) << 1) | (q & 1);
-      acc[j] = add2(acc[j], pack2(p0, p1));
-      pk[q] = kFormat == 0 ? pack_bf16x2(p0, p1) : pack_f16x2(p0, p1);
-    }
-    tc5::tmem_st16(pcol + c * 16, pk);
-    float t0, t1;
     if (kFormat == 0) {
-      unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), t0, t1);
+      const uint64_t scale2 = pack2(sl2, sl2), shift2 = pack2(-u, -u);
+      uint64_t acc[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] = pack2(0.f, 0.f);
+      uint32_t pk[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        float x0, x1;
+        unpack2(fma2(pack2(v[2 * q], v[2 * q + 1]), scale2, shift2), x0, x1);
+        const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);   // masked: 2^-inf = 0
+        acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
+        pk[q] = pack_bf16x2(p0, p1);
+      }
+      tc5::tmem_st16(pcol + c * 16, pk);
+      const uint64_t t = add2(add2(acc[0], acc[1]), add2(acc[2], acc[3]));
+      float t0, t1;
+      unpack2(t, t0, t1);
       psum += t0 + t1;
     } else {
-      unpack2(add2(acc[0], acc[1]), t0, t1);
-      psum = fmaf(t0 + t1, g0.z, psum);
-      unpack2(add2(acc[2], acc[3]), t0, t1);
-      psum = fmaf(t0 + t1, g1.z, psum);
+      // one scale group at a time: fewer registers at once
+#pragma unroll
+      for (int gr = 0; gr < 2; ++gr) {
+        const float4 g = gr == 0 ? g0 : g1;
+        const float f = sl2 * g.x, h = g.y - u;
+        const uint64_t scale2 = pack2(f, f), shift2 = pack2(h, h);
+        uint64_t acc[2] = {pack2(0.f, 0.f), pack2(0.f, 0.f)};
+        uint32_t pk[8];
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          float x0, x1;
+          unpack2(fma2(pack2(v[16 * gr + 2 * q], v[16 * gr + 2 * q + 1]), scale2, shift2), x0, x1);
+          const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
+          acc[q & 1] = add2(acc[q & 1], pack2(p0, p1));
+          pk[q] = pack_f16x2(p0, p1);
+        }
+        tc5::tmem_st8(pcol + c * 16 + gr * 8, pk);
+        float t0, t1;
+        unpack2(add2(acc[0], acc[1]), t0, t1);
+        psum = fmaf(t0 + t1, g.z, psum);
+      }
     }
   }
   return psum;
@@ -1033,7 +1095,7 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
   float l = 0.f;                               // this half's sum of P
   if (kFormat != 0 && n > 0) {                 // the first K tiles, the first V tile
     ok = x == 0 ? convert_k<kFormat>(w, smem, bars, 0) : convert_v<kFormat>(w, smem, bars, 0);
-    if (x == 0 && n > 1) ok = ok && convert_k<kFormat>(w, smem, bars, 1);
+    if (x == 0 && n > 1) ok = ok && convert_k<kFormat, false>(w, smem, bars, 1);
   }
   for (int i = 0; i < n && ok; ++i) {
     // 8-bit: this half's four groups of scales
@@ -1151,6 +1213,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   uint8_t* smem = align1024(smem_raw);
   Bars* bars = reinterpret_cast<Bars*>(smem + kDataBytes);
   __shared__ int issued;
+  __shared__ Work shared_work;
   const int warp = threadIdx.x >> 5;
 
   // launched as a programmatic dependent: q, the appended K/V, the tables and
@@ -1184,11 +1247,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     if (kFormat != 0) {
       for (int s = 0; s < kScaleSlots; ++s) mbar_init(&bars->scales_full[s], 1);
       mbar_init(&bars->raw_k_full, 1);
+      mbar_init(&bars->raw_k1_full, 1);
       mbar_init(&bars->raw_k_empty, kSoftmaxWarps / 2);
       for (int s = 0; s < kStages; ++s) mbar_init(&bars->raw_v_full[s], 1);
     }
     bars->abort = 0;
     issued = 0;
+    if (kFormat != 0) shared_work = w;
     fence_barrier_init();
     // Q by TMA: one box per (row tile, 64-dim half), rows past q or
     // before it read as zeros, rows of a following sequence are masked
@@ -1201,6 +1266,11 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         tma_load_rows(smem + kOffQ + dh * kHalf, &qmap, &bars->q_full[0], dh * 64,
                       w.g * a.group, tok);
     }
+  }
+  ProducerQ8 producer{a, w, &kmap, &vmap, smem, bars};
+  if (kFormat != 0 && warp == kProducerWarp) {
+    __syncwarp();                              // the barriers are set up
+    producer.begin();
   }
   if (warp == kMmaWarp) tc5::tmem_alloc(&bars->tmem_base, kTmemCols);
 
@@ -1237,8 +1307,9 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     // warp = 8 x + 4 half + lane quadrant
     const int x = warp >> 3, half = (warp >> 2) & 1;
     if (x == 0 || w.has_b)
-      softmax_rows<kFormat>(a, w, smem, bars, &omap, reinterpret_cast<float*>(smem + kOffSlots),
-                            tmem, x, half);
+      // 8-bit: the work's fields stay in shared memory, for the registers' sake
+      softmax_rows<kFormat>(a, kFormat == 0 ? w : shared_work, smem, bars, &omap,
+                            reinterpret_cast<float*>(smem + kOffSlots), tmem, x, half);
     else if (kFormat != 0)                     // no tile B: V is all its warps do
       convert_all_v<kFormat>(a, w, smem, bars);
   } else if (warp == kProducerWarp) {
@@ -1255,7 +1326,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
         }
       }
     } else {
-      produce_q8(a, w, &kmap, &vmap, smem, bars);
+      producer.rest();
     }
   } else {
     if ((threadIdx.x & 31) == 0) issue_mmas<kFormat>(a, w, smem, bars, tmem);

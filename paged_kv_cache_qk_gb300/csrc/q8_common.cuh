@@ -34,6 +34,14 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
   return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// 2^x on the SFU (relative error ~2^-22; -inf -> +0): what it gives is rounded to
+// f16 or summed.
+__device__ __forceinline__ float ex2_sfu(float x) {
+  float y;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+  return y;
+}
+
 // Bytes (0, 1) -> lo, bytes (2, 3) -> hi.
 template <int kFormat>
 __device__ __forceinline__ void codes_adjacent(uint32_t w, uint32_t& lo, uint32_t& hi) {
