@@ -603,45 +603,43 @@ struct ProducerQ8 {
 };
 
 // Q rows as f16 in both tiles' shared memory, before the warps take their roles:
-// thread i brings 64 dims (half i / 256) of row i % 256, scaled by the power of
-// two of its row's largest magnitude (so it reads the other half too); the
-// inverse goes to the row's slot.
+// half-warp h of the sixteen softmax warps' 32 brings rows h, h + 32, .. (16 bytes a
+// lane, all eight loads in flight), each scaled by the power of two of its largest
+// magnitude; the inverse goes to the row's slot.  (One thread a half row, 16-byte
+// loads 32 rows apart, took 18,000 cycles a CTA.)
 __device__ __forceinline__ void q_rows_to_f16(const PrefillArgs& a, const Work& w,
                                               uint8_t* smem) {
-  const int row = threadIdx.x % (2 * kM), dh = threadIdx.x / (2 * kM);
-  const int rg = w.mt * 2 * kM + row;
-  const int t = div_group(a, rg);
-  const bool live = rg < w.rows && w.q0 + t >= 0 && w.q0 + t < a.total_q;
-  const uint4* src = reinterpret_cast<const uint4*>(
-      a.q + (live ? w.q0 + t : 0) * a.q_stride_t +
-      static_cast<long long>(w.g * a.group + (live ? rg - t * a.group : 0)) * a.q_stride_h);
-  uint4 v[8], other[8];
+  constexpr int kEach = 2 * kM / (2 * kSoftmaxWarps);
+  const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
+  uint4 v[kEach];
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    v[c] = live ? __ldg(src + dh * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
-    other[c] = live ? __ldg(src + (dh ^ 1) * 8 + c) : make_uint4(0u, 0u, 0u, 0u);
+  for (int i = 0; i < kEach; ++i) {
+    const int rg = w.mt * 2 * kM + i * 2 * kSoftmaxWarps + hw;
+    const int t = div_group(a, rg);
+    const bool live = rg < w.rows && w.q0 + t >= 0 && w.q0 + t < a.total_q;
+    v[i] = live ? __ldg(reinterpret_cast<const uint4*>(
+                            a.q + (w.q0 + t) * a.q_stride_t +
+                            static_cast<long long>(w.g * a.group + rg - t * a.group) *
+                                a.q_stride_h) + l)
+                : make_uint4(0u, 0u, 0u, 0u);
   }
-  float amax = 0.f;
 #pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float f[8], g[8];
-    unpack8(v[c], f);
-    unpack8(other[c], g);
+  for (int i = 0; i < kEach; ++i) {
+    const int row = i * 2 * kSoftmaxWarps + hw;
+    float f[8], amax = 0.f;
+    unpack8(v[i], f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fmaxf(fabsf(f[e]), fabsf(g[e])));
-  }
-  float inverse;
-  const float up = q_row_scale(amax, inverse);
-  uint8_t* dst = smem + kOffQ + (row / kM) * kTile + dh * kHalf;
-#pragma unroll
-  for (int c = 0; c < 8; ++c) {
-    float f[8];
-    unpack8(v[c], f);
-    *reinterpret_cast<uint4*>(dst + swz128(row % kM, c)) =
+    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
+    amax = __uint_as_float(
+        __reduce_max_sync(0xffffu << (threadIdx.x & 16), __float_as_uint(amax)));
+    float inverse;
+    const float up = q_row_scale(amax, inverse);
+    *reinterpret_cast<uint4*>(smem + kOffQ + (row / kM) * kTile + (l >> 3) * kHalf +
+                              swz128(row % kM, l & 7)) =
         make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
                    pack_f16x2(f[4] * up, f[5] * up), pack_f16x2(f[6] * up, f[7] * up));
+    if (l == 0) reinterpret_cast<float*>(smem + kOffRowScale)[row] = inverse;
   }
-  if (dh == 0) reinterpret_cast<float*>(smem + kOffRowScale)[row] = inverse;
   tc5::fence_smem_for_async();
 }
 
