@@ -496,99 +496,123 @@ struct ProducerQ8 {
   const CUtensorMap* vmap;
   uint8_t* smem;
   Bars* bars;
-  int lane, id, slot;                          // block id and slot of the next tile's group
+  int lane;
+  // A tile on its way: where its codes are, and its scales.
+  struct Tile {
+    int id, slot;                              // block (-1: not looked up), slot in it
+    float ks, vs;
+  };
+  Tile next;                                   // looked up, not yet sent
   int v_slot, v_c3;                            // of the tile whose V is due
+  float ks0, vs0, ks1, vs1;                    // scales of tiles 0 and 1 until rest()
   int k_sent, v_sent;
 
   __device__ __forceinline__ int group_key(int i) const {
     return w.k0 + i * kN + (lane & (kGroupsPerTile - 1)) * kScaleGroup;
   }
-  __device__ __forceinline__ void look_up(int i) {
+  __device__ __forceinline__ void look_up(int i, Tile& t) const {
     const int key = group_key(i);
-    id = -1;
-    slot = 0;
+    t.id = -1;
+    t.slot = 0;
     if (i < w.ntiles && key < w.key_end) {
-      const int page = group_page(a, key, &slot);
-      id = __ldg(a.block_tables + static_cast<long long>(w.b) * a.max_blocks_per_seq + page);
+      const int page = group_page(a, key, &t.slot);
+      t.id = __ldg(a.block_tables + static_cast<long long>(w.b) * a.max_blocks_per_seq + page);
     }
+  }
+  __device__ __forceinline__ bool good(const Tile& t) const {
+    return t.id >= 0 && static_cast<long long>(t.id) < a.num_blocks;
+  }
+  __device__ __forceinline__ int block_of(const Tile& t) const {   // past the extent: zeros
+    return good(t) ? t.id : static_cast<int>(a.num_blocks);
+  }
+  __device__ __forceinline__ void load_scales(int i, Tile& t) const {
+    t.ks = t.vs = 1.f;
+    if (good(t)) {
+      const long long so = t.id * a.scales.block_stride +
+                           (t.slot / kScaleGroup) * a.scales.group_stride +
+                           w.g * a.scales.head_stride;
+      t.ks = __ldg(a.scales.k + so);
+      t.vs = __ldg(a.scales.v + so);
+    } else if (group_key(i) < w.key_end) {
+      report(a.status_flags, kFlagBadBlock);
+    }
+  }
+  __device__ __forceinline__ void put_scales(int i, float ks, float vs) const {
+    const int ring = i & (kScaleSlots - 1);
+    ks = usable_scale(ks);
+    vs = usable_scale(vs);
+    if (lane < kGroupsPerTile)
+      reinterpret_cast<float4*>(smem + kOffScales)[ring * kGroupsPerTile + lane] =
+          make_float4(ks, log2f(vs), __frcp_rn(vs), 0.f);
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&bars->scales_full[ring]);
   }
   // one box per lane that starts one
   __device__ __forceinline__ void send(uint8_t* dst, const CUtensorMap* map, uint64_t* bar, int at,
-                                       int c3) {
+                                       int c3) const {
     if (lane == 0) mbar_arrive_expect_tx(bar, kRawBytes);
     __syncwarp();
     const int tb = 1 << box_shift(a.block_size);
     if (lane < kGroupsPerTile && (lane * kScaleGroup) % tb == 0)
       tma_load_4d_keep(dst + lane * kScaleGroup * kHeadDim, map, bar, at, w.g, c3);
   }
-  __device__ __forceinline__ bool send_v(int i) {
+  __device__ __forceinline__ bool send_v(int i, int at, int c3) {
     const int s = i & 1;
     if (i >= 2 && !warp_wait(&bars->empty_v[s], ((i >> 1) - 1) & 1)) return false;   // PV(i - 2)
-    send(smem + kOffV + s * kTile, vmap, &bars->raw_v_full[s], v_slot, v_c3);
+    send(smem + kOffV + s * kTile, vmap, &bars->raw_v_full[s], at, c3);
     v_sent = i + 1;
     return true;
   }
-  // K(i) and the tile's scales; leaves its slot and block for V
-  __device__ __forceinline__ bool send_k(int i) {
-    const bool good = id >= 0 && static_cast<long long>(id) < a.num_blocks;
-    if (!good && group_key(i) < w.key_end) report(a.status_flags, kFlagBadBlock);
-    const int c3 = good ? id : static_cast<int>(a.num_blocks);   // past the extent: zeros
-    const int at = slot;
-    float ks = 1.f, vs = 1.f;
-    if (good) {
-      const long long so = id * a.scales.block_stride +
-                           (slot / kScaleGroup) * a.scales.group_stride +
-                           w.g * a.scales.head_stride;
-      ks = __ldg(a.scales.k + so);
-      vs = __ldg(a.scales.v + so);
-    }
-    if (i == 1) {
-      send(smem + kOffK + kTile, kmap, &bars->raw_k1_full, at, c3);
-    } else {
-      if (i >= 2 && !warp_wait(&bars->raw_k_empty, (staging_use(i) - 1) & 1)) return false;
-      send(smem + kOffRaw, kmap, &bars->raw_k_full, at, c3);
-    }
-    k_sent = i + 1;
-    look_up(i + 1);
-    // Slot i % 4 was last read for tile i - 4.  K(i - 1) has been read: tile A's
-    // warps do so after their P(i - 3) and after S_B(i - 3), which was issued after
-    // P_B(i - 4).
-    ks = usable_scale(ks);
-    vs = usable_scale(vs);
-    const int ring = i & (kScaleSlots - 1);
-    if (lane < kGroupsPerTile)
-      reinterpret_cast<float4*>(smem + kOffScales)[ring * kGroupsPerTile + lane] =
-          make_float4(ks, log2f(vs), __frcp_rn(vs), 0.f);
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&bars->scales_full[ring]);
-    v_slot = at;
-    v_c3 = c3;
-    return true;
-  }
 
+  // Before the CTA's roles begin: K(0) V(0) K(1) on their way, the scales of tiles 0
+  // and 1 asked for.
   __device__ __forceinline__ void begin() {
     lane = threadIdx.x & 31;
     k_sent = v_sent = 0;
-    look_up(0);
     if (w.ntiles == 0) return;
-    send_k(0);
-    send_v(0);
-    if (w.ntiles > 1) send_k(1);
+    Tile first;
+    look_up(0, first);
+    look_up(1, next);
+    send(smem + kOffRaw, kmap, &bars->raw_k_full, first.slot, block_of(first));
+    send_v(0, first.slot, block_of(first));
+    k_sent = 1;
+    if (w.ntiles > 1) {
+      send(smem + kOffK + kTile, kmap, &bars->raw_k1_full, next.slot, block_of(next));
+      k_sent = 2;
+    }
+    v_slot = next.slot;
+    v_c3 = block_of(next);
+    load_scales(0, first);
+    if (w.ntiles > 1) load_scales(1, next);
+    ks0 = first.ks;
+    vs0 = first.vs;
+    ks1 = next.ks;
+    vs1 = next.vs;
+    look_up(2, next);
   }
   __device__ __forceinline__ void rest() {
     const int n = w.ntiles;
+    if (n > 0) put_scales(0, ks0, vs0);
+    if (n > 1) put_scales(1, ks1, vs1);
     bool ok = true;
     for (int i = 2; i < n && ok; ++i) {
-      const int s = v_slot, c3 = v_c3;         // tile i - 1's
-      ok = send_k(i);
-      const int ks = v_slot, kc3 = v_c3;
-      v_slot = s;
+      const int at = next.slot, c3 = block_of(next);
+      load_scales(i, next);
+      const float ks = next.ks, vs = next.vs;
+      ok = warp_wait(&bars->raw_k_empty, (staging_use(i) - 1) & 1);
+      if (!ok) break;
+      send(smem + kOffRaw, kmap, &bars->raw_k_full, at, c3);
+      k_sent = i + 1;
+      look_up(i + 1, next);
+      // Slot i % 4 was last read for tile i - 4.  K(i - 1) has been read: tile A's
+      // warps do so after their P(i - 3) and after S_B(i - 3), which was issued after
+      // P_B(i - 4).
+      put_scales(i, ks, vs);
+      ok = send_v(i - 1, v_slot, v_c3);
+      v_slot = at;
       v_c3 = c3;
-      ok = ok && send_v(i - 1);
-      v_slot = ks;
-      v_c3 = kc3;
     }
-    if (ok && n > 1) ok = send_v(n - 1);
+    if (ok && n > 1) ok = send_v(n - 1, v_slot, v_c3);
     if (!ok && lane == 0) {
       bars->abort = 1;
       report(a.status_flags, kFlagTimeout);
@@ -626,14 +650,16 @@ __device__ __forceinline__ void q_rows_to_f16(const PrefillArgs& a, const Work& 
 #pragma unroll
   for (int i = 0; i < kEach; ++i) {
     const int row = i * 2 * kSoftmaxWarps + hw;
-    float f[8], amax = 0.f;
-    unpack8(v[i], f);
-#pragma unroll
-    for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(f[e]));
-    amax = __uint_as_float(
-        __reduce_max_sync(0xffffu << (threadIdx.x & 16), __float_as_uint(amax)));
+    // the largest magnitude of the row, by its bf16 bits (order as integers, NaN last)
+    auto larger = [](uint32_t x, uint32_t y) {
+      return __vmaxu2(x & 0x7fff7fffu, y & 0x7fff7fffu);
+    };
+    const uint32_t m2 = larger(larger(v[i].x, v[i].y), larger(v[i].z, v[i].w));
+    const uint32_t m = __reduce_max_sync(0xffffu << (threadIdx.x & 16), max(m2 & 0xffffu, m2 >> 16));
     float inverse;
-    const float up = q_row_scale(amax, inverse);
+    const float up = q_row_scale(__uint_as_float(m << 16), inverse);
+    float f[8];
+    unpack8(v[i], f);
     *reinterpret_cast<uint4*>(smem + kOffQ + (row / kM) * kTile + (l >> 3) * kHalf +
                               swz128(row % kM, l & 7)) =
         make_uint4(pack_f16x2(f[0] * up, f[1] * up), pack_f16x2(f[2] * up, f[3] * up),
