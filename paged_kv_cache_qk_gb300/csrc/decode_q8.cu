@@ -48,28 +48,37 @@ constexpr int kHeadTileBytes = kTK * kHeadDim;
 constexpr float kHeadroom = 4.f;               // log2 by which a score may pass m
 constexpr float kBias = 10.f;                  // P' = 2^(x - m + kBias) <= 2^14
 
-template <int HPC>
+template <int HPC, int NT>
 struct GeometryQ8 {
+  static constexpr int kSplit = HPC == 8 ? 1 : 2;     // consumer warps per head
+  static constexpr int kConsumers = HPC * kSplit;
+  // With 9 to 16 rows and nine warps a CTA (168 registers) the q fragments, 32
+  // registers, are read from shared memory, [k-step][n-tile][lane] of each warp:
+  // pairs of tiles then spill ~30 registers at their edges and still beat single
+  // tiles (32 x 5 rows of 4 a kv head, 7 splits: 84.5 -> 75.5 us).
+  static constexpr bool kQInSmem = NT == 2 && kConsumers == 8;
+  static constexpr int kQBytes = kQInSmem ? 8 * NT * 32 * 8 : 0;
   static constexpr int kBudgetKb = HPC >= 4 ? 192 : (HPC == 2 ? 96 : 64);
   static constexpr int kStageBytes = 2 * HPC * kHeadTileBytes;
   static constexpr int kRaw = kBudgetKb * 1024 / kStageBytes;
-  static constexpr int kStages = kRaw > 12 ? 12 : kRaw;
-  static constexpr int kSplit = HPC == 8 ? 1 : 2;     // consumer warps per head
-  static constexpr int kConsumers = HPC * kSplit;
+  static constexpr int kMostStages = kQInSmem ? 10 : 12;
+  static constexpr int kStages = kRaw > kMostStages ? kMostStages : kRaw;
   // one n-tile of a warp's result, per head: O, then (l, mu, top) of two rows a lane
   static constexpr int kMergeBytes = kSplit > 1 ? 32 * (32 + 6) * 4 : 0;
   static constexpr int kOffMerge = kStages * kStageBytes;
-  static constexpr int kSmemBytes = kOffMerge + HPC * kMergeBytes + 1024;
+  static constexpr int kOffQ = kOffMerge + HPC * kMergeBytes;
+  static constexpr int kSmemBytes = kOffQ + kConsumers * kQBytes + 1024;
+  static_assert(kSmemBytes <= 227 * 1024, "shared memory");
   static constexpr int kThreads = (kConsumers + 1) * 32;
 };
 
 // ----------------------------------------------------------------- producer
 
-template <int HPC>
+template <int HPC, int NT>
 __device__ void produce_q8(const CUtensorMap* kmap, const CUtensorMap* vmap, const DecodeArgs& a,
                            const Plan* plan, uint8_t* stages, uint64_t* full, uint64_t* empty,
                            volatile int* abort_flag, int* issued_out) {
-  using Geo = GeometryQ8<HPC>;
+  using Geo = GeometryQ8<HPC, NT>;
   constexpr int STAGES = Geo::kStages;
   const int lane = threadIdx.x & 31;
   if (lane == 0) {
@@ -177,7 +186,7 @@ template <int HPC, int NT, int kFormat>
 __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan* plan,
                            uint8_t* stages, uint64_t* full, uint64_t* empty, uint64_t* merge_full,
                            uint64_t* merge_empty, volatile int* abort_flag) {
-  using Geo = GeometryQ8<HPC>;
+  using Geo = GeometryQ8<HPC, NT>;
   constexpr int STAGES = Geo::kStages;
   constexpr int kSplit = Geo::kSplit;
   const int lane = threadIdx.x & 31;
@@ -206,7 +215,9 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
     float2 next = tile_scales(a, sv, seg, kvh, lane);
 
     // q rows as f16, dims in the order the K words bring them
-    uint32_t qb[NT][8][2];
+    uint32_t qb[Geo::kQInSmem ? 1 : NT][8][2];
+    const uint32_t q_frag = smem_addr(stages + Geo::kOffQ + (threadIdx.x >> 5) * Geo::kQBytes) + lane * 8;
+    if (Geo::kQInSmem) __syncwarp();           // reads of the segment before
     float rf[NT][2];                           // score factor of rows 2c, 2c + 1
     int lim[NT][2];
 #pragma unroll
@@ -245,8 +256,17 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
           unpack8(u[j][hf], f);
 #pragma unroll
           for (int w = 0; w < 2; ++w) {
-            qb[nt][j * 4 + hf * 2 + w][0] = pack_f16x2(f[4 * w] * up, f[4 * w + 1] * up);
-            qb[nt][j * 4 + hf * 2 + w][1] = pack_f16x2(f[4 * w + 2] * up, f[4 * w + 3] * up);
+            const int step = j * 4 + hf * 2 + w;
+            const uint32_t b0 = pack_f16x2(f[4 * w] * up, f[4 * w + 1] * up);
+            const uint32_t b1 = pack_f16x2(f[4 * w + 2] * up, f[4 * w + 3] * up);
+            if constexpr (Geo::kQInSmem) {
+              asm volatile("st.shared.v2.b32 [%0], {%1, %2};" ::"r"(q_frag + (step * NT + nt) * 256),
+                           "r"(b0), "r"(b1)
+                           : "memory");
+            } else {
+              qb[nt][step][0] = b0;
+              qb[nt][step][1] = b1;
+            }
           }
         }
       const float mine = inverse * a.scale_log2;
@@ -332,8 +352,18 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
             codes_adjacent<kFormat>(wa[w], a0, a2);
             codes_adjacent<kFormat>(wb[w], a1, a3);
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-              mma_f16(chain[j % kChains][nt], a0, a1, a2, a3, qb[nt][j * 4 + w][0], qb[nt][j * 4 + w][1]);
+            for (int nt = 0; nt < NT; ++nt) {
+              uint32_t b0, b1;
+              if constexpr (Geo::kQInSmem)
+                asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];"
+                             : "=r"(b0), "=r"(b1)
+                             : "r"(q_frag + ((j * 4 + w) * NT + nt) * 256));
+              else {
+                b0 = qb[nt][j * 4 + w][0];
+                b1 = qb[nt][j * 4 + w][1];
+              }
+              mma_f16(chain[j % kChains][nt], a0, a1, a2, a3, b0, b1);
+            }
           }
         }
 #pragma unroll
@@ -442,8 +472,7 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
         iv_l = __frcp_rn(vs);
         next = tile_scales(a, sv, seg, kvh, i + 32 + lane);
       }
-      // pairs, except with 16 rows and nine warps a CTA, which get 168 registers
-      constexpr int kAtOnce = HPC >= 4 && NT == 2 ? 1 : 2;
+      constexpr int kAtOnce = 2;
       const int n = min(seg.ntiles - i, kAtOnce);
       if (kSplit > 1 && ((i / kAtOnce) % kSplit) != part) {   // the other warp's
         i += n;
@@ -551,7 +580,7 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
 // Towards L2 while the previous kernel runs, as in the bf16 kernel: the first
 // ring of tiles (split schedule) or the sequence lengths (balanced).  A prefetch
 // binds no value; what decides its address is read past L1.
-template <int HPC>
+template <int HPC, int NT>
 __device__ void prefetch_before_wait_q8(const CUtensorMap* kmap, const CUtensorMap* vmap,
                                         const DecodeArgs& a) {
   const int lane = threadIdx.x & 31;
@@ -559,7 +588,7 @@ __device__ void prefetch_before_wait_q8(const CUtensorMap* kmap, const CUtensorM
     for (int i = lane * 32; i < a.batch; i += 32 * 32) prefetch_l2(a.seq_lens + i);
     return;
   }
-  if (lane >= GeometryQ8<HPC>::kStages) return;
+  if (lane >= GeometryQ8<HPC, NT>::kStages) return;
   const int b = blockIdx.z, hg = blockIdx.y, j = blockIdx.x;
   const long long cap = static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
   long long L = __ldcg(a.seq_lens + b);
@@ -580,11 +609,11 @@ __device__ void prefetch_before_wait_q8(const CUtensorMap* kmap, const CUtensorM
 // ------------------------------------------------------------------ kernel
 
 template <int HPC, int NT, int kFormat>
-__global__ void __launch_bounds__(GeometryQ8<HPC>::kThreads, 1)
+__global__ void __launch_bounds__(GeometryQ8<HPC, NT>::kThreads, 1)
 paged_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
                        const __grid_constant__ CUtensorMap vmap, const DecodeArgs a,
                        const ScaleView sv) {
-  using Geo = GeometryQ8<HPC>;
+  using Geo = GeometryQ8<HPC, NT>;
   constexpr int STAGES = Geo::kStages;
   extern __shared__ uint8_t smem_raw[];
   __shared__ uint64_t full[STAGES];
@@ -611,7 +640,7 @@ paged_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
     issued = 0;
     fence_barrier_init();
   }
-  if (warp == kProducer) prefetch_before_wait_q8<HPC>(&kmap, &vmap, a);
+  if (warp == kProducer) prefetch_before_wait_q8<HPC, NT>(&kmap, &vmap, a);
   __syncthreads();
   pdl_launch_dependents();
   pdl_wait();
@@ -621,7 +650,7 @@ paged_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
     write_empty_units(a, HPC);
   }
   if (warp == kProducer)
-    produce_q8<HPC>(&kmap, &vmap, a, &plan, stages, full, empty, &abort_flag, &issued);
+    produce_q8<HPC, NT>(&kmap, &vmap, a, &plan, stages, full, empty, &abort_flag, &issued);
   else
     consume_q8<HPC, NT, kFormat>(a, sv, &plan, stages, full, empty, merge_full, merge_empty,
                                  &abort_flag);
@@ -632,7 +661,7 @@ paged_decode_q8_kernel(const __grid_constant__ CUtensorMap kmap,
 template <int HPC, int NT, int kFormat>
 cudaError_t launch_one(const CUtensorMap& kmap, const CUtensorMap& vmap, const DecodeArgs& a,
                        const ScaleView& sv, int grid_ctas, cudaStream_t stream) {
-  using Geo = GeometryQ8<HPC>;
+  using Geo = GeometryQ8<HPC, NT>;
   auto kern = paged_decode_q8_kernel<HPC, NT, kFormat>;
   static std::atomic<uint64_t> smem_set{0};
   const cudaError_t e = set_smem_limit_once(kern, Geo::kSmemBytes, smem_set);
