@@ -613,10 +613,12 @@ struct ProducerQ8 {
       v_c3 = c3;
     }
     if (ok && n > 1) ok = send_v(n - 1, v_slot, v_c3);
-    if (!ok && lane == 0) {
-      bars->abort = 1;
-      report(a.status_flags, kFlagTimeout);
-      // the copies in flight land before the CTA leaves
+    if (lane == 0) {
+      if (!ok) {
+        bars->abort = 1;
+        report(a.status_flags, kFlagTimeout);
+      }
+      // the copies in flight land before the CTA leaves, whoever gave up
       if (k_sent > 1) mbar_wait(&bars->raw_k1_full, 0);
       if (k_sent != 0) mbar_wait(&bars->raw_k_full, staging_use(k_sent == 2 ? 0 : k_sent - 1) & 1);
       for (int i = v_sent < 2 ? 0 : v_sent - 2; i < v_sent; ++i)
@@ -1103,7 +1105,10 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
   uint64_t* xbar = &bars->xch[x][wq];
   uint32_t uses = 0;
   bool ok = true;
-  if (kFormat != 0) sl2 *= reinterpret_cast<const float*>(smem + kOffRowScale)[x * kM + r];
+  // 8-bit: held where no product with a scale, 2^-64 at least, becomes 0: masked
+  // scores are -inf
+  if (kFormat != 0)
+    sl2 = fmaxf(sl2 * reinterpret_cast<const float*>(smem + kOffRowScale)[x * kM + r], 0x1p-85f);
 
   // decided once: interior tiles end at or before every row's limit (the
   // warp's smallest), and only the last tile can reach past key_end (tile A

@@ -79,11 +79,13 @@ __device__ __forceinline__ float usable_scale(float s) {
 
 // bf16 rows become f16 operands after a multiplication by 2^k that brings the
 // row's largest magnitude to [2^14, 2^15): exact for every value within 2^-28
-// of it.  2^k from that magnitude (0, infinite or NaN: 1), and 2^-k.
+// of it.  2^k from that magnitude (0, infinite or NaN: 1), and 2^-k.  k <= 72 keeps
+// 2^-k times any softmax scale above 2^-13 and any K scale from becoming 0; in rows
+// below 2^-57 what is under 2^-97 is dropped, 2^-18 of a score at the largest K.
 __device__ __forceinline__ float q_row_scale(float amax, float& inverse) {
   const int e = static_cast<int>(__float_as_uint(amax) >> 23);   // biased
   int k = (amax > 0.f && e < 255) ? 14 + 127 - e : 0;
-  k = k > 126 ? 126 : k;                       // amax below 2^-112
+  k = k > 72 ? 72 : k;
   inverse = __int_as_float((127 - k) << 23);
   return __int_as_float((127 + k) << 23);
 }

@@ -246,3 +246,15 @@ def test_q8_decode_of_a_bf16_cache_s_values(lib):
 def test_codes_round_trip():
     b = np.arange(256, dtype=np.uint8).reshape(2, 128)
     assert np.array_equal(code_bytes(from_bytes(b, "int8")), b)
+
+
+@pytest.mark.parametrize("fmt", CLASSES)
+def test_decode_tiny_rows_over_groups_of_the_smallest_scale(lib, fmt):
+    p = _problem(16, 8, 4, 16, [130, 4], 21)
+    c = Q8(p, fmt, 22)
+    used = ~torch.isnan(c.ks)
+    c.ks[used] = 2.0 ** -64
+    q = p.q.clone()
+    q[1:6] *= 2.0 ** -110
+    out, lse = _decode(lib, p, c, 1, q=q)
+    check_attention(p, c, out, lse, fmt, q=q)

@@ -297,3 +297,17 @@ def test_prefill_benchmark_shape_sampled_rows(lib):
             tol = 2.0 ** -8 * np.abs(ref[0, 0]) + (2.0 ** -11 + 2.0 ** -14) * mag[0, 0]
             assert (np.abs(got - ref[0, 0]) <= tol).all(), (b, t)
             assert np.abs(lse[b, t].double().cpu().numpy() - ref_lse[0, 0]).max() <= 2.0 ** -11
+
+
+@pytest.mark.parametrize("fmt", CLASSES)
+def test_prefill_tiny_rows_over_groups_of_the_smallest_scale(lib, fmt):
+    """Score factors that underflow (2^-110 rows, 2^-64 scales): masked keys stay
+    masked, the others weigh the same."""
+    p = _problem(16, 8, 40, 16, [130, 0], 21)
+    c = Q8(p, fmt, 22)
+    used = ~torch.isnan(c.ks)
+    c.ks[used] = 2.0 ** -64
+    q = p.q.clone()
+    q[5:20] *= 2.0 ** -110
+    out, lse = _prefill(lib, p, c, q=q)
+    check_attention(p, c, out, lse, fmt, q=q)
