@@ -26,6 +26,14 @@
 // of different sequences meet.  A token's rotary angles are read (table) or
 // computed once per CTA and chunk and serve all its heads; the next head's values
 // load while a head is being quantised.
+//
+// Bound, many tokens: instructions and the latencies between them, not HBM (4 x 2048
+// tokens, 16 q and 8 kv heads: 42.5 us where the bytes need 17.4; 214 instructions a
+// warp and head vector against the bf16 append's 150, issue slots 58 % busy, DRAM
+// 25 %).  Few tokens: the chain slots -> angles, values, scales -> maxima -> codes
+// (64 tokens 5.2 us, the bf16 append 2.5).  A value nearer the middle of two codes
+// than the fp32 norm's and rotation's 2^-20 may get either code; deciding those in
+// float64 cost 3 us of 42, 5 of 6.5 on 160 tokens.
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"

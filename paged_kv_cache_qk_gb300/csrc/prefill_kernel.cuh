@@ -386,7 +386,10 @@ __device__ void drain_copies(Bars* bars, int issued) {
 // four or seven in a launch of 24 warps at 80 registers 1694-1743 us (the softmax
 // then spills), three converting out of TMA slots 1703 us: a lone warp beside
 // four softmax warps issues an instruction every ~5 cycles, and conversion, waits
-// and hand-over are ~5000 of them a key tile.
+// and hand-over are ~5000 of them a key tile.  By the softmax warps: 1280 us, K a tile
+// ahead of V 1097, the first tiles asked for before the roles begin, no spills in the
+// softmax loop and Q by half-warps 1006 = 1318 TFLOP/s.  What the conversion adds to
+// the softmax warps' chain and to shared memory's traffic is the rest of the distance.
 
 // This warp's 16 keys (group g of the tile) of codes at `raw` into the stage;
 // keys from `left` on become zeros (slots that no row sees may hold NaN codes).
