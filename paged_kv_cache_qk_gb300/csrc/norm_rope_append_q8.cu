@@ -123,8 +123,12 @@ __device__ __forceinline__ float max_finite(float (&y)[8], bool& bad) {
   return m;
 }
 
-__device__ __forceinline__ uint32_t half_mask() {
-  return 0xffffu << (threadIdx.x & 16);
+// Over the half-warp.  Shuffles: one reduction instruction per half, with two masks
+// in a warp, runs them one after the other (4 x 2048 tokens 42.5 us against 38.4).
+__device__ __forceinline__ float half_warp_max(float m) {
+#pragma unroll
+  for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+  return m;
 }
 
 // Where a token's codes and its group's scale live: offsets for head 0.
@@ -301,7 +305,8 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
     const bool first = active && j == rs;
     uint32_t written = 0u;                     // slots of the group that the run writes
     if (rs + l < re) written = 1u << (sm.slot[rs + l + 1] & (kScaleGroup - 1));
-    written = __reduce_or_sync(half_mask(), written);
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) written |= __shfl_xor_sync(0xffffffffu, written, o);
     const int peer = rs + l < re ? rs + l - b : -1;   // half-warp whose maximum this lane takes
     const int64_t tok = active ? t0 + j : 0;
     if (kIsK) put_angles(n, sm, active ? n.positions[tok] : 0, computed, hw, l);
@@ -353,14 +358,14 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
         }
       }
       float m = max_finite(y, bad);
-      m = __uint_as_float(__reduce_max_sync(half_mask(), __float_as_uint(m)));
+      m = half_warp_max(m);
       if (l == 0) sm.amax[k & 1][hw] = m;
       __syncthreads();
       rescale<kFormat>(sm.grown[list], sm.num_grown[list], n.slot_stride, hw, l);
       list = list == 2 ? 0 : list + 1;
       if (tid == 0) sm.num_grown[list == 2 ? 0 : list + 1] = 0;
       m = peer >= 0 ? sm.amax[k & 1][peer] : 0.f;
-      m = __uint_as_float(__reduce_max_sync(half_mask(), __float_as_uint(m)));
+      m = half_warp_max(m);
       if (active) {
         float prev;
         const float now = group_scale<kFormat>(m, stored, written, &prev);
