@@ -511,6 +511,7 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
   a.num_blocks = L.num_blocks;
   a.num_splits = S;
   a.chunk_pages = std::max(1, (hint_pages + S - 1) / S);
+  a.longest = hint;
   a.m_tiles = m_tiles;
   const float scale = c.scale > 0.f ? c.scale : 1.0f / std::sqrt(128.0f);
   a.scale_log2 = scale * 1.4426950408889634f;

@@ -30,6 +30,7 @@ struct PrefillArgs {
   int64_t num_blocks;
   int32_t num_splits;              // >= 1
   int32_t chunk_pages;             // pages per split
+  int32_t longest;                 // host's bound of seq_lens (decides the launch order)
   int32_t m_tiles;                 // ceil(q_len * group / kPrefillRowsPerCta)
   float scale_log2;                // softmax scale * log2(e)
   __nv_bfloat16* out;              // num_splits == 1: [tokens, Hq, 128]

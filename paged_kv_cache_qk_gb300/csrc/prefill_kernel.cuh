@@ -230,7 +230,8 @@ struct Work {
   bool has_b;    // row tile B holds rows
 };
 
-__device__ Work decode_work(const PrefillArgs& a) {
+// What the grid and the row offsets say; L is the sequence's length as read.
+__device__ __forceinline__ Work place_work(const PrefillArgs& a) {
   Work w;
   if (a.mt_major) {
     // the launch order runs over all sequences' last row tiles first: for
@@ -253,12 +254,7 @@ __device__ Work decode_work(const PrefillArgs& a) {
     w.j = x / a.num_kv_heads;
     w.b = blockIdx.y;
   }
-  const long long cap = static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
-  const long long L = min(static_cast<long long>(max(a.seq_lens[w.b], 0)), cap);
-  w.L = static_cast<int>(L);
-  const long long chunk_keys = static_cast<long long>(a.chunk_pages) * a.block_size;
-  w.k0 = static_cast<int>(min(L, w.j * chunk_keys));
-  w.k1 = (w.j == a.num_splits - 1) ? w.L : static_cast<int>(min(L, (w.j + 1) * chunk_keys));
+  w.L = a.seq_lens[w.b];
   if (a.cu_seqlens_q != nullptr) {
     const long long c0 = a.cu_seqlens_q[w.b], c1 = a.cu_seqlens_q[w.b + 1];
     w.q0 = c0;
@@ -268,13 +264,23 @@ __device__ Work decode_work(const PrefillArgs& a) {
     w.q_len = a.q_len;
   }
   w.rows = w.q_len * a.group;
+  return w;
+}
+
+// The keys of the CTA's rows.
+__device__ __forceinline__ void find_keys(const PrefillArgs& a, Work& w) {
+  const long long cap = static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
+  const long long L = min(static_cast<long long>(max(w.L, 0)), cap);
+  w.L = static_cast<int>(L);
+  const long long chunk_keys = static_cast<long long>(a.chunk_pages) * a.block_size;
+  w.k0 = static_cast<int>(min(L, w.j * chunk_keys));
+  w.k1 = (w.j == a.num_splits - 1) ? w.L : static_cast<int>(min(L, (w.j + 1) * chunk_keys));
   const int row0 = w.mt * 2 * kM;
   w.has_b = row0 + kM < w.rows;
   const int last_row = min(row0 + 2 * kM - 1, w.rows - 1);
   const int t_last = div_group(a, max(last_row, 0));   // rows == 0: no tiles either way
   w.key_end = max(w.k0, min(w.k1, w.L - w.q_len + t_last + 1));
   w.ntiles = row0 < w.rows ? (w.key_end - w.k0 + kN - 1) / kN : 0;
-  return w;
 }
 
 // ------------------------------------------------------------- producer
@@ -636,13 +642,13 @@ struct ProducerQ8 {
 // lane, all eight loads in flight), each scaled by the power of two of its largest
 // magnitude; the inverse goes to the row's slot.  (One thread a half row, 16-byte
 // loads 32 rows apart, took 18,000 cycles a CTA.)
-__device__ __forceinline__ void q_rows_to_f16(const PrefillArgs& a, const Work& w,
-                                              uint8_t* smem) {
-  constexpr int kEach = 2 * kM / (2 * kSoftmaxWarps);
+constexpr int kQRowsEach = 2 * kM / (2 * kSoftmaxWarps);
+
+__device__ __forceinline__ void load_q_rows(const PrefillArgs& a, const Work& w,
+                                            uint4 (&v)[kQRowsEach]) {
   const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
-  uint4 v[kEach];
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
+  for (int i = 0; i < kQRowsEach; ++i) {
     const int rg = w.mt * 2 * kM + i * 2 * kSoftmaxWarps + hw;
     const int t = div_group(a, rg);
     const bool live = rg < w.rows && w.q0 + t >= 0 && w.q0 + t < a.total_q;
@@ -652,8 +658,12 @@ __device__ __forceinline__ void q_rows_to_f16(const PrefillArgs& a, const Work& 
                                 a.q_stride_h) + l)
                 : make_uint4(0u, 0u, 0u, 0u);
   }
+}
+
+__device__ __forceinline__ void q_rows_to_f16(const uint4 (&v)[kQRowsEach], uint8_t* smem) {
+  const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
 #pragma unroll
-  for (int i = 0; i < kEach; ++i) {
+  for (int i = 0; i < kQRowsEach; ++i) {
     const int row = i * 2 * kSoftmaxWarps + hw;
     // the largest magnitude of the row, by its bf16 bits (order as integers, NaN last)
     auto larger = [](uint32_t x, uint32_t y) {
@@ -1251,10 +1261,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   // launched as a programmatic dependent: q, the appended K/V, the tables and
   // the lengths may come from the previous kernel in the stream
   pdl_wait();
-  const Work w = decode_work(a);
+  Work w = place_work(a);
   // row tiles past this sequence's rows (varlen grids cover the longest
   // sequence): nothing to compute or write; leave before any set-up
   if (w.mt * 2 * kM >= w.rows) return;
+  uint4 q_row[kQRowsEach];                     // 8-bit: Q on its way before the length is known
+  if (kFormat != 0 && warp < kSoftmaxWarps) load_q_rows(a, w, q_row);
+  find_keys(a, w);
 
   if (threadIdx.x == kProducerWarp * 32) {
     prefetch_tensormap(&kmap);
@@ -1307,7 +1320,7 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   if (warp == kMmaWarp) tc5::tmem_alloc(&bars->tmem_base, kTmemCols);
 
   if (kFormat != 0) {
-    if (warp < kSoftmaxWarps && w.ntiles > 0) q_rows_to_f16(a, w, smem);
+    if (warp < kSoftmaxWarps && w.ntiles > 0) q_rows_to_f16(q_row, smem);
   } else if (warp < kSoftmaxWarps && !a.q_tma) {
     // Q tiles: thread i loads 64 dims (half i / 256) of row i % 128 of tile
     // (i / 128) % 2 (row = (token, q head of the group)), one swizzled half
