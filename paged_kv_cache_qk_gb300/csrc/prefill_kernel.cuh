@@ -433,7 +433,7 @@ __device__ __forceinline__ void convert_group(const uint8_t* raw, uint8_t* stage
   __syncwarp();
 }
 
-// K (tile A's warps) and V (tile B's) of key tile i; false: a wait gave up.  K(1) is
+// K (tile A's warps; K(1): tile B's) and V (tile B's) of key tile i; false: a wait gave up.  K(1) is
 // there from the start, in its stage as V is (the staging tile holds K(0) then):
 // the staging tile's use u is K(0), K(2), K(3) ..
 __device__ __forceinline__ int staging_use(int i) { return i == 0 ? 0 : i - 1; }
@@ -465,14 +465,20 @@ __device__ __forceinline__ bool convert_v(const Work& w, uint8_t* smem, Bars* ba
 }
 
 template <int kFormat>
-__device__ __forceinline__ void convert_all_v(const PrefillArgs& a, const Work& w, uint8_t* smem,
-                                              Bars* bars) {
-  for (int i = 0; i < w.ntiles; ++i)
-    if (!convert_v<kFormat>(w, smem, bars, i)) {
-      bars->abort = 1;
-      report(a.status_flags, kFlagTimeout);
-      return;
-    }
+__device__ __forceinline__ bool convert_first_b(const Work& w, uint8_t* smem, Bars* bars) {
+  return (w.ntiles < 2 || convert_k<kFormat, false>(w, smem, bars, 1)) &&
+         convert_v<kFormat>(w, smem, bars, 0);
+}
+
+template <int kFormat>
+__device__ __forceinline__ void convert_without_b(const PrefillArgs& a, const Work& w,
+                                                  uint8_t* smem, Bars* bars) {
+  bool ok = w.ntiles == 0 || convert_first_b<kFormat>(w, smem, bars);
+  for (int i = 1; i < w.ntiles && ok; ++i) ok = convert_v<kFormat>(w, smem, bars, i);
+  if (!ok) {
+    bars->abort = 1;
+    report(a.status_flags, kFlagTimeout);
+  }
 }
 
 // Page of the group that holds key `key` (a multiple of 16): page, slot in it.
@@ -666,13 +672,12 @@ __device__ __forceinline__ void q_rows_to_f16(const uint4 (&v)[kQRowsEach], uint
   for (int i = 0; i < kQRowsEach; ++i) {
     const int row = i * 2 * kSoftmaxWarps + hw;
     // the largest magnitude of the row, by its bf16 bits (order as integers, NaN last)
-    auto larger = [](uint32_t x, uint32_t y) {
-      return __vmaxu2(x & 0x7fff7fffu, y & 0x7fff7fffu);
-    };
-    const uint32_t m2 = larger(larger(v[i].x, v[i].y), larger(v[i].z, v[i].w));
-    const uint32_t m = __reduce_max_sync(0xffffu << (threadIdx.x & 16), max(m2 & 0xffffu, m2 >> 16));
+    constexpr uint32_t kAbs = 0x7fff7fffu;
+    uint32_t m2 = __vmaxu2(__vmaxu2(v[i].x & kAbs, v[i].y & kAbs), __vmaxu2(v[i].z & kAbs, v[i].w & kAbs));
+#pragma unroll
+    for (int o = 8; o > 0; o >>= 1) m2 = __vmaxu2(m2, __shfl_xor_sync(0xffffffffu, m2, o));
     float inverse;
-    const float up = q_row_scale(__uint_as_float(m << 16), inverse);
+    const float up = q_row_scale(__uint_as_float(max(m2 << 16, m2 & 0xffff0000u)), inverse);
     float f[8];
     unpack8(v[i], f);
     *reinterpret_cast<uint4*>(smem + kOffQ + (row / kM) * kTile + (l >> 3) * kHalf +
@@ -1135,10 +1140,9 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
 
   float m_ref = -INFINITY;                     // reference max (log2 units), integer once set
   float l = 0.f;                               // this half's sum of P
-  if (kFormat != 0 && n > 0) {                 // the first K tiles, the first V tile
-    ok = x == 0 ? convert_k<kFormat>(w, smem, bars, 0) : convert_v<kFormat>(w, smem, bars, 0);
-    if (x == 0 && n > 1) ok = ok && convert_k<kFormat, false>(w, smem, bars, 1);
-  }
+  // the first tiles; K(1) by tile B's warps, whose scores come after tile A's
+  if (kFormat != 0 && n > 0)
+    ok = x == 0 ? convert_k<kFormat>(w, smem, bars, 0) : convert_first_b<kFormat>(w, smem, bars);
   for (int i = 0; i < n && ok; ++i) {
     // 8-bit: this half's four groups of scales
     const float4* scales = nullptr;
@@ -1355,8 +1359,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
       // 8-bit: the work's fields stay in shared memory, for the registers' sake
       softmax_rows<kFormat>(a, kFormat == 0 ? w : shared_work, smem, bars, &omap,
                             reinterpret_cast<float*>(smem + kOffSlots), tmem, x, half);
-    else if (kFormat != 0)                     // no tile B: V is all its warps do
-      convert_all_v<kFormat>(a, w, smem, bars);
+    else if (kFormat != 0)                     // no tile B: codes are all its warps do
+      convert_without_b<kFormat>(a, w, smem, bars);
   } else if (warp == kProducerWarp) {
     if constexpr (kFormat == 0) {
       int n = 0;
