@@ -28,12 +28,11 @@
 // load while a head is being quantised.
 //
 // Bound, many tokens: instructions and the latencies between them, not HBM (4 x 2048
-// tokens, 16 q and 8 kv heads: 42.5 us where the bytes need 17.4; 214 instructions a
-// warp and head vector against the bf16 append's 150, issue slots 58 % busy, DRAM
-// 25 %).  Few tokens: the chain slots -> angles, values, scales -> maxima -> codes
+// tokens, 16 q and 8 kv heads: 38.4 us where the bytes need 17.4; ~210 instructions a
+// warp and head vector against the bf16 append's 150).  Few tokens: the chain slots -> angles, values, scales -> maxima -> codes
 // (64 tokens 5.2 us, the bf16 append 2.5).  A value nearer the middle of two codes
 // than the fp32 norm's and rotation's 2^-20 may get either code; deciding those in
-// float64 cost 3 us of 42, 5 of 6.5 on 160 tokens.
+// float64 cost 3 us more, 5 us on 160 tokens.
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
@@ -49,8 +48,8 @@ constexpr int kWindow = 16;                    // tokens per CTA, one per half-w
 constexpr int kThreads = kWindow * 16;
 // Many tokens: four CTAs share an SM at 64 registers and a head vector's share of
 // a window is cut so that three waves of them come (measured on 4 x 2048 tokens, 16
-// q and 8 kv heads: 42.8 us; two waves 44.6, four 47.7; three CTAs an SM 46.7-50.8,
-// two at 108 registers 57.2).  Few: two, without spills (64 tokens 5.1 us against 5.9).
+// q and 8 kv heads, before the maxima went through shuffles: 42.8 us; two waves 44.6,
+// four 47.7; three CTAs an SM 46.7-50.8, two at 108 registers 57.2).  Few: two, without spills (64 tokens 5.1 us against 5.9).
 constexpr int kManyTokens = 1024;
 constexpr int kManyCtas = 4, kManyWaves = 3, kFewCtas = 2;
 static_assert(kWindow == kScaleGroup, "a run spans at most two windows");

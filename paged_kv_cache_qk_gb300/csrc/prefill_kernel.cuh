@@ -378,8 +378,8 @@ __device__ void drain_copies(Bars* bars, int issued) {
 // Codes come in by TMA, K's into a staging tile, V's into the first half of their
 // stage, and the softmax warps turn them into the f16 operands while they would
 // wait for the tensor core: tile A's eight warps convert K(i + 2) after P_A(i),
-// tile B's convert V(i + 1) after P_B(i) (or do nothing else, where there is no
-// tile B), one 16-slot group a warp: four reads of 16 bytes a lane, eight stores.
+// tile B's, after K(1) and V(0), V(i + 1) after P_B(i) (or do nothing else, where there
+// is no tile B), one 16-slot group a warp: four reads of 16 bytes a lane, eight stores.
 // A group of V becomes f16 in place: its codes lie where its first half of dims
 // goes, so a warp only overwrites what it has read.
 // Lane group lane / 4 reads row order[lane / 4] of 8 rows so that the two rows of
@@ -394,7 +394,7 @@ __device__ void drain_copies(Bars* bars, int issued) {
 // four softmax warps issues an instruction every ~5 cycles, and conversion, waits
 // and hand-over are ~5000 of them a key tile.  By the softmax warps: 1280 us, K a tile
 // ahead of V 1097, the first tiles asked for before the roles begin, no spills in the
-// softmax loop and Q by half-warps 1006 = 1318 TFLOP/s.  What the conversion adds to
+// softmax loop and Q by half-warps 1005 = 1320 TFLOP/s.  What the conversion adds to
 // the softmax warps' chain and to shared memory's traffic is the rest of the distance.
 
 // This warp's 16 keys (group g of the tile) of codes at `raw` into the stage;
@@ -433,9 +433,9 @@ __device__ __forceinline__ void convert_group(const uint8_t* raw, uint8_t* stage
   __syncwarp();
 }
 
-// K (tile A's warps; K(1): tile B's) and V (tile B's) of key tile i; false: a wait gave up.  K(1) is
-// there from the start, in its stage as V is (the staging tile holds K(0) then):
-// the staging tile's use u is K(0), K(2), K(3) ..
+// K (tile A's warps; K(1): tile B's) and V (tile B's) of key tile i; false: a wait
+// gave up.  K(1) is there from the start, in its stage as V is (the staging tile holds
+// K(0) then): the staging tile's use u is K(0), K(2), K(3) ..
 __device__ __forceinline__ int staging_use(int i) { return i == 0 ? 0 : i - 1; }
 
 template <int kFormat, bool kStaged = true>
@@ -646,8 +646,9 @@ struct ProducerQ8 {
 // Q rows as f16 in both tiles' shared memory, before the warps take their roles:
 // half-warp h of the sixteen softmax warps' 32 brings rows h, h + 32, .. (16 bytes a
 // lane, all eight loads in flight), each scaled by the power of two of its largest
-// magnitude; the inverse goes to the row's slot.  (One thread a half row, 16-byte
-// loads 32 rows apart, took 18,000 cycles a CTA.)
+// magnitude; the inverse goes to the row's slot.  Of a CTA's ~20,000 cycles outside its
+// key tiles the loads take ~2,000 and the conversion 2,500.  (One thread a half row,
+// 16-byte loads 32 rows apart: 18,000.)
 constexpr int kQRowsEach = 2 * kM / (2 * kSoftmaxWarps);
 
 __device__ __forceinline__ void load_q_rows(const PrefillArgs& a, const Work& w,
