@@ -41,8 +41,6 @@
 #include "decode_schedule.cuh"
 #include "q8_common.cuh"
 
-#include <type_traits>
-
 namespace pkvqk {
 
 namespace {
@@ -77,6 +75,10 @@ struct GeometryQ8 {
   static constexpr int kThreads = (kConsumers + 1) * 32;
 };
 
+// A segment's tiles in whole pairs (the consumers take two at once): an odd one is
+// followed by one of zeros, whose keys nobody sees.
+__device__ __forceinline__ int paired(int ntiles) { return (ntiles + 1) & ~1; }
+
 // ----------------------------------------------------------------- producer
 
 template <int HPC, int NT>
@@ -98,8 +100,9 @@ __device__ void produce_q8(const CUtensorMap* kmap, const CUtensorMap* vmap, con
   bool ok = true;
   while (ok && src.next(seg)) {
     const int32_t* bt = a.block_tables + static_cast<int64_t>(seg.b) * a.max_blocks_per_seq;
-    for (int i0 = 0; i0 < seg.ntiles && ok; i0 += 32) {
-      int blk = 0, slot0 = 0;
+    const int tiles = paired(seg.ntiles);
+    for (int i0 = 0; i0 < tiles && ok; i0 += 32) {
+      int blk = static_cast<int>(a.num_blocks), slot0 = 0;   // outside the cache: zeros
       const int i = i0 + lane;
       if (i < seg.ntiles) {
         const int key = seg.k0 + i * kTK;
@@ -108,7 +111,7 @@ __device__ void produce_q8(const CUtensorMap* kmap, const CUtensorMap* vmap, con
         blk = __ldg(bt + page);
         if (blk < 0 || blk >= a.num_blocks) report(a.status_flags, kFlagBadBlock);
       }
-      const int n = min(32, seg.ntiles - i0);
+      const int n = min(32, tiles - i0);
       for (int j = 0; j < n; ++j) {
         const int bj = __shfl_sync(0xffffffffu, blk, j);
         const int sj = __shfl_sync(0xffffffffu, slot0, j);
@@ -215,7 +218,7 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
   int it0 = 0;                                 // ring position of the segment's first tile
   uint32_t merges = 0;
   bool aborted = false;
-  for (; !aborted && src.next(seg); it0 += seg.ntiles) {
+  for (; !aborted && src.next(seg); it0 += paired(seg.ntiles)) {
     const int kvh = seg.hg * HPC + hh;
     float2 next = tile_scales(a, sv, seg, kvh, lane);
 
@@ -225,7 +228,7 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
     if (Geo::kQInSmem) __syncwarp();           // reads of the segment before
     float rf[NT][2];                           // score factor of rows 2c, 2c + 1
     int lim[NT][2];
-#pragma unroll
+#pragma unroll(Geo::kQInSmem ? 1 : NT)
     for (int nt = 0; nt < NT; ++nt) {
       const int rr = 8 * nt + g;
       const int t = rr / a.group, gi = rr - t * a.group;
@@ -277,12 +280,19 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
       const float mine = inverse * a.scale_log2;
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
-        rf[nt][e] = __shfl_sync(0xffffffffu, mine, (2 * c + e) * 4);
+        const float factor = __shfl_sync(0xffffffffu, mine, (2 * c + e) * 4);
         const int row = 8 * nt + 2 * c + e;
-        lim[nt][e] = row < R ? seg.seq_len - a.q_len + row / a.group + 1 : 0;
+        const int end = row < R ? min(seg.seq_len - a.q_len + row / a.group + 1, seg.k1) : 0;
+        if (nt == 0) {
+          rf[0][e] = factor;
+          lim[0][e] = end;
+        } else {
+          rf[NT - 1][e] = factor;
+          lim[NT - 1][e] = end;
+        }
       }
     }
-    const int lim_all = seg.seq_len - a.q_len + 1;   // visible to every row
+    const int lim_all = min(seg.seq_len - a.q_len + 1, seg.k1);   // visible to every row
 
     float o[NT][8][4], mu[NT][2], top[NT][2], l[NT][2];
 #pragma unroll
@@ -299,9 +309,9 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
     }
 
     float ks_l = 1.f, lv_l = 0.f, iv_l = 1.f;
-    // U tiles (i .. i + U - 1 of the segment) at once; false: a wait gave up
-    auto tiles = [&](auto count, int i) {
-      constexpr int U = decltype(count)::value;
+    // tiles i and i + 1 of the segment at once; false: a wait gave up
+    constexpr int U = 2;
+    auto pair = [&](int i) {
       const int it = it0 + i;
       float ks[U], lv[U], iv[U];
       uint32_t kt[U];                          // shared-memory address of the K tile
@@ -408,8 +418,8 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float m = fmaxf(sc[0][nt][e], sc[0][nt][2 + e]);
-            if (U == 2) m = fmaxf(m, fmaxf(sc[U - 1][nt][e], sc[U - 1][nt][2 + e]));
+            float m = fmaxf(fmaxf(sc[0][nt][e], sc[0][nt][2 + e]),
+                            fmaxf(sc[1][nt][e], sc[1][nt][2 + e]));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 4));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 8));
             m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 16));
@@ -468,8 +478,7 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
       }
       return true;
     };
-    int i = 0;
-    while (i < seg.ntiles && !aborted) {
+    for (int i = 0; i < seg.ntiles; i += U) {
       if ((i & 31) == 0) {                     // the next 32 tiles' scales
         ks_l = usable_scale(next.x);
         const float vs = usable_scale(next.y);
@@ -477,41 +486,37 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
         iv_l = __frcp_rn(vs);
         next = tile_scales(a, sv, seg, kvh, i + 32 + lane);
       }
-      constexpr int kAtOnce = 2;
-      const int n = min(seg.ntiles - i, kAtOnce);
-      if (kSplit > 1 && ((i / kAtOnce) % kSplit) != part) {   // the other warp's
-        i += n;
-        continue;
-      }
-      const bool ok = n == kAtOnce ? tiles(std::integral_constant<int, kAtOnce>{}, i)
-                                   : tiles(std::integral_constant<int, 1>{}, i);
-      if (!ok) {
+      if (kSplit > 1 && (i / U) % kSplit != part) continue;   // the other warp's
+      if (!pair(i)) {
         *abort_flag = 1;
         report(a.status_flags, kFlagTimeout);
         aborted = true;
+        break;
       }
-      i += n;
     }
+    if (kSplit > 1 && aborted) break;
 
-    // two warps of a head: the second hands its rows over, one n-tile at a time
-    if constexpr (kSplit > 1) {
-      if (aborted) break;
-      float4* mo = reinterpret_cast<float4*>(stages + Geo::kOffMerge + hh * Geo::kMergeBytes);
-      float* ml = reinterpret_cast<float*>(mo + 8 * 32);
-#pragma unroll
-      for (int nt = 0; nt < NT; ++nt, ++merges) {
+    // The end of a segment runs once or a few times, so its code is kept small: loops
+    // over n-tiles and rows whose turn's values are always those of index 0.  Unrolled,
+    // its first run waited on instruction fetches: 7 us, 13 us with two n-tiles.
+#pragma unroll 1
+    for (int nt = 0; nt < NT && !aborted; ++nt) {
+      // two warps of a head: the second hands its rows over, one n-tile at a time
+      if constexpr (kSplit > 1) {
+        float4* mo = reinterpret_cast<float4*>(stages + Geo::kOffMerge + hh * Geo::kMergeBytes);
+        float* ml = reinterpret_cast<float*>(mo + 8 * 32);
         bool ok = true;
         if (part == 1) {
           if (merges > 0) ok = mbar_wait(&merge_empty[hh], (merges - 1) & 1);
           if (ok) {
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt)
-              mo[mt * 32 + lane] = make_float4(o[nt][mt][0], o[nt][mt][1], o[nt][mt][2], o[nt][mt][3]);
+              mo[mt * 32 + lane] = make_float4(o[0][mt][0], o[0][mt][1], o[0][mt][2], o[0][mt][3]);
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-              ml[(3 * e) * 32 + lane] = l[nt][e];
-              ml[(3 * e + 1) * 32 + lane] = mu[nt][e];
-              ml[(3 * e + 2) * 32 + lane] = top[nt][e];
+              ml[(3 * e) * 32 + lane] = l[0][e];
+              ml[(3 * e + 1) * 32 + lane] = mu[0][e];
+              ml[(3 * e + 2) * 32 + lane] = top[0][e];
             }
           }
           __syncwarp();
@@ -523,62 +528,81 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
               const float mu1 = ml[(3 * e + 1) * 32 + lane];
-              const bool has0 = top[nt][e] != -INFINITY, has1 = ml[(3 * e + 2) * 32 + lane] != -INFINITY;
-              const float m = has0 ? (has1 ? fmaxf(mu[nt][e], mu1) : mu[nt][e]) : mu1;
-              w[e][0] = has0 ? exp2f(mu[nt][e] - m) : 0.f;
+              const bool has0 = top[0][e] != -INFINITY, has1 = ml[(3 * e + 2) * 32 + lane] != -INFINITY;
+              const float m = has0 ? (has1 ? fmaxf(mu[0][e], mu1) : mu[0][e]) : mu1;
+              w[e][0] = has0 ? exp2f(mu[0][e] - m) : 0.f;
               w[e][1] = has1 ? exp2f(mu1 - m) : 0.f;
-              l[nt][e] = l[nt][e] * w[e][0] + ml[(3 * e) * 32 + lane] * w[e][1];
-              mu[nt][e] = m;
+              l[0][e] = l[0][e] * w[e][0] + ml[(3 * e) * 32 + lane] * w[e][1];
+              mu[0][e] = m;
             }
 #pragma unroll
             for (int mt = 0; mt < 8; ++mt) {
               const float4 x = mo[mt * 32 + lane];
-              o[nt][mt][0] = o[nt][mt][0] * w[0][0] + x.x * w[0][1];
-              o[nt][mt][1] = o[nt][mt][1] * w[1][0] + x.y * w[1][1];
-              o[nt][mt][2] = o[nt][mt][2] * w[0][0] + x.z * w[0][1];
-              o[nt][mt][3] = o[nt][mt][3] * w[1][0] + x.w * w[1][1];
+              o[0][mt][0] = o[0][mt][0] * w[0][0] + x.x * w[0][1];
+              o[0][mt][1] = o[0][mt][1] * w[1][0] + x.y * w[1][1];
+              o[0][mt][2] = o[0][mt][2] * w[0][0] + x.z * w[0][1];
+              o[0][mt][3] = o[0][mt][3] * w[1][0] + x.w * w[1][1];
             }
           }
           __syncwarp();
           if (lane == 0 && ok) mbar_arrive(&merge_empty[hh]);
         }
+        ++merges;
         if (!ok) {
           *abort_flag = 1;
           report(a.status_flags, kFlagTimeout);
           aborted = true;
+          break;
         }
       }
-      if (aborted || part == 1) continue;
+      if (kSplit == 1 || part == 0) {
+#pragma unroll 1
+        for (int e = 0; e < 2; ++e) {
+          float sum = l[0][0];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          const int rr = 8 * nt + 2 * c + e;
+          if (rr < R) {
+            const int t = rr / a.group, gi = rr - t * a.group;
+            const RowDest d = row_dest<HPC>(a, seg, t, hh, gi);
+            // a sum of 0: no visible key; NaN goes through
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const float lse = sum == 0.f ? -INFINITY : (mu[0][0] + log2f(sum)) * kLn2;
+            if (d.out != nullptr) {
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt)
+                *reinterpret_cast<uint32_t*>(d.out + 16 * mt + 2 * g) =
+                    pack_bf16x2(o[0][mt][0] * inv, o[0][mt][2] * inv);
+              if (g == 0 && d.lse != nullptr) *d.lse = lse;
+            } else {
+#pragma unroll
+              for (int mt = 0; mt < 8; ++mt)
+                *reinterpret_cast<float2*>(d.po + 16 * mt + 2 * g) =
+                    make_float2(o[0][mt][0] * inv, o[0][mt][2] * inv);
+              if (g == 0) *d.plse = lse;
+            }
+          }
+          l[0][0] = l[0][1];
+          mu[0][0] = mu[0][1];
+#pragma unroll
+          for (int mt = 0; mt < 8; ++mt) {
+            o[0][mt][0] = o[0][mt][1];
+            o[0][mt][2] = o[0][mt][3];
+          }
+        }
+      }
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {            // the second n-tile's turn
+        l[0][e] = l[NT - 1][e];
+        mu[0][e] = mu[NT - 1][e];
+        top[0][e] = top[NT - 1][e];
+      }
+#pragma unroll
+      for (int mt = 0; mt < 8; ++mt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) o[0][mt][e] = o[NT - 1][mt][e];
     }
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float sum = l[nt][e];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        const int rr = 8 * nt + 2 * c + e;
-        if (rr >= R) continue;
-        const int t = rr / a.group, gi = rr - t * a.group;
-        const RowDest d = row_dest<HPC>(a, seg, t, hh, gi);
-        // a sum of 0: no visible key; NaN goes through
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const float lse = sum == 0.f ? -INFINITY : (mu[nt][e] + log2f(sum)) * kLn2;
-        if (d.out != nullptr) {
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
-            *reinterpret_cast<uint32_t*>(d.out + 16 * mt + 2 * g) =
-                pack_bf16x2(o[nt][mt][e] * inv, o[nt][mt][2 + e] * inv);
-          if (g == 0 && d.lse != nullptr) *d.lse = lse;
-        } else {
-#pragma unroll
-          for (int mt = 0; mt < 8; ++mt)
-            *reinterpret_cast<float2*>(d.po + 16 * mt + 2 * g) =
-                make_float2(o[nt][mt][e] * inv, o[nt][mt][2 + e] * inv);
-          if (g == 0) *d.plse = lse;
-        }
-      }
   }
 }
 
