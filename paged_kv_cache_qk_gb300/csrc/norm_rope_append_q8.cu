@@ -136,7 +136,10 @@ struct Place {
 };
 
 __device__ __forceinline__ Place place(const AppendQ8Args& a, int64_t slot) {
-  const int64_t blk = slot / a.base.block_size;
+  // 32-bit where that holds it: a 64-bit division is ~100 instructions
+  const int64_t blk = slot <= 0xffffffffll
+                          ? static_cast<uint32_t>(slot) / static_cast<uint32_t>(a.base.block_size)
+                          : slot / a.base.block_size;
   const int in = static_cast<int>(slot - blk * a.base.block_size);
   Place p;
   p.code = blk * a.base.block_stride + in * a.base.slot_stride;
@@ -160,6 +163,7 @@ struct Smem {
   alignas(16) Grown grown[3][kMostGrown];
   int num_grown[3];
   alignas(16) int64_t slot[2 * kWindow + 1];   // of tokens window - 1 .. window + 31, -1: none
+  int64_t pos[2 * kWindow + 1];                // theirs; 0 where there is no token
 };
 
 // The half-warp's angles of position pos into its part of shared memory: from the
@@ -272,15 +276,17 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
   const NormRopeAppendArgs& n = a.base;
   const int tid = threadIdx.x, lane = tid & 31, l = tid & 15, hw = tid >> 4;
   const int t0 = blockIdx.x * kWindow;
-  // V: tokens window .. window + 31 with a slot; B: those that start a run
+  // of the tokens window .. window + 31, B: those that start a run; E: those, and those
+  // without a slot, so that a position of E, or 32, ends the run before it
   const int64_t my = sm.slot[lane + 1], before = sm.slot[lane];
-  const uint32_t V = __ballot_sync(0xffffffffu, my >= 0);
   const uint32_t B = __ballot_sync(
       0xffffffffu, my >= 0 && (before < 0 || before / kScaleGroup != my / kScaleGroup));
-  auto run_end = [&](int s) {
-    const uint32_t after = (B | ~V) & ~((2u << s) - 1u);
-    return after != 0u ? __ffs(after) - 1 : 2 * kWindow;
+  const uint32_t E = B | __ballot_sync(0xffffffffu, my < 0);
+  auto next_end = [&](uint32_t from) {         // the first of E among the bits `from`
+    const uint32_t e = E & from;
+    return e != 0u ? __ffs(e) - 1 : 2 * kWindow;
   };
+
   // head k of all chunks: maxima in buffer k % 2; grown groups in list k % 3,
   // rescaled at the next head's barrier and emptied at the one after
   int k = 0, list = 0;
@@ -288,19 +294,17 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
   uint32_t todo = B & 0xffffu;                 // runs that start in the window
 #pragma unroll 1
   while (todo != 0u) {                         // uniform over the CTA
-    // chunk [b, b + len): whole runs, at most 16 tokens; half-warp hw has b + hw
-    const int b = __ffs(todo) - 1;
-    int len = 0;
-    while (todo != 0u) {
-      const int e = run_end(__ffs(todo) - 1);
-      if (len > 0 && e - b > kWindow) break;
-      len = min(e - b, kWindow);
-      todo &= todo - 1u;
-    }
+    // chunk [b, end): whole runs that start in the window, at most 16 tokens;
+    // half-warp hw has token b + hw
+    const int b = __ffs(todo) - 1, most = min(b + kWindow, next_end(0xffffu << kWindow));
+    const uint32_t ends = E & ((2u << most) - 1u) & ~((2u << b) - 1u);   // b + 1 .. most
+    // none: more tokens than slots, some given twice
+    const int end = ends != 0u ? 31 - __clz(ends) : most;
+    todo &= ~0u << end;
     const int j = b + hw;
-    const bool active = hw < len && ((V >> j) & 1u);
+    const bool active = j < end && (((~E | B) >> j) & 1u);
     const int rs = active ? 31 - __clz(B & ((2u << j) - 1u)) : j;
-    const int re = active ? min(run_end(j), b + len) : j;
+    const int re = active ? min(next_end(~0u << j << 1), end) : j;
     const bool first = active && j == rs;
     uint32_t written = 0u;                     // slots of the group that the run writes
     if (rs + l < re) written = 1u << (sm.slot[rs + l + 1] & (kScaleGroup - 1));
@@ -308,7 +312,6 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
     for (int o = 8; o > 0; o >>= 1) written |= __shfl_xor_sync(0xffffffffu, written, o);
     const int peer = rs + l < re ? rs + l - b : -1;   // half-warp whose maximum this lane takes
     const int64_t tok = active ? t0 + j : 0;
-    if (kIsK) put_angles(n, sm, active ? n.positions[tok] : 0, computed, hw, l);
     // of head h: this lane's values, code chunk and scale
     const int64_t stride_h = kIsK ? n.k_stride_h : n.v_stride_h;
     const __nv_bfloat16* src =
@@ -328,6 +331,7 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
       x1w = __ldg(reinterpret_cast<const uint2*>(src + 64));
       if (!(written & 1u)) next_scale = *scale;
     }
+    if (kIsK) put_angles(n, sm, active ? sm.pos[j + 1] : 0, computed, hw, l);
 #pragma unroll 1
     for (int h = h0; h < h1; ++h, ++k) {
       float x0[4], x1[4], y[8];
@@ -414,10 +418,9 @@ norm_rope_append_q8_kernel(const __grid_constant__ AppendQ8Args a) {
     }
     sm.slot[tid] = slot < 0 ? -1 : slot;
     if (tid < 3) sm.num_grown[tid] = 0;
-    if (tid > 0) {
-      const int64_t pos = live ? n.positions[t] : 0;
-      outside = !(pos >= 0 && pos < n.table_positions);
-    }
+    const int64_t pos = live ? n.positions[t] : 0;
+    sm.pos[tid] = pos;
+    outside = tid > 0 && !(pos >= 0 && pos < n.table_positions);
   }
   const bool computed = __syncthreads_or(outside) != 0;
   if (computed) {
@@ -434,7 +437,7 @@ norm_rope_append_q8_kernel(const __grid_constant__ AppendQ8Args a) {
   if (q0 >= q1) return;
   const bool live = t0 + hw < n.num_tokens;
   const int64_t tok = live ? t0 + hw : 0;
-  put_angles(n, sm, live ? n.positions[tok] : 0, computed, hw, l);
+  put_angles(n, sm, sm.pos[hw + 1], computed, hw, l);
   float g0[4], g1[4];
   gains(n.gamma_q, l, g0, g1);
   const __nv_bfloat16* src = n.q + tok * n.q_stride_t;
