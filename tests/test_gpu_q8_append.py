@@ -288,3 +288,31 @@ def test_append_of_many_tokens_padding_bad_slots_and_non_finite_values(lib):
     check_appended(np.nan_to_num(v, nan=0.0, posinf=np.inf), s, *before["v"], code_bytes(c.v),
                    c.vs.cpu().numpy(), "e4m3", "v")
     assert bf16_ulp_distance(bits(q_out), oracle.f64_to_bf16_bits(q)).max() <= 1
+
+
+@pytest.mark.parametrize("fmt", CLASSES)
+def test_append_of_one_slot_given_twice_leaves_other_groups_right(lib, fmt):
+    """More tokens than slots in a group: its contents are undefined, every other
+    group's are those of a call without it."""
+    p = workloads.make_problem("q8", 16, 8, 128, 32, [60], 60, 3, 8, "cuda")
+    slots = torch.full((60,), -1, dtype=torch.int64)
+    slots[0:16] = torch.arange(16)               # group 0
+    slots[16:38] = 32 + torch.arange(22) % 16    # group 2, six slots twice
+    slots[38:44] = 80 + torch.arange(6)          # group 5
+    slots[50:60] = 20                            # group 1, one slot ten times
+    c, d = (Q8(p, fmt, 4, unused=None) for _ in range(2))
+    _run(lib, p, c, slots=slots.cuda(), q_out=torch.empty_like(p.q))
+    once = slots.clone()
+    once[16:38] = -1
+    once[50:60] = -1
+    before = _before(d)
+    q_out = torch.empty_like(p.q)
+    _run(lib, p, d, slots=once.cuda(), q_out=q_out)
+    torch.cuda.synchronize()
+    _check(p, d, before, q_out, slots=once)
+    keep = [0, 3, 4, 5]                          # groups whose contents are defined
+    for x, y in ((c.k, d.k), (c.v, d.v)):
+        x, y = (t.view(torch.uint8).reshape(6, 16, 8, 128)[keep] for t in (x, y))
+        assert torch.equal(x, y)
+    for x, y in ((c.ks, d.ks), (c.vs, d.vs)):
+        assert torch.equal(x.reshape(6, 8)[keep], y.reshape(6, 8)[keep])

@@ -258,3 +258,43 @@ def test_decode_tiny_rows_over_groups_of_the_smallest_scale(lib, fmt):
     q[1:6] *= 2.0 ** -110
     out, lse = _decode(lib, p, c, 1, q=q)
     check_attention(p, c, out, lse, fmt, q=q)
+
+
+def test_two_calls_at_once_on_two_streams(lib):
+    """Decode and prefill calls that overlap, each with a workspace of its own."""
+    p = _problem(16, 8, 5, 16, [3000, 900, 5, 40], 31)
+    c = Q8(p, "int8", 32)
+    want = {S: _decode(lib, p, c, S) for S in (0, 3)}
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    got = {}
+    for S, s in zip((0, 3), streams):
+        n = lib.decode_workspace_bytes(p.B, p.q_len, p.Hq, p.D, S)
+        got[S] = (torch.empty(n, dtype=torch.uint8, device="cuda"),
+                  torch.empty_like(want[S][0]), torch.empty_like(want[S][1]))
+    torch.cuda.synchronize()
+    for _ in range(20):
+        for S, s in zip((0, 3), streams):
+            ws, out, lse = got[S]
+            with torch.cuda.stream(s):
+                lib.paged_decode_q8(p.q, *c.args(), p.block_tables, p.seq_lens, out, q_len=p.q_len,
+                                    num_splits=S, max_seq_len_hint=p.max_seq_len, lse_out=lse,
+                                    workspace=ws)
+    torch.cuda.synchronize()
+    for S in (0, 3):
+        assert torch.equal(got[S][1].view(torch.int16), want[S][0].view(torch.int16))
+        assert torch.equal(got[S][2], want[S][1])
+
+
+@pytest.mark.parametrize("fmt", CLASSES)
+@pytest.mark.parametrize("S", [1, 2, 0])
+def test_odd_tiles_at_a_cut_inside_a_sequence(lib, fmt, S):
+    """Segments of an odd number of 16-key tiles: what follows the last one belongs to
+    the next split, and is counted once."""
+    p = _problem(16, 8, 1, 16, [16 * 7, 16 * 3 + 5, 16, 16 * 11 + 1], 33)
+    c = Q8(p, fmt, 34)
+    out, lse = _decode(lib, p, c, S, hint=16 * 6)    # splits of 3 pages
+    check_attention(p, c, out, lse, f"{fmt} S={S}")
+    p = _problem(8, 2, 4, 16, [16 * 7, 16 * 3 + 5], 35)
+    c = Q8(p, fmt, 36)
+    out, lse = _decode(lib, p, c, S, hint=16 * 6)
+    check_attention(p, c, out, lse, f"{fmt} S={S} GQA-4")
