@@ -46,12 +46,14 @@ namespace {
 
 constexpr int kWindow = 16;                    // tokens per CTA, one per half-warp
 constexpr int kThreads = kWindow * 16;
-// Many tokens: four CTAs share an SM at 64 registers and a head vector's share of
-// a window is cut so that three waves of them come (measured on 4 x 2048 tokens, 16
-// q and 8 kv heads, before the maxima went through shuffles: 42.8 us; two waves 44.6,
-// four 47.7; three CTAs an SM 46.7-50.8, two at 108 registers 57.2).  Few: two, without spills (64 tokens 5.1 us against 5.9).
-constexpr int kManyTokens = 1024;
-constexpr int kManyCtas = 4, kManyWaves = 3, kFewCtas = 2;
+// Many tokens: four CTAs share an SM at 64 registers, with a few spills; few: two,
+// without (16 q and 8 kv heads, 1024 tokens: 9.4 us with two, 10.7 with four; 1600:
+// 11.5, 11.9; 2048: 14.7, 14.0; 8192: 49.6, 37.4; three CTAs an SM 41.2).  A window's
+// head vectors are cut so that at most two waves of CTAs come (512 tokens 7.5 us, three
+// waves 9.8; 2048: 14.0, 17.0; 4096: 20.3, 22.7), or three where two would leave a CTA
+// more than a quarter of them (8192: 37.4 us, two waves 39.2).
+constexpr int kManyTokens = 2048;
+constexpr int kManyCtas = 4, kFewCtas = 2;
 static_assert(kWindow == kScaleGroup, "a run spans at most two windows");
 
 template <int kFormat>
@@ -480,11 +482,12 @@ cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& args, cudaStream_t st
   AppendQ8Args a = args;
   const int windows = (a.base.num_tokens + kWindow - 1) / kWindow;
   const int items = a.base.num_q_heads + 2 * a.base.num_kv_heads;
-  // enough parts for the wanted CTAs on 152 SMs, at most one head vector each
+  // parts of a window on 152 SMs, at least one head vector each
   const bool many = a.base.num_tokens >= kManyTokens;
-  const int ctas = 152 * (many ? kManyCtas * kManyWaves : 3 * kFewCtas);
-  const int want = (ctas + windows - 1) / windows;
-  a.parts = want < 1 ? 1 : (want > items ? items : want);
+  const int wave = 152 * (many ? kManyCtas : kFewCtas);
+  int want = 2 * wave / windows;
+  if (want < 4) want = (3 * wave + windows - 1) / windows;
+  a.parts = want > items ? items : want;
   const dim3 grid(windows, a.parts);
   if (a.format == kFormatE4m3)
     return launch_pdl(many ? norm_rope_append_q8_kernel<kFormatE4m3, kManyCtas>
