@@ -351,10 +351,11 @@ PKVQK_API pkvqk_status pkvqk_paged_decode(
 
 /*
  * pkvqk_paged_decode over an 8-bit cache: the same definition with K_n and V_n
- * = code * scale, the same schedules, pkvqk_choose_num_splits and
- * pkvqk_decode_workspace_bytes.  Codes and q enter the products exactly (q is
- * scaled by a power of two per row first), sums are fp32, softmax weights are
- * rounded to 2^-11.  Slots at or past seq_lens[b] may hold any code and scale;
+ * = code * scale, the same schedules (the balanced one with a CTA per SM),
+ * pkvqk_choose_num_splits and pkvqk_decode_workspace_bytes.  Codes and q enter
+ * the products exactly (a q row is scaled by a power of two first; only what is
+ * 2^-28 below its largest magnitude is rounded), sums are fp32, softmax weights
+ * are rounded to 2^-11.  Slots at or past seq_lens[b] may hold any code and scale;
  * an e4m3 NaN code of a visible V makes NaN of every row of its sequence and
  * kv head.
  * More than 16 rows per kv head run as pkvqk_paged_prefill_q8 does.

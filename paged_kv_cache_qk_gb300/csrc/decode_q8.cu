@@ -32,11 +32,12 @@
 // One warp per kv head at 8 heads a CTA, else two: they take the pairs in turn and
 // merge at the end of a segment through shared memory.  The producer warp issues
 // one TMA box for K and one for V per 16-key tile into the ring.  Scales are read
-// by the consumer warps, one tile per lane, 32 tiles ahead.
+// by the consumer warps, one tile per lane, 32 tiles ahead (by the producer warp they
+// held its boxes up every 32 tiles: 206 us against 158 on 64 x 8192).
 //
-// Measured: 64 sequences x 8192 keys, 16 q and 8 kv heads, 158 us = 6.80 TB/s (a plain
+// Measured: 64 sequences x 8192 keys, 16 q and 8 kv heads, 157 us = 6.85 TB/s (a plain
 // copy 6.77; the bf16 cache 301 us); 8 x 32768 83 us = 6.47 TB/s; 64 mixed lengths at
-// 32 q and 4 kv heads 51 us = 4.7 TB/s; 32 x 5 rows 75.7 us = 4.1 TB/s, where a warp's
+// 32 q and 4 kv heads 51 us = 4.7 TB/s; 32 x 5 rows 75 us = 4.2 TB/s, where a warp's
 // instructions for two n-tiles bound it.
 #include "decode_schedule.cuh"
 #include "q8_common.cuh"

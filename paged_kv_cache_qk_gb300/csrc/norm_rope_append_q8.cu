@@ -28,9 +28,9 @@
 // load while a head is being quantised.
 //
 // Bound, many tokens: instructions and the latencies between them, not HBM (4 x 2048
-// tokens, 16 q and 8 kv heads: 37.7 us where the bytes need 17.4; ~210 instructions a
-// warp and head vector against the bf16 append's 150).  Few tokens: the chain slots -> angles, values, scales -> maxima -> codes
-// (64 tokens 4.0 us, the bf16 append 2.5).  A value nearer the middle of two codes
+// tokens, 16 q and 8 kv heads: 37.7 us where the bytes need 17.4; 205 instructions a
+// warp and head vector against the bf16 append's 150, issue slots 62 % busy).  Few tokens: the chain slots -> angles, values, scales -> maxima -> codes
+// (64 tokens 4.1 us, the bf16 append 2.5).  A value nearer the middle of two codes
 // than the fp32 norm's and rotation's 2^-20 may get either code; deciding those in
 // float64 cost 3 us more, 5 us on 160 tokens.
 #include <cuda_fp16.h>
