@@ -4,6 +4,7 @@
 
 #include <cudaTypedefs.h>
 
+#include <climits>
 #include <cstring>
 #include <mutex>
 
@@ -75,7 +76,9 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap,
   // sequence (fresh 4 x 2048 tokens 106 -> 90 us, 1 x 4096 103 -> 69, 3 x 1500 after 700
   // 86 -> 70, 8 x 1024 after 1024 238 -> 228).  Else the row tiles of a sequence
   // together: 8 x 512 after 0 to 6144, 4 kv heads, 215 us against 238.
-  a.mt_major = a.cu_seqlens_q != nullptr || (kFormat != 0 && 2ll * a.q_len >= a.longest) ? 1 : 0;
+  const long long gx = static_cast<long long>(a.m_tiles) * a.num_kv_heads * a.num_splits;
+  const bool mostly_new = kFormat != 0 && 2ll * a.q_len >= a.longest && gx * a.batch <= INT_MAX;
+  a.mt_major = a.cu_seqlens_q != nullptr || mostly_new ? 1 : 0;
   a.group_shift = -1;
   if (a.group > 0 && (a.group & (a.group - 1)) == 0)
     for (int s = 0; s < 31; ++s)
@@ -86,7 +89,6 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap,
              encode_rows_map(&omap, a.out, a.total_q, a.num_q_heads, kHeadDim * 2,
                              static_cast<long long>(a.num_q_heads) * kHeadDim * 2, a.group))
                 ? 1 : 0;
-  const long long gx = static_cast<long long>(a.m_tiles) * a.num_kv_heads * a.num_splits;
   return launch_pdl(kern, dim3(static_cast<unsigned>(gx), a.batch),
                     dim3(kThreads), kSmemBytes<kFormat>, stream, kmap, vmap, qmap, omap, a);
 }
