@@ -228,9 +228,10 @@ PKVQK_API pkvqk_status pkvqk_norm_rope_append_cached(
  *   2^e, e the smallest integer in -64 .. 63 with a <= M*2^e (at most 63)
  *   scale = 2^e                        where slot 0 of the group is written,
  *         = max(2^e, stored scale)     elsewhere: the group holds earlier tokens
- *   code  = value / scale, to the nearest code, ties to even (K's values come
- *           from an fp32 norm and rotation: one within 2^-20 of itself of the
- *           middle between two codes may get either)
+ *   code  = value / scale, to the nearest code, ties to even (in calls of 2048
+ *           tokens and more K's values come from an fp32 norm and rotation, and
+ *           one within 2^-20 of itself of the middle between two codes may get
+ *           either; so may, in any call, a subnormal e4m3 code)
  * and where the stored scale grew, the codes of the group's other slots are
  * rescaled (code * old / new, to the nearest), so that earlier tokens keep
  * their values.  Writing slot 0 starts a group anew: what other slots of it

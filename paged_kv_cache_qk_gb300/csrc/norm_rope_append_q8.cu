@@ -29,10 +29,12 @@
 //
 // Bound, many tokens: instructions and the latencies between them, not HBM (4 x 2048
 // tokens, 16 q and 8 kv heads: 37.7 us where the bytes need 17.4; 205 instructions a
-// warp and head vector against the bf16 append's 150, issue slots 62 % busy).  Few tokens: the chain slots -> angles, values, scales -> maxima -> codes
-// (64 tokens 4.1 us, the bf16 append 2.5).  A value nearer the middle of two codes
-// than the fp32 norm's and rotation's 2^-20 may get either code; deciding those in
-// float64 cost 3 us more, 5 us on 160 tokens, in pairs of floats 5 us more and 1.
+// warp and head vector against the bf16 append's 150, issue slots 62 % busy).  Few
+// tokens: the chain slots -> angles, values, scales -> maxima -> codes (64 tokens 4.1
+// us, the bf16 append 2.5).  A K value nearer the middle of two codes than the fp32
+// norm's and rotation's 2^-20 could get either code; settling those in pairs of floats
+// costs calls of few tokens 0.1 us (64) to 0.9 (32 x 5), and is done there; many tokens
+// 5 us of 38, for the registers it takes, and is not.
 #include <cuda_fp16.h>
 
 #include "device_common.cuh"
@@ -257,22 +259,100 @@ __device__ __forceinline__ float group_scale(float m, float stored, uint32_t wri
   return (written & 1u) ? want : fmaxf(want, *prev);
 }
 
-// The lane's eight values as codes (dims 4l.. at `code`, 64 + 4l.. 64 bytes on);
-// returns 1 / scale, exact for a power of two.
+// Is one of z = y / scale so near the middle of two codes that the fp32 norm and
+// rotation may have taken it across?  They are within 13 half-ulps of y (the sum of
+// squares 12 roundings deep, halved by the square root: 6; the mean 1, the square root
+// 4, the difference and the product 2).  e4m3: the 20 bits below a code's mantissa
+// against their middle (subnormal codes, 2^-14 of the group's maximum, are left as
+// they are).
 template <int kFormat>
-__device__ __forceinline__ float write_codes(const float (&y)[8], float scale, uint8_t* code) {
-  const float inv = __frcp_rn(scale);
-  const uint64_t inv2 = pack2(inv, inv);
-  float z[8];
+__device__ __forceinline__ bool near_middle(const float (&z)[8]) {
+  if (kFormat == kFormatE4m3) {
+    uint32_t d = ~0u;
 #pragma unroll
-  for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(y[e], y[e + 1]), inv2), z[e], z[e + 1]);
+    for (int e = 0; e < 8; ++e) d = min(d, (__float_as_uint(z[e]) - (0x80000u - 14u)) & 0xfffffu);
+    return d <= 28u;
+  }
+  constexpr float kRound = 12582912.f;         // 1.5 * 2^23: its unit is 1
+  const uint64_t up = pack2(kRound, kRound);
+  float m = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; e += 2) {
+    const uint64_t v = pack2(z[e], z[e + 1]);
+    float d0, d1;
+    unpack2(sub2(v, sub2(add2(v, up), up)), d0, d1);
+    m = fmaxf(m, fmaf(fabsf(z[e]), 14.f * 0x1p-24f, fabsf(d0)));
+    m = fmaxf(m, fmaf(fabsf(z[e + 1]), 14.f * 0x1p-24f, fabsf(d1)));
+  }
+  return m >= 0.5f;
+}
+
+// The lane's eight values as codes (dims 4l.. at `code`, 64 + 4l.. 64 bytes on).
+template <int kFormat>
+__device__ __forceinline__ void write_codes(const float (&z)[8], uint8_t* code) {
   *reinterpret_cast<uint32_t*>(code) = encode4<kFormat>(z[0], z[1], z[2], z[3]);
   *reinterpret_cast<uint32_t*>(code + 64) = encode4<kFormat>(z[4], z[5], z[6], z[7]);
-  return inv;
+}
+
+// hi + lo to float by truncation, the lowest bit set where something was cut off: a
+// rounding to 8 bits that follows is that of the sum.
+__device__ __forceinline__ float to_odd(float hi, float lo) {
+  uint32_t u = __float_as_uint(hi);
+  if (lo == 0.f || hi == 0.f) return hi;
+  if ((lo < 0.f) != (hi < 0.f)) --u;           // towards zero
+  return __uint_as_float(u | 1u);
+}
+
+// The codes of one K head vector by a half-warp from the norm and rotation in pairs of
+// floats (2^-40), for the ~0.5 % of vectors with a value that fp32 leaves in doubt.
+// inv: 1 / scale.
+template <int kFormat>
+__device__ __noinline__ void settle_codes(const NormRopeAppendArgs& n, const Smem& sm,
+                                          const __nv_bfloat16* src, float inv, uint8_t* code) {
+  const int l = threadIdx.x & 15, hw = threadIdx.x >> 4;
+  const uint32_t half = 0xffffu << (threadIdx.x & 16);
+  float x0[4], x1[4], g0[4], g1[4], z[8];
+  unpack4(__ldg(reinterpret_cast<const uint2*>(src)), x0);
+  unpack4(__ldg(reinterpret_cast<const uint2*>(src + 64)), x1);
+  unpack4(__ldg(reinterpret_cast<const uint2*>(n.gamma_k + 4 * l)), g0);
+  unpack4(__ldg(reinterpret_cast<const uint2*>(n.gamma_k + 64 + 4 * l)), g1);
+  FF ss = {0.f, 0.f};                          // squares of bf16 values are exact
+#pragma unroll
+  for (int j = 0; j < 8; ++j) {
+    const float x = j < 4 ? x0[j & 3] : x1[j & 3];
+    const FF t = two_sum(ss.hi, PKVQK_MUL(x, x));
+    ss = {t.hi, PKVQK_ADD(ss.lo, t.lo)};
+  }
+#pragma unroll 1
+  for (int o = 8; o > 0; o >>= 1)
+    ss = ff_add(ss, {__shfl_xor_sync(half, ss.hi, o), __shfl_xor_sync(half, ss.lo, o)});
+  const FF m = ff_add({ss.hi * (1.f / kHeadDim), ss.lo * (1.f / kHeadDim)}, {n.eps, 0.f});
+  // one Newton step in pairs from the fp32 root
+  const float r0 = rsqrtf(m.hi);
+  const FF t = ff_mul(m, ff_mul({r0, 0.f}, {r0, 0.f}));
+  const FF r = {r0, 0.5f * r0 * PKVQK_SUB(PKVQK_SUB(1.f, t.hi), t.lo)};
+  bool finite = true;
+#pragma unroll 1
+  for (int half_of = 0; half_of < 2; ++half_of) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const FF c = {sm.trig[0][hw][4 * l + j], sm.trig[1][hw][4 * l + j]};
+      const float sign = half_of ? 1.f : -1.f;
+      const FF w = {sign * sm.trig[2][hw][4 * l + j], sign * sm.trig[3][hw][4 * l + j]};
+      const float a = x0[j] * g0[j], b = x1[j] * g1[j];   // exact
+      // first half a c - b s, second b c + a s
+      const FF y = ff_mul(r, ff_add(ff_mul({half_of ? b : a, 0.f}, c), ff_mul({half_of ? a : b, 0.f}, w)));
+      const float v = to_odd(y.hi * inv, y.lo * inv);
+      finite = finite && fabsf(y.hi * inv) <= 3.402823466e38f;
+      z[j] = half_of ? z[j] : v;
+      z[4 + j] = v;
+    }
+  }
+  if (finite) write_codes<kFormat>(z, code);   // else those of fp32 stay
 }
 
 // K (kIsK) or V of kv heads [h0, h1): the runs that start in the window.
-template <int kFormat, bool kIsK>
+template <int kFormat, bool kIsK, bool kFew>
 __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bool computed,
                                              int h0, int h1) {
   const NormRopeAppendArgs& n = a.base;
@@ -374,7 +454,15 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
       if (active) {
         float prev;
         const float now = group_scale<kFormat>(m, stored, written, &prev);
-        const float inv = write_codes<kFormat>(y, now, code);
+        const float inv = __frcp_rn(now);      // exact for a power of two
+        const uint64_t inv2 = pack2(inv, inv);
+        float z[8];
+#pragma unroll
+        for (int e = 0; e < 8; e += 2) unpack2(mul2(pack2(y[e], y[e + 1]), inv2), z[e], z[e + 1]);
+        write_codes<kFormat>(z, code);
+        // V is not rounded before
+        if (kIsK && kFew && __any_sync(0xffffu << (threadIdx.x & 16), near_middle<kFormat>(z)))
+          settle_codes<kFormat>(n, sm, src - stride_h, inv, code);
         if (first && l == 0) {
           *scale = now;
           if (!(written & 1u) && now > prev)
@@ -430,9 +518,10 @@ norm_rope_append_q8_kernel(const __grid_constant__ AppendQ8Args a) {
       (&sm.knots[0][0])[e] = (&n.sincos_tab[0][0])[e];
     __syncthreads();
   }
-  if (i0 < hkv) append_heads<kFormat, true>(a, sm, computed, i0, min(i1, hkv));
+  constexpr bool kFew = kMinCtas == kFewCtas;
+  if (i0 < hkv) append_heads<kFormat, true, kFew>(a, sm, computed, i0, min(i1, hkv));
   if (i0 < 2 * hkv && i1 > hkv)
-    append_heads<kFormat, false>(a, sm, computed, max(i0 - hkv, 0), min(i1 - hkv, hkv));
+    append_heads<kFormat, false, kFew>(a, sm, computed, max(i0 - hkv, 0), min(i1 - hkv, hkv));
 
   // ---- q heads of this part
   const int q0 = max(i0 - 2 * hkv, 0), q1 = i1 - 2 * hkv;

@@ -316,3 +316,23 @@ def test_append_of_one_slot_given_twice_leaves_other_groups_right(lib, fmt):
         assert torch.equal(x, y)
     for x, y in ((c.ks, d.ks), (c.vs, d.vs)):
         assert torch.equal(x.reshape(6, 8)[keep], y.reshape(6, 8)[keep])
+
+
+@pytest.mark.parametrize("fmt", CLASSES)
+def test_append_below_2048_tokens_gives_the_nearest_codes(lib, fmt):
+    """1.2 million K values, some within an fp32 norm's error of the middle between two
+    codes: each code is the float64 value's (subnormal e4m3 codes aside)."""
+    p = workloads.make_problem("q8", 1, 8, 128, 16, [1200], 1200, 76, 17, "cuda")
+    c = Q8(p, fmt, 5, unused=None)
+    before = _before(c)
+    _run(lib, p, c, q_out=torch.empty_like(p.q))
+    torch.cuda.synchronize()
+    k = _exact(p)[1]
+    want, scales = oracle.q8_append(k, p.slot_mapping.cpu().numpy(), *before["k"], fmt)
+    assert np.array_equal(scales, c.ks.double().cpu().numpy())
+    got = oracle.q8_values(code_bytes(c.k), fmt)
+    same = got == want
+    if fmt == "e4m3":
+        same |= np.maximum(np.abs(got), np.abs(want)) < 2.0 ** -6
+    same |= np.isnan(got) & np.isnan(want)
+    assert same.all(), f"{(~same).sum()} codes"
