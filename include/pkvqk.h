@@ -243,8 +243,8 @@ PKVQK_API pkvqk_status pkvqk_norm_rope_append_cached(
  * Tokens of one call whose slots lie in one group must be adjacent in token
  * order (as the consecutive tokens of a sequence are), with no other token and
  * no padding between them; otherwise, as when two tokens share a slot, the
- * group's contents are undefined.  Results do not depend on how a sequence's
- * other groups are spread over calls.
+ * group's contents are undefined.  Such near-ties aside, results do not depend
+ * on how a sequence's other groups are spread over calls.
  *
  *   q, k, v, positions, slot_mapping, gamma_q/_k, theta, eps: as
  *   pkvqk_norm_rope_append; q_out as q (own strides); rope_table as
