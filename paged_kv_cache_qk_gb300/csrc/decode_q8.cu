@@ -29,8 +29,9 @@
 //  * two tiles go through a warp at once, so that one's loads and conversions fill
 //    the latencies of the other's products (a tile alone takes a warp ~1050 cycles,
 //    a pair ~1850; 64 sequences of mixed lengths, 4 kv heads: 68.9 -> 59.5 us).
-// One warp per kv head at 8 heads a CTA, else two: they take the pairs in turn and
-// merge at the end of a segment through shared memory.  The producer warp issues
+// One warp per kv head at 8 heads a CTA, else two: they take the pairs in turn, by
+// their place in the ring (decode_q8_ring.cuh), and merge at the end of a segment
+// through shared memory.  The producer warp issues
 // one TMA box for K and one for V per 16-key tile into the ring.  Scales are read
 // by the consumer warps, one tile per lane, 32 tiles ahead (by the producer warp they
 // held its boxes up every 32 tiles: 206 us against 158 on 64 x 8192).
@@ -39,6 +40,7 @@
 // copy 6.77; the bf16 cache 301 us); 8 x 32768 83 us = 6.47 TB/s; 64 mixed lengths at
 // 32 q and 4 kv heads 51 us = 4.7 TB/s; 32 x 5 rows 75 us = 4.2 TB/s, where a warp's
 // instructions for two n-tiles bound it.
+#include "decode_q8_ring.cuh"
 #include "decode_schedule.cuh"
 #include "q8_common.cuh"
 
@@ -53,32 +55,18 @@ constexpr float kHeadroom = 4.f;               // log2 by which a score may pass
 constexpr float kBias = 10.f;                  // P' = 2^(x - m + kBias) <= 2^14
 
 template <int HPC, int NT>
-struct GeometryQ8 {
-  static constexpr int kSplit = HPC == 8 ? 1 : 2;     // consumer warps per head
-  static constexpr int kConsumers = HPC * kSplit;
-  // With 9 to 16 rows and nine warps a CTA (168 registers) the q fragments, 32
-  // registers, are read from shared memory, [k-step][n-tile][lane] of each warp:
-  // pairs of tiles then spill ~30 registers at their edges and still beat single
-  // tiles (32 x 5 rows of 4 a kv head, 7 splits: 84.5 -> 75.5 us).
-  static constexpr bool kQInSmem = NT == 2 && kConsumers == 8;
-  static constexpr int kQBytes = kQInSmem ? 8 * NT * 32 * 8 : 0;
-  static constexpr int kBudgetKb = HPC >= 4 ? 192 : (HPC == 2 ? 96 : 64);
-  static constexpr int kStageBytes = 2 * HPC * kHeadTileBytes;
-  static constexpr int kRaw = kBudgetKb * 1024 / kStageBytes;
-  static constexpr int kMostStages = kQInSmem ? 10 : 12;
-  static constexpr int kStages = kRaw > kMostStages ? kMostStages : kRaw;
+struct GeometryQ8 : RingQ8<HPC, NT> {
+  using Ring = RingQ8<HPC, NT>;
+  static_assert(Ring::kStageBytes == 2 * HPC * kHeadTileBytes, "a stage holds K and V of a tile");
+  static constexpr int kQBytes = Ring::kQInSmem ? 8 * NT * 32 * 8 : 0;
   // one n-tile of a warp's result, per head: O, then (l, mu, top) of two rows a lane
-  static constexpr int kMergeBytes = kSplit > 1 ? 32 * (32 + 6) * 4 : 0;
-  static constexpr int kOffMerge = kStages * kStageBytes;
+  static constexpr int kMergeBytes = Ring::kSplit > 1 ? 32 * (32 + 6) * 4 : 0;
+  static constexpr int kOffMerge = Ring::kStages * Ring::kStageBytes;
   static constexpr int kOffQ = kOffMerge + HPC * kMergeBytes;
-  static constexpr int kSmemBytes = kOffQ + kConsumers * kQBytes + 1024;
+  static constexpr int kSmemBytes = kOffQ + Ring::kConsumers * kQBytes + 1024;
   static_assert(kSmemBytes <= 227 * 1024, "shared memory");
-  static constexpr int kThreads = (kConsumers + 1) * 32;
+  static constexpr int kThreads = (Ring::kConsumers + 1) * 32;
 };
-
-// A segment's tiles in whole pairs (the consumers take two at once): an odd one is
-// followed by one of zeros, whose keys nobody sees.
-__device__ __forceinline__ int paired(int ntiles) { return (ntiles + 1) & ~1; }
 
 // ----------------------------------------------------------------- producer
 
@@ -487,7 +475,7 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
         iv_l = __frcp_rn(vs);
         next = tile_scales(a, sv, seg, kvh, i + 32 + lane);
       }
-      if (kSplit > 1 && (i / U) % kSplit != part) continue;   // the other warp's
+      if (kSplit > 1 && pair_owner(it0 + i, kSplit) != part) continue;   // the other warp's
       if (!pair(i)) {
         *abort_flag = 1;
         report(a.status_flags, kFlagTimeout);
