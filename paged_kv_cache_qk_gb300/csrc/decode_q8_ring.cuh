@@ -45,3 +45,5 @@ PKVQK_HD constexpr int paired(int ntiles) { return (ntiles + 1) & ~1; }
 PKVQK_HD constexpr int pair_owner(int at, int split) { return at / 2 % split; }
 
 }  // namespace pkvqk
+
+#undef PKVQK_HD

@@ -4,7 +4,6 @@
 
 #include <cudaTypedefs.h>
 
-#include <climits>
 #include <cstring>
 #include <mutex>
 
@@ -77,8 +76,8 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap,
   // 86 -> 70, 8 x 1024 after 1024 238 -> 228).  Else the row tiles of a sequence
   // together: 8 x 512 after 0 to 6144, 4 kv heads, 215 us against 238.
   const long long gx = static_cast<long long>(a.m_tiles) * a.num_kv_heads * a.num_splits;
-  const bool mostly_new = kFormat != 0 && 2ll * a.q_len >= a.longest && gx * a.batch <= INT_MAX;
-  a.mt_major = a.cu_seqlens_q != nullptr || mostly_new ? 1 : 0;
+  const bool mostly_new = kFormat != 0 && 2ll * a.q_len >= a.longest;
+  a.mt_major = row_tile_major(a.cu_seqlens_q != nullptr || mostly_new, gx, a.batch) ? 1 : 0;
   a.group_shift = -1;
   if (a.group > 0 && (a.group & (a.group - 1)) == 0)
     for (int s = 0; s < 31; ++s)
