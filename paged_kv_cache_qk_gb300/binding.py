@@ -393,6 +393,7 @@ def paged_prefill_varlen(q, cu_seqlens_q, max_q_len, k_cache, v_cache, block_tab
 _Q8_PACK = struct.Struct("=4Qq4i3q2i3q")       # pkvqk_q8_cache, no padding
 assert _Q8_PACK.size == ctypes.sizeof(Q8Cache)
 _q8 = {}                                       # torch names, filled on first use
+_ROPE_ROW_BYTES = pkvqk_rope_table_bytes(1)
 
 
 def _q8_names():
@@ -456,11 +457,17 @@ def q8_cache(k_cache, v_cache, k_scales, v_scales) -> Q8Cache:
 
 def _heads(t, x, name):
     """(tokens, heads, token stride, head stride) of a [tokens, heads, head_dim] view."""
-    n, h, _ = x.shape
+    n, h, d = x.shape
     s0, s1, s2 = x.stride()
-    if x.dtype is not t["bf16"] or s2 != 1:
-        raise ValueError(f"{name} must be bfloat16 with head_dim the contiguous axis")
+    if x.dtype is not t["bf16"] or d != 128 or s2 != 1:
+        raise ValueError(f"{name} must be bfloat16 with a head_dim of 128, the contiguous axis")
     return n, h, s0, s1
+
+
+def _gains(t, x, name):
+    if x.dtype is not t["bf16"] or x.numel() != 128 or not x.is_contiguous():
+        raise ValueError(f"{name} must be 128 contiguous bfloat16 values")
+    return x.data_ptr()
 
 
 def _ints(x, dtype, n, name):
@@ -480,6 +487,23 @@ def _results(t, out, lse_out, rows, heads):
             or lse_out.numel() < rows * heads:
         raise ValueError("lse_out must be contiguous float32, one value per row and head")
     return out.data_ptr(), lse_out.data_ptr()
+
+
+def _flags(t, x):
+    if x is None:
+        return 0
+    if x.dtype is not t["i32"] or x.numel() < 1:
+        raise ValueError("status_flags must be int32")
+    return x.data_ptr()
+
+
+def _workspace(x):
+    """Pointer and bytes of a workspace (or None)."""
+    if x is None:
+        return 0, 0
+    if not x.is_contiguous():
+        raise ValueError("workspace must be contiguous")
+    return x.data_ptr(), x.nbytes
 
 
 def _table(t, block_tables, batch):
@@ -509,14 +533,16 @@ def norm_rope_append_q8(q, k, v, positions, slot_mapping, gamma_q, gamma_k, thet
     Tv, Hv, vs, vh = _heads(t, v, "v")
     if (To, Ho) != (T, Hq) or Tk != T or Tv != T or Hk != Hv or Hk != k_cache.shape[2]:
         raise ValueError("q, q_out, k and v must agree in tokens, and k, v and the cache in heads")
-    if gamma_q.dtype is not t["bf16"] or gamma_k.dtype is not t["bf16"]:
-        raise ValueError("gamma_q and gamma_k must be bfloat16")
+    if rope_table is not None and (not rope_table.is_contiguous()
+                                   or rope_table.nbytes < table_positions * _ROPE_ROW_BYTES):
+        raise ValueError(f"rope_table must be contiguous and hold {table_positions} positions")
     check(_append_q8(
         q.data_ptr(), qs, qh, q_out.data_ptr(), os_, oh, k.data_ptr(), ks, kh,
         v.data_ptr(), vs, vh, _ints(positions, t["i64"], T, "positions"),
-        _ints(slot_mapping, t["i64"], T, "slot_mapping"), gamma_q.data_ptr(), gamma_k.data_ptr(),
-        theta, eps, T, Hq, _pack_q8(t, k_cache, v_cache, k_scales, v_scales),
-        _ptr(rope_table), table_positions, _ptr(status_flags), _raw_stream(t, stream, q)))
+        _ints(slot_mapping, t["i64"], T, "slot_mapping"), _gains(t, gamma_q, "gamma_q"),
+        _gains(t, gamma_k, "gamma_k"), theta, eps, T, Hq,
+        _pack_q8(t, k_cache, v_cache, k_scales, v_scales), _ptr(rope_table), table_positions,
+        _flags(t, status_flags), _raw_stream(t, stream, q)))
 
 
 def _attend_q8(f, q, caches, block_tables, seq_lens, out, q_len, num_splits, max_seq_len_hint,
@@ -531,8 +557,7 @@ def _attend_q8(f, q, caches, block_tables, seq_lens, out, q_len, num_splits, max
     check(f(
         q.data_ptr(), qs, qh, _pack_q8(t, *caches), table, width,
         _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, q_len, Hq, num_splits,
-        max_seq_len_hint, scale, o, lse, _ptr(workspace),
-        0 if workspace is None else workspace.nbytes, _ptr(status_flags),
+        max_seq_len_hint, scale, o, lse, *_workspace(workspace), _flags(t, status_flags),
         _raw_stream(t, stream, q)))
 
 
@@ -568,5 +593,5 @@ def paged_prefill_varlen_q8(q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scal
         q.data_ptr(), qs, qh, _ints(cu_seqlens_q, t["i32"], batch + 1, "cu_seqlens_q"), max_q_len,
         total_q, _pack_q8(t, k_cache, v_cache, k_scales, v_scales), table, width,
         _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, Hq, num_splits, max_seq_len_hint,
-        scale, o, lse, _ptr(workspace), 0 if workspace is None else workspace.nbytes,
-        _ptr(status_flags), _raw_stream(t, stream, q)))
+        scale, o, lse, *_workspace(workspace), _flags(t, status_flags),
+        _raw_stream(t, stream, q)))
