@@ -108,13 +108,14 @@ __device__ __forceinline__ float max_abs3(float a, float b, float c) {
 }
 
 // The largest |y| of eight values; where that is not finite, NaN in y becomes 0
-// (which is how it is stored), infinities do not count, and the result is of the
-// finite ones.
-__device__ __forceinline__ float max_finite(float (&y)[8], bool& bad) {
+// (which is how it is stored), infinities do not count, the result is of the finite
+// ones, and `bad` is set if the values are a token's (the zeros of a half-warp without
+// one become NaN where eps is 0).
+__device__ __forceinline__ float max_finite(float (&y)[8], bool token, bool& bad) {
   float m = max_abs3(max_abs3(0.f, y[0], y[1]), y[2], y[3]);
   m = max_abs3(max_abs3(m, y[4], y[5]), y[6], y[7]);
   if (!(m <= 3.402823466e38f)) {
-    bad = true;
+    bad = bad || token;
     m = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
@@ -442,7 +443,7 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
           y[4 + e] = x1[e];
         }
       }
-      float m = max_finite(y, bad);
+      float m = max_finite(y, active, bad);
       m = half_warp_max(m);
       if (l == 0) sm.amax[k & 1][hw] = m;
       __syncthreads();
@@ -478,7 +479,7 @@ __device__ __forceinline__ void append_heads(const AppendQ8Args& a, Smem& sm, bo
   rescale<kFormat>(sm.grown[list], sm.num_grown[list], n.slot_stride, hw, l);
   __syncthreads();
   if (tid < 3) sm.num_grown[tid] = 0;          // for the next tensor (it has a barrier before use)
-  if (bad) report(n.status_flags, kFlagBadValue);   // inactive half-warps hold zeros
+  if (bad) report(n.status_flags, kFlagBadValue);
 }
 
 template <int kFormat, int kMinCtas>
