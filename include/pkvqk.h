@@ -306,7 +306,8 @@ PKVQK_API size_t pkvqk_decode_workspace_bytes(int32_t batch, int32_t q_len,
  *                 slot n % block_size
  *   s_n = scale * <q, K_n>   (scale <= 0 selects head_dim^-1/2)
  *   out = sum_n softmax(s)_n V_n,  lse = log sum_n exp(s_n)
- * A row with no visible key outputs 0 and lse = -inf.
+ * A row with no visible key outputs 0 and lse = -inf; a row with a NaN score is
+ * NaN, lse included.
  *
  * Schedules (the result does not depend on them, up to rounding):
  * - num_splits >= 1 (split-KV): with C = ceil(ceil(max_seq_len_hint /
@@ -436,7 +437,7 @@ PKVQK_API size_t pkvqk_static_workspace_capacity(void);
  *   M = max_j lse[r][j];  w_j = exp(lse[r][j] - M)
  *   out[r] = sum_j w_j o[r][j] / sum_j w_j,  lse_out[r] = M + log sum_j w_j
  * Splits with lse = -inf weigh 0; a row whose splits are all empty outputs
- * 0 and -inf.
+ * 0 and -inf, one with a split whose lse is NaN NaN.
  *   ws_o    device fp32 [rows][num_splits][head_dim]
  *   ws_lse  device fp32 [rows][num_splits]
  *   out     device bf16 [rows][head_dim];  lse_out device fp32 [rows] or NULL

@@ -16,9 +16,16 @@ namespace pkvqk {
 
 constexpr float kLog2e = 1.4426950408889634f;
 
+__device__ __forceinline__ float max_nan(float a, float b) {
+  float d;
+  asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+  return d;
+}
+
 // Merge of n partial rows at ws index base + j * stride (j < n) into one
 // bf16 output row (+ lse); one warp.  The partials come from the previous
-// kernel in the stream, so the read-only path may cache them.
+// kernel in the stream, so the read-only path may cache them.  A split whose lse
+// is NaN makes the row NaN; a row of empty splits (-inf) is 0 and -inf.
 __device__ __forceinline__ void combine_row(const float* __restrict__ ws_o,
                                             const float* __restrict__ ws_lse, long long base,
                                             long long stride, int n, __nv_bfloat16* out_row,
@@ -27,9 +34,9 @@ __device__ __forceinline__ void combine_row(const float* __restrict__ ws_o,
   auto ld_part4 = [](const float4* ptr) { return __ldg(ptr); };
   // pass 1: the row's max lse (lane j holds split j, j + 32, ...)
   float M = -INFINITY;
-  for (int j = lane; j < n; j += 32) M = fmaxf(M, ld_part(ws_lse + base + j * stride));
+  for (int j = lane; j < n; j += 32) M = max_nan(M, ld_part(ws_lse + base + j * stride));
 #pragma unroll
-  for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+  for (int off = 16; off > 0; off >>= 1) M = max_nan(M, __shfl_xor_sync(0xffffffffu, M, off));
 
   // pass 2: weights in the lanes that own the splits, partial rows summed
   // with 8 independent float4 loads in flight per lane
@@ -66,12 +73,12 @@ __device__ __forceinline__ void combine_row(const float* __restrict__ ws_o,
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1) wsum += __shfl_xor_sync(0xffffffffu, wsum, off);
   }
-  const float inv = wsum > 0.f ? 1.f / wsum : 0.f;
+  const float inv = wsum == 0.f ? 0.f : 1.f / wsum;
   uint2 packed;
   packed.x = pack_bf16x2(acc.x * inv, acc.y * inv);
   packed.y = pack_bf16x2(acc.z * inv, acc.w * inv);
   *reinterpret_cast<uint2*>(out_row + 4 * lane) = packed;
-  if (lane == 0 && lse_dst != nullptr) *lse_dst = wsum > 0.f ? M + logf(wsum) : -INFINITY;
+  if (lane == 0 && lse_dst != nullptr) *lse_dst = wsum == 0.f ? -INFINITY : M + logf(wsum);
 }
 
 

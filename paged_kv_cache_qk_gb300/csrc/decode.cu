@@ -283,7 +283,7 @@ __device__ void consume_simt(const DecodeArgs& a, const Plan* plan, const uint8_
       for (int rr = 0; rr < R; ++rr) {
         const int t = rr / a.group, gi = rr - t * a.group;
         const RowDest d = row_dest<HPC>(a, seg, t, hh, gi);
-        const float inv = l[rr] > 0.f ? 1.f / l[rr] : 0.f;
+        const float inv = inverse_sum(l[rr]);
         const float lse = final_lse(m[rr], l[rr]);
         if (d.out != nullptr) {
           uint4 w0, w1;
@@ -487,7 +487,7 @@ __device__ void consume_tc(const DecodeArgs& a, const Plan* plan, const uint8_t*
       const float m = half ? mB : mA;
       const int t = rr / a.group, gi = rr - t * a.group;
       const RowDest d = row_dest<HPC>(a, seg, t, hh, gi);
-      const float inv = l > 0.f ? 1.f / l : 0.f;
+      const float inv = inverse_sum(l);
       if (d.out != nullptr) {
 #pragma unroll
         for (int nt = 0; nt < 16; ++nt)

@@ -555,9 +555,7 @@ __device__ void consume_q8(const DecodeArgs& a, const ScaleView& sv, const Plan*
           if (rr < R) {
             const int t = rr / a.group, gi = rr - t * a.group;
             const RowDest d = row_dest<HPC>(a, seg, t, hh, gi);
-            // a sum of 0: no visible key; NaN goes through
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const float lse = sum == 0.f ? -INFINITY : (mu[0][0] + log2f(sum)) * kLn2;
+            const float inv = inverse_sum(sum), lse = final_lse(mu[0][0], sum);
             if (d.out != nullptr) {
 #pragma unroll
               for (int mt = 0; mt < 8; ++mt)

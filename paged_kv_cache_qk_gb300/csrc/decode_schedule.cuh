@@ -249,8 +249,10 @@ __device__ __forceinline__ RowDest row_dest(const DecodeArgs& a, const Segment& 
   return d;
 }
 
+// A row without a visible key has the sum l = 0; a NaN sum stays NaN.
 __device__ __forceinline__ float final_lse(float m, float l) {
-  return l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
+__device__ __forceinline__ float inverse_sum(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 }  // namespace pkvqk

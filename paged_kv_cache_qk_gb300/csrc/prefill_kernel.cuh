@@ -995,8 +995,9 @@ __device__ __forceinline__ void write_rows(const PrefillArgs& a, const Work& w, 
                           x * kN + half * (kHeadDim / 2);
   const int h = w.g * a.group + hh;
   const long long row = (w.q0 + t) * a.num_q_heads + h;
-  const float inv = l > 0.f ? 1.f / l : 0.f;
-  const float lse = l > 0.f ? (m_ref + log2f(l)) * kLn2 : -INFINITY;
+  // a sum of 0: no visible key; a NaN sum stays NaN
+  const float inv = l == 0.f ? 0.f : 1.f / l;
+  const float lse = l == 0.f ? -INFINITY : (m_ref + log2f(l)) * kLn2;
   const bool have_o = w.ntiles > 0;            // uniform over the CTA
   const int d0 = half * (kHeadDim / 2);
   // a whole row tile inside the sequence and inside out (uniform over the
