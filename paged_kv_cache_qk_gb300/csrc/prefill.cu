@@ -82,8 +82,10 @@ cudaError_t launch_format(const CUtensorMap& kmap, const CUtensorMap& vmap,
   if (a.group > 0 && (a.group & (a.group - 1)) == 0)
     for (int s = 0; s < 31; ++s)
       if ((1 << s) == a.group) a.group_shift = s;
-  a.q_tma = encode_rows_map(&qmap, a.q, a.total_q, a.num_q_heads, a.q_stride_h * 2,
-                            a.q_stride_t * 2, a.group) ? 1 : 0;
+  a.q_tma = 0;                                 // 8-bit: Q is loaded and turned into f16
+  if constexpr (kFormat == 0)
+    a.q_tma = encode_rows_map(&qmap, a.q, a.total_q, a.num_q_heads, a.q_stride_h * 2,
+                              a.q_stride_t * 2, a.group) ? 1 : 0;
   a.o_tma = (a.num_splits == 1 &&
              encode_rows_map(&omap, a.out, a.total_q, a.num_q_heads, kHeadDim * 2,
                              static_cast<long long>(a.num_q_heads) * kHeadDim * 2, a.group))

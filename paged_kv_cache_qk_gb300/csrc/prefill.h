@@ -38,8 +38,8 @@ struct PrefillArgs {
   float* ws_o;                     // num_splits > 1: [rows, S, 128] normalised partials
   float* ws_lse;                   // num_splits > 1: [rows, S]
   int32_t* status_flags;
-  // set by launch_paged_prefill: q rows arrive by TMA through qmap, and whole
-  // row tiles of out (num_splits == 1) leave by TMA through omap
+  // set by launch_paged_prefill: q rows arrive by TMA through qmap (bf16 caches), and
+  // whole row tiles of out (num_splits == 1) leave by TMA through omap
   int32_t q_tma, o_tma;
   // set by launch_paged_prefill: the grid runs over (row tile descending,
   // sequence, kv head, split) instead of (sequence, split, kv head, row tile
