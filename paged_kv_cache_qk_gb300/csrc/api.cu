@@ -714,7 +714,7 @@ pkvqk_status run_append_q8(const void* q, int64_t q_stride_t, int64_t q_stride_h
   a.v_codes = static_cast<uint8_t*>(cache->v);
   a.scales = scale_view(*cache);
   a.format = cache->format;
-  const cudaError_t e = pkvqk::launch_norm_rope_append_q8(a, stream);
+  const cudaError_t e = pkvqk::launch_norm_rope_append_q8(a, sm_count_current(), stream);
   if (e != cudaSuccess) return cuda_fail(e, "norm_rope_append_q8 launch");
   return ok();
 }

@@ -69,7 +69,7 @@ struct AppendQ8Args {
   int32_t parts;                   // set by the launch: CTAs that share a window's heads
 };
 
-cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& a, cudaStream_t stream);
+cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& a, int sm_count, cudaStream_t stream);
 
 struct DecodeArgs {
   const __nv_bfloat16* q;

@@ -567,14 +567,15 @@ norm_rope_append_q8_kernel(const __grid_constant__ AppendQ8Args a) {
 
 }  // namespace
 
-cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& args, cudaStream_t stream) {
+cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& args, int sm_count,
+                                       cudaStream_t stream) {
   if (args.base.num_tokens == 0) return cudaSuccess;
   AppendQ8Args a = args;
   const int windows = (a.base.num_tokens + kWindow - 1) / kWindow;
   const int items = a.base.num_q_heads + 2 * a.base.num_kv_heads;
-  // parts of a window on 152 SMs, at least one head vector each
+  // parts of a window, at least one head vector each
   const bool many = a.base.num_tokens >= kManyTokens;
-  const int wave = 152 * (many ? kManyCtas : kFewCtas);
+  const int wave = sm_count * (many ? kManyCtas : kFewCtas);
   int want = 2 * wave / windows;
   if (want < 4) want = (3 * wave + windows - 1) / windows;
   a.parts = want > items ? items : want;
