@@ -1,6 +1,7 @@
 // Host side of the multi-query attention kernel (prefill_kernel.cuh): row-tile
 // tensor maps of q and out, and the launches, for bf16 and 8-bit caches.
 #include "prefill_kernel.cuh"
+#include "prefill_order.h"
 
 #include <cudaTypedefs.h>
 

@@ -72,7 +72,6 @@
 #include "device_common.cuh"
 #include "q8_common.cuh"
 #include "prefill.h"
-#include "prefill_order.cuh"
 #include "tc5.cuh"
 
 namespace pkvqk {
@@ -233,13 +232,28 @@ struct Work {
 
 // What the grid and the row offsets say; L is the sequence's length as read.
 __device__ __forceinline__ Work place_work(const PrefillArgs& a) {
-  const PrefillPlace at = place_cta(a.mt_major != 0, blockIdx.x, blockIdx.y, gridDim.x, gridDim.y,
-                                    a.m_tiles, a.num_kv_heads, a.num_splits);
   Work w;
-  w.mt = at.mt;
-  w.b = at.b;
-  w.g = at.g;
-  w.j = at.j;
+  if (a.mt_major) {
+    // the launch order runs over all sequences' last row tiles first: for
+    // fresh prompts a row tile's keys grow with its index, so this hands the
+    // longest work out first (row_tile_major: the CTA's number fits an int)
+    const int per_mt = gridDim.y * a.num_kv_heads * a.num_splits;
+    int x = blockIdx.y * gridDim.x + blockIdx.x;
+    w.mt = a.m_tiles - 1 - x / per_mt;
+    x %= per_mt;
+    w.b = x / (a.num_kv_heads * a.num_splits);
+    x %= a.num_kv_heads * a.num_splits;
+    w.g = x / a.num_splits;
+    w.j = x % a.num_splits;
+  } else {
+    // within a (sequence, kv head) the last row tile (the most keys) first
+    int x = blockIdx.x;
+    w.mt = a.m_tiles - 1 - x % a.m_tiles;
+    x /= a.m_tiles;
+    w.g = x % a.num_kv_heads;
+    w.j = x / a.num_kv_heads;
+    w.b = blockIdx.y;
+  }
   w.L = a.seq_lens[w.b];
   if (a.cu_seqlens_q != nullptr) {
     const long long c0 = a.cu_seqlens_q[w.b], c1 = a.cu_seqlens_q[w.b + 1];

@@ -1,26 +1,47 @@
-// Host walk of the multi-query attention kernel's launch order (csrc/prefill_order.cuh):
-// every CTA's place lies inside the call and every place is taken once, in grids of all
-// sizes that the entry points allow: 65535 sequences, 2^31 - 1 CTAs a sequence.
+// Host walk of the multi-query attention kernel's launch order under the launch's rule
+// (csrc/prefill_order.h): every CTA's place, by the arithmetic of place_work in
+// csrc/prefill_kernel.cuh, lies inside the call and every place is taken once, in grids
+// of all sizes that the entry points allow: 65535 sequences, 2^31 - 1 CTAs a sequence.
 // Built with wrapping integers, as the GPU's are.
 #include <cstdio>
 #include <random>
 #include <vector>
 
-#include "../../paged_kv_cache_qk_gb300/csrc/prefill_order.cuh"
+#include "../../paged_kv_cache_qk_gb300/csrc/prefill_order.h"
 
 namespace {
 
 int failures = 0;
 
-pkvqk::PrefillPlace place(bool wanted, long long gx, int batch, int m_tiles, int hkv, int splits,
-                          int x, int y) {
-  const bool major = pkvqk::row_tile_major(wanted, gx, batch);
-  const auto p = pkvqk::place_cta(major, x, y, static_cast<int>(gx), batch, m_tiles, hkv, splits);
+struct Place {
+  int b, g, j, mt;
+};
+
+Place place(bool wanted, long long gx, int batch, int m_tiles, int hkv, int splits, int cta_x,
+            int cta_y) {
+  Place p;
+  int x = cta_x;
+  if (pkvqk::row_tile_major(wanted, gx, batch)) {
+    const int per_mt = batch * hkv * splits;
+    x = cta_y * static_cast<int>(gx) + cta_x;
+    p.mt = m_tiles - 1 - x / per_mt;
+    x %= per_mt;
+    p.b = x / (hkv * splits);
+    x %= hkv * splits;
+    p.g = x / splits;
+    p.j = x % splits;
+  } else {
+    p.mt = m_tiles - 1 - x % m_tiles;
+    x /= m_tiles;
+    p.g = x % hkv;
+    p.j = x / hkv;
+    p.b = cta_y;
+  }
   if (p.b < 0 || p.b >= batch || p.g < 0 || p.g >= hkv || p.j < 0 || p.j >= splits || p.mt < 0 ||
       p.mt >= m_tiles) {
     if (failures++ < 8)
       std::printf("batch %d, %d row tiles, %d heads, %d splits: CTA (%d, %d) has %d %d %d %d\n",
-                  batch, m_tiles, hkv, splits, x, y, p.b, p.g, p.j, p.mt);
+                  batch, m_tiles, hkv, splits, cta_x, cta_y, p.b, p.g, p.j, p.mt);
   }
   return p;
 }
