@@ -232,7 +232,10 @@ PKVQK_API pkvqk_status pkvqk_norm_rope_append_cached(
  *           tokens and more K's values come from an fp32 norm and rotation, and
  *           one within 2^-20 of itself of the middle between two codes may get
  *           either; so may, in any call, a subnormal e4m3 code)
- * and where the stored scale grew, the codes of the group's other slots are
+ * In any call K's a comes from that norm and rotation: within 2^-20 of M*2^e it may
+ * get that e or the next.  A stored scale that is no power of two is kept as it is
+ * where it is the larger; value / scale is then rounded to fp32 before the code.
+ * Where the stored scale grew, the codes of the group's other slots are
  * rescaled (code * old / new, to the nearest), so that earlier tokens keep
  * their values.  Writing slot 0 starts a group anew: what other slots of it
  * hold is free.  A stored scale outside 2^-64 .. 2^63 counts as 2^-64.

@@ -12,8 +12,7 @@
 
 namespace pkvqk {
 
-// Two f16 values from the codes in bytes (SEL & 3) of w, in the order given by
-// the selector's low two nibbles used below.
+// Two f16 values from two e4m3 codes, the low byte's in the low half.
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint16_t w) {
   uint32_t r;
   asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(w));

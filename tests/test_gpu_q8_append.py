@@ -228,8 +228,9 @@ def test_append_on_a_side_stream_captured_and_replayed(lib):
     assert not torch.equal(c.k.view(torch.uint8), d.k.view(torch.uint8))
 
 
-# calls of 1024 tokens and more run on the kernel's narrower form: whole groups, runs that start inside a group and end in the next window,
-# many short sequences (several runs a window), padding between them
+# many windows (the kernel's narrow form, for larger calls: test_gpu_q8_append_many.py):
+# whole groups, runs that start inside a group and end in the next window, many short
+# sequences (several runs a window), padding between them
 MANY = [
     (16, 8, [1024, 37, 200], 16, [0, 5, 16]),
     (32, 4, [700, 700], 256, [3, 255]),

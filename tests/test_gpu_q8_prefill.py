@@ -35,8 +35,8 @@ def _problem(Hq, Hkv, q_len, bs, priors, seed, extra=3):
 
 
 # (Hq, Hkv, new tokens, page, priors): one row to several CTAs a kv head, with and
-# without a second row tile, ragged ones, groups that are no power of two (q comes
-# in by loads), pages that are no power of two, one key to many tiles
+# without a second row tile, ragged ones, groups that are no power of two (rows find
+# their token by a division), pages that are no power of two, one key to many tiles
 CASES = [
     (16, 8, 1, 16, [0, 126, 127, 128, 700]),
     (32, 4, 40, 32, [250, 1]),
@@ -113,8 +113,8 @@ def test_prefill_rows_without_keys(lib):
 
 
 def test_prefill_q_rows_of_any_magnitude(lib):
-    p = _problem(12, 4, 50, 16, [60, 200], 9)        # q by loads
-    for p in (p, _problem(16, 8, 50, 16, [60, 200], 9)):   # and by row-tile boxes
+    p = _problem(12, 4, 50, 16, [60, 200], 9)        # a group that is no power of two
+    for p in (p, _problem(16, 8, 50, 16, [60, 200], 9)):   # and one that is
         q = p.q.clone()
         q[3] = 0
         q[4] *= 2.0 ** -100
