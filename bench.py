@@ -132,29 +132,29 @@ CPU_BASELINE_WORKLOADS = ("decode_64x8192", "decode_long_8x32768", "decode_gqa8_
 # three warm-up steps), keyed by workload and split count (0: balanced).  A
 # capture describes the kernel sources it was taken with: when the sources
 # hash differently, the bench reports traffic as null.
-SRC = "53582c2775d61dfe"
+SRC = "69e50fad5aa2f043"
 MEASURED_TRAFFIC = {
-    ("decode_1x2048", 32): {"src": SRC, "bytes": 8468352},
+    ("decode_1x2048", 32): {"src": SRC, "bytes": 8467840},
     ("decode_1x512", 8): {"src": SRC, "bytes": 2176128},
-    ("decode_1x8192", 64): {"src": SRC, "bytes": 33635584},
-    ("decode_32x2048", 4): {"src": SRC, "bytes": 270230912},
-    ("decode_32x512", 4): {"src": SRC, "bytes": 67453696},
-    ("decode_32x8192", 4): {"src": SRC, "bytes": 1075746432},
-    ("decode_64x2048", 2): {"src": SRC, "bytes": 538666496},
-    ("decode_64x512", 2): {"src": SRC, "bytes": 135940096},
-    ("decode_64x8192", 2): {"src": SRC, "bytes": 2149515264},
-    ("decode_8x2048", 16): {"src": SRC, "bytes": 67362816},
-    ("decode_8x512", 8): {"src": SRC, "bytes": 16885632},
-    ("decode_8x8192", 16): {"src": SRC, "bytes": 270131456},
-    ("decode_gqa4_32x8192", 4): {"src": SRC, "bytes": 1075707776},
-    ("decode_gqa8_64", 0): {"src": SRC, "bytes": 468448000},
-    ("decode_gqa8_64x4096", 2): {"src": SRC, "bytes": 539089920},
-    ("decode_long_8x32768", 1): {"src": SRC, "bytes": 1075767936},
-    ("decode_long_8x32768", 8): {"src": SRC, "bytes": 1075376000},
-    ("decode_long_8x32768", 16): {"src": SRC, "bytes": 1075483776},
-    ("decode_long_8x32768", 32): {"src": SRC, "bytes": 1075882368},
-    ("decode_long_8x32768", 128): {"src": SRC, "bytes": 1076084992},
-    ("verify_32x5", 6): {"src": SRC, "bytes": 710233856},
+    ("decode_1x8192", 64): {"src": SRC, "bytes": 33635328},
+    ("decode_32x2048", 4): {"src": SRC, "bytes": 270183808},
+    ("decode_32x512", 4): {"src": SRC, "bytes": 67449216},
+    ("decode_32x8192", 4): {"src": SRC, "bytes": 1075546880},
+    ("decode_64x2048", 2): {"src": SRC, "bytes": 538998144},
+    ("decode_64x512", 2): {"src": SRC, "bytes": 135937920},
+    ("decode_64x8192", 2): {"src": SRC, "bytes": 2149483136},
+    ("decode_8x2048", 16): {"src": SRC, "bytes": 67321472},
+    ("decode_8x512", 8): {"src": SRC, "bytes": 16887808},
+    ("decode_8x8192", 16): {"src": SRC, "bytes": 270206720},
+    ("decode_gqa4_32x8192", 4): {"src": SRC, "bytes": 1075698048},
+    ("decode_gqa8_64", 0): {"src": SRC, "bytes": 468466432},
+    ("decode_gqa8_64x4096", 2): {"src": SRC, "bytes": 539252352},
+    ("decode_long_8x32768", 1): {"src": SRC, "bytes": 1076131328},
+    ("decode_long_8x32768", 8): {"src": SRC, "bytes": 1075634944},
+    ("decode_long_8x32768", 16): {"src": SRC, "bytes": 1075515776},
+    ("decode_long_8x32768", 32): {"src": SRC, "bytes": 1075909888},
+    ("decode_long_8x32768", 128): {"src": SRC, "bytes": 1076105216},
+    ("verify_32x5", 6): {"src": SRC, "bytes": 710189056},
 }
 
 
@@ -162,7 +162,7 @@ def kernel_src_hash():
     import hashlib
     csrc = os.path.join(ROOT, "paged_kv_cache_qk_gb300", "csrc")
     parts = []
-    for f in ("decode.cu", "device_common.cuh", "kernels.h", "api.cu"):
+    for f in ("decode.cu", "decode_schedule.cuh", "device_common.cuh", "kernels.h", "api.cu"):
         with open(os.path.join(csrc, f), "rb") as fh:
             parts.append(hashlib.sha256(fh.read()).hexdigest())
     return hashlib.sha256("".join(parts).encode()).hexdigest()[:16]
