@@ -74,7 +74,9 @@ typedef enum pkvqk_status {
 #define PKVQK_FLAG_BAD_SLOT      0x1  /* slot >= num_blocks*block_size: skipped */
 #define PKVQK_FLAG_BAD_BLOCK_ID  0x2  /* block id outside [0, num_blocks): its keys read as zeros */
 #define PKVQK_FLAG_WAIT_TIMEOUT  0x4  /* a pipeline wait gave up: output invalid */
-#define PKVQK_FLAG_BAD_VALUE     0x8  /* 8-bit append: a k or v value that is not finite */
+#define PKVQK_FLAG_BAD_VALUE     0x8  /* 8-bit append: a k or v value that is not finite;
+                                         drafts: a NaN or negative probability, or none above 0 */
+#define PKVQK_FLAG_BAD_TOKEN     0x10 /* drafted token outside [0, vocab_size): not accepted */
 
 /*
  * Layout of a paged cache, shared by the K and the V cache of a layer:
@@ -209,6 +211,40 @@ PKVQK_API pkvqk_status pkvqk_norm_rope_append_cached(
     const void* k, int64_t k_stride_t, int64_t k_stride_h,
     const void* v, int64_t v_stride_t, int64_t v_stride_h,
     const int64_t* positions, const int64_t* slot_mapping,
+    const void* gamma_q, const void* gamma_k,
+    float theta, float eps,
+    int32_t num_tokens, int32_t num_q_heads,
+    void* k_cache, void* v_cache, const pkvqk_cache_layout* layout,
+    const void* rope_table, int32_t table_positions,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+/*
+ * pkvqk_norm_rope_append with rotary positions of several axes, as the tokens of
+ * images and videos have (time, height, width): frequency i < D/2 of token t
+ * turns by the angle
+ *     positions[freq_axes[i]*positions_stride_a + t] * theta^(-2i/D),
+ * everything else as there.  Text tokens have the same position on every axis
+ * and get what pkvqk_norm_rope_append gives them, bit for bit.
+ *
+ *   q, q_out           device bf16, own strides; q_out may be q, else they must not overlap
+ *   positions          device int64, [num_axes][num_tokens], the axes positions_stride_a
+ *                      elements apart, a token's neighbours adjacent
+ *   num_axes           1 .. 4
+ *   freq_axes          HOST uint8 [head_dim / 2], each below num_axes; read before the
+ *                      call returns.  Contiguous sections and interleaved axes are both
+ *                      such maps; where every four frequencies 4l .. 4l+3 share an axis a
+ *                      token's angles are read from the table in 16-byte pieces
+ *   rope_table, table_positions   as pkvqk_norm_rope_append_cached (0: no table is read); a
+ *                      token is served by the table where it has the positions of all its axes
+ */
+PKVQK_API pkvqk_status pkvqk_norm_rope_append_axes(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    void* q_out, int64_t q_out_stride_t, int64_t q_out_stride_h,
+    const void* k, int64_t k_stride_t, int64_t k_stride_h,
+    const void* v, int64_t v_stride_t, int64_t v_stride_h,
+    const int64_t* positions, int64_t positions_stride_a,
+    int32_t num_axes, const uint8_t* freq_axes,
+    const int64_t* slot_mapping,
     const void* gamma_q, const void* gamma_k,
     float theta, float eps,
     int32_t num_tokens, int32_t num_q_heads,
@@ -450,6 +486,61 @@ PKVQK_API pkvqk_status pkvqk_lse_combine(const float* ws_o, const float* ws_lse,
                                int32_t rows, int32_t head_dim,
                                int32_t num_splits, void* out, float* lse_out,
                                pkvqk_stream_t stream);
+
+/* Types of the probabilities that pkvqk_verify_drafts reads. */
+typedef enum pkvqk_prob_type {
+  PKVQK_PROB_FP32 = 0,
+  PKVQK_PROB_BF16 = 1,
+  PKVQK_PROB_FP16 = 2
+} pkvqk_prob_type;
+
+/*
+ * Verdict on drafted tokens, after a verify step (pkvqk_paged_decode with
+ * q_len = drafts + 1, and the model's head) has given the target's probabilities.
+ * Source: the speculative verify of InfiniLM PR #585, Summary item 4.
+ *
+ * Sequence b has n = draft_lens[b] drafts (max_drafts where draft_lens is NULL) x_i,
+ * target rows p_i, i <= n, draft rows q_i, i < n, and uniforms u_i.  With
+ * draft_probs NULL the drafts were certain (looked up in the prompt): q_i(x_i) is 1
+ * and q_i is 0 elsewhere.
+ *   draft i is accepted if all before it are and u_i * q_i(x_i) < p_i(x_i) (the
+ *   product not rounded); j = the number accepted
+ *   w(v) = max(p_j(v) - q_j(v), 0) where j < n; p_n(v) where j = n; where no w(v) is
+ *   above 0, w = p_j
+ *   y = the smallest v with w(0) + .. + w(v) > u_{max_drafts} * sum of w
+ *   tokens[b] = x_0 .. x_{j-1}, y, then -1;  num_accepted[b] = j
+ *   kept_lens[b] = seq_lens[b] - (n - j): the keys that stay, where seq_lens[b] counts
+ *   the cached tokens of the verify step; what the cache holds past them is free
+ * so that with independent u, uniform in [0, 1), the tokens are distributed as the
+ * target's own.  The sums are exact: probabilities count as multiples of 2^-44, to the
+ * nearest.  Probabilities above 1 count as 1, NaN and negative ones as 0 (reported by
+ * PKVQK_FLAG_BAD_VALUE where y's rows hold them); a row without any weight gives
+ * y = -1 and the same flag.  A draft outside [0, vocab_size) is not accepted, takes no
+ * weight away where draft_probs is NULL, and is reported by PKVQK_FLAG_BAD_TOKEN.
+ * u_{max_drafts} counts as its nearest value in [0, 1); NaN as 0.
+ *
+ *   target_probs  device, row (b, i) of vocab_size values at
+ *                 b*target_stride_b + i*target_stride_t elements, i <= max_drafts
+ *   draft_probs   device, the same type, i < max_drafts; or NULL
+ *   type          pkvqk_prob_type of both; 16-byte rows (base, strides) are read fastest
+ *   draft_tokens  device int32 [batch, max_drafts]   (may be NULL where max_drafts is 0)
+ *   draft_lens    device int32 [batch] or NULL; values outside 0 .. max_drafts count as
+ *                 the nearest of them
+ *   uniforms      device fp32 [batch, max_drafts + 1]
+ *   tokens        device int32 [batch, max_drafts + 1];  num_accepted device int32 [batch]
+ *   seq_lens, kept_lens  device int32 [batch], both or neither; may be the same
+ * Rows past n are not read.  max_drafts 0 .. 255 (0: y drawn from p_0), vocab_size
+ * 1 .. 2^20 - 1, batch <= 65535.
+ */
+PKVQK_API pkvqk_status pkvqk_verify_drafts(
+    const void* target_probs, int64_t target_stride_b, int64_t target_stride_t,
+    const void* draft_probs, int64_t draft_stride_b, int64_t draft_stride_t,
+    int32_t type,
+    const int32_t* draft_tokens, const int32_t* draft_lens, const float* uniforms,
+    int32_t batch, int32_t max_drafts, int32_t vocab_size,
+    int32_t* tokens, int32_t* num_accepted,
+    const int32_t* seq_lens, int32_t* kept_lens,
+    int32_t* status_flags, pkvqk_stream_t stream);
 
 /*
  * Split count for pkvqk_paged_prefill from host-side facts only: batch, kv

@@ -45,3 +45,8 @@ from .quantised import (  # noqa: F401
     q8_scale_exponent,
     q8_values,
 )
+from .scored import (  # noqa: F401
+    norm_rope_append_axes,
+    scored_attention,
+    verify_drafts,
+)

@@ -40,9 +40,14 @@ FLAG_BAD_SLOT = 0x1
 FLAG_BAD_BLOCK_ID = 0x2
 FLAG_WAIT_TIMEOUT = 0x4
 FLAG_BAD_VALUE = 0x8
+FLAG_BAD_TOKEN = 0x10
 
 Q8_E4M3 = 1
 Q8_INT8 = 2
+
+PROB_FP32 = 0
+PROB_BF16 = 1
+PROB_FP16 = 2
 
 
 class CacheLayout(ctypes.Structure):
@@ -176,6 +181,29 @@ pkvqk_paged_prefill_varlen_q8 = _sig("pkvqk_paged_prefill_varlen_q8", ctypes.c_i
     c_i32, c_i32, c_f32,                # num_splits, max_seq_len_hint, scale
     c_vp, c_vp, c_vp, c_size, c_vp, c_vp])
 
+pkvqk_norm_rope_append_axes = _sig("pkvqk_norm_rope_append_axes", ctypes.c_int, [
+    c_vp, c_i64, c_i64,                 # q, strides
+    c_vp, c_i64, c_i64,                 # q_out
+    c_vp, c_i64, c_i64,                 # k
+    c_vp, c_i64, c_i64,                 # v
+    c_vp, c_i64, c_i32, ctypes.c_char_p,  # positions, axis stride, num_axes, freq_axes (host)
+    c_vp,                               # slot_mapping
+    c_vp, c_vp,                         # gamma_q, gamma_k
+    c_f32, c_f32,                       # theta, eps
+    c_i32, c_i32,                       # num_tokens, num_q_heads
+    c_vp, c_vp, ctypes.POINTER(CacheLayout),
+    c_vp, c_i32,                        # rope_table, table_positions
+    c_vp, c_vp])                        # status_flags, stream
+pkvqk_verify_drafts = _sig("pkvqk_verify_drafts", ctypes.c_int, [
+    c_vp, c_i64, c_i64,                 # target_probs, strides
+    c_vp, c_i64, c_i64,                 # draft_probs, strides
+    c_i32,                              # type
+    c_vp, c_vp, c_vp,                   # draft_tokens, draft_lens, uniforms
+    c_i32, c_i32, c_i32,                # batch, max_drafts, vocab_size
+    c_vp, c_vp,                         # tokens, num_accepted
+    c_vp, c_vp,                         # seq_lens, kept_lens
+    c_vp, c_vp])                        # status_flags, stream
+
 EXPORTED = [
     "pkvqk_last_error", "pkvqk_abi_version", "pkvqk_norm_rope_append",
     "pkvqk_choose_num_splits", "pkvqk_decode_workspace_bytes", "pkvqk_paged_decode",
@@ -184,7 +212,7 @@ EXPORTED = [
     "pkvqk_prefill_workspace_bytes", "pkvqk_paged_prefill", "pkvqk_paged_prefill_varlen",
     "pkvqk_rope_table_bytes", "pkvqk_rope_table_build", "pkvqk_norm_rope_append_cached",
     "pkvqk_norm_rope_append_q8", "pkvqk_paged_decode_q8", "pkvqk_paged_prefill_q8",
-    "pkvqk_paged_prefill_varlen_q8",
+    "pkvqk_paged_prefill_varlen_q8", "pkvqk_norm_rope_append_axes", "pkvqk_verify_drafts",
 ]
 
 
@@ -399,16 +427,21 @@ _ROPE_ROW_BYTES = pkvqk_rope_table_bytes(1)
 def _q8_names():
     torch = _torch()
     _q8.update(formats={torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8},
+               probs={torch.float32: PROB_FP32, torch.bfloat16: PROB_BF16,
+                      torch.float16: PROB_FP16},
                bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32, i64=torch.int64,
                raw_stream=torch._C._cuda_getCurrentRawStream)
     return _q8
 
 
+_STRUCTS = (ctypes.POINTER(Q8Cache), ctypes.POINTER(CacheLayout))
+
+
 def _fast(name, args):
-    """The entry point with the cache passed as packed bytes."""
+    """The entry point with the cache (or its layout) passed as packed bytes."""
     f = _lib[name]
     f.restype = ctypes.c_int
-    f.argtypes = [ctypes.c_char_p if a is ctypes.POINTER(Q8Cache) else a for a in args]
+    f.argtypes = [ctypes.c_char_p if a in _STRUCTS else a for a in args]
     return f
 
 
@@ -595,3 +628,118 @@ def paged_prefill_varlen_q8(q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scal
         _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, Hq, num_splits, max_seq_len_hint,
         scale, o, lse, *_workspace(workspace), _flags(t, status_flags),
         _raw_stream(t, stream, q)))
+
+
+# ------------------------------------------------- positions of several axes
+
+_LAYOUT_PACK = struct.Struct("=q4i3q")         # pkvqk_cache_layout, no padding
+assert _LAYOUT_PACK.size == ctypes.sizeof(CacheLayout)
+_append_axes = _fast("pkvqk_norm_rope_append_axes", pkvqk_norm_rope_append_axes.argtypes)
+
+
+def _pack_layout(t, k_cache, v_cache):
+    shape, st = k_cache.shape, k_cache.stride()
+    if k_cache.dtype is not t["bf16"] or v_cache.dtype is not t["bf16"]:
+        raise ValueError("k_cache and v_cache must be bfloat16")
+    if v_cache.stride() != st or v_cache.shape != shape:
+        raise ValueError("k_cache and v_cache must share one layout")
+    nb, bs, hkv, d = shape
+    if st[3] != 1:
+        raise ValueError("head_dim must be the contiguous axis")
+    return _LAYOUT_PACK.pack(nb, bs, hkv, d, 0, st[0], st[1], st[2])
+
+
+def rope_axes(sections, *, interleaved=False):
+    """The axis of each of the head_dim // 2 frequencies, for norm_rope_append_axes.
+
+    sections: how many frequencies each axis has (they sum to 64).  Axis after axis, or,
+    interleaved, dealt out in turn until an axis has its share.
+    """
+    left = [int(n) for n in sections]
+    if not 1 <= len(left) <= 4 or min(left) < 0 or sum(left) != 64:
+        raise ValueError("sections must be 1 to 4 counts that sum to 64")
+    if not interleaved:
+        return bytes(a for a, n in enumerate(left) for _ in range(n))
+    axes = bytearray()
+    while len(axes) < 64:
+        for a, n in enumerate(left):
+            if n:
+                left[a] = n - 1
+                axes.append(a)
+    return bytes(axes)
+
+
+def norm_rope_append_axes(q, k, v, positions, freq_axes, slot_mapping, gamma_q, gamma_k, theta,
+                          eps, k_cache, v_cache, *, q_out=None, rope_table=None,
+                          table_positions=0, status_flags=None, stream=None):
+    """norm_rope_append with positions [axes, T] int64 and the axis of each frequency
+    (rope_axes); q [T, Hq, D] is written to q_out (default: in place).  rope_table as for
+    norm_rope_append_cached."""
+    t = _q8 or _q8_names()
+    q_out = q if q_out is None else q_out
+    T, Hq, qs, qh = _heads(t, q, "q")
+    To, Ho, os_, oh = _heads(t, q_out, "q_out")
+    Tk, Hk, ks, kh = _heads(t, k, "k")
+    Tv, Hv, vs, vh = _heads(t, v, "v")
+    if (To, Ho) != (T, Hq) or Tk != T or Tv != T or Hk != Hv or Hk != k_cache.shape[2]:
+        raise ValueError("q, q_out, k and v must agree in tokens, and k, v and the cache in heads")
+    if positions.dtype is not t["i64"] or positions.dim() != 2 or positions.shape[1] != T \
+            or (T > 1 and positions.stride(1) != 1):
+        raise ValueError("positions must be int64 [axes, tokens], the tokens contiguous")
+    if len(freq_axes) != 64:
+        raise ValueError("freq_axes must be 64 bytes")
+    if rope_table is not None and (not rope_table.is_contiguous()
+                                   or rope_table.nbytes < table_positions * _ROPE_ROW_BYTES):
+        raise ValueError(f"rope_table must be contiguous and hold {table_positions} positions")
+    check(_append_axes(
+        q.data_ptr(), qs, qh, q_out.data_ptr(), os_, oh, k.data_ptr(), ks, kh,
+        v.data_ptr(), vs, vh, positions.data_ptr(), positions.stride(0), positions.shape[0],
+        bytes(freq_axes), _ints(slot_mapping, t["i64"], T, "slot_mapping"),
+        _gains(t, gamma_q, "gamma_q"), _gains(t, gamma_k, "gamma_k"), theta, eps, T, Hq,
+        k_cache.data_ptr(), v_cache.data_ptr(), _pack_layout(t, k_cache, v_cache),
+        _ptr(rope_table), table_positions, _flags(t, status_flags), _raw_stream(t, stream, q)))
+
+
+# ----------------------------------------------------------- drafted tokens
+
+def _rows_of(x, batch, rows, vocab, name):
+    """Strides of a [batch, >= rows, vocab] view whose rows are contiguous."""
+    if x.dim() != 3 or x.shape[0] != batch or x.shape[1] < rows or x.shape[2] != vocab \
+            or (vocab > 1 and x.stride(2) != 1):
+        raise ValueError(f"{name} must be [batch, drafts, vocab], the vocabulary contiguous")
+    return x.stride(0), x.stride(1)
+
+
+def verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, tokens, num_accepted, *,
+                  draft_lens=None, seq_lens=None, kept_lens=None, status_flags=None, stream=None):
+    """Which drafted tokens are kept, and the token that follows them.
+
+    target_probs [B, K + 1, V] fp32, bf16 or fp16; draft_probs [B, K, V] of the same type, or
+    None for drafts that were certain (looked up in the prompt); draft_tokens int32 [B, K];
+    uniforms fp32 [B, K + 1]; tokens int32 [B, K + 1] and num_accepted int32 [B] are written,
+    and kept_lens int32 [B] from seq_lens int32 [B] where both are given.
+    """
+    t = _q8 or _q8_names()
+    B, K = draft_tokens.shape
+    V = target_probs.shape[-1]
+    kind = t["probs"].get(target_probs.dtype)
+    if kind is None:
+        raise ValueError("target_probs must be float32, bfloat16 or float16")
+    pb, pt = _rows_of(target_probs, B, K + 1, V, "target_probs")
+    q, qb, qt = 0, 0, 0
+    if draft_probs is not None:
+        if draft_probs.dtype is not target_probs.dtype:
+            raise ValueError("draft_probs must have target_probs' type")
+        if K:                                  # without drafts none of it is read
+            qb, qt = _rows_of(draft_probs, B, K, V, "draft_probs")
+            q = draft_probs.data_ptr()
+    i32 = t["i32"]
+    check(pkvqk_verify_drafts(
+        target_probs.data_ptr(), pb, pt, q, qb, qt, kind,
+        _ints(draft_tokens, i32, B * K, "draft_tokens"),
+        0 if draft_lens is None else _ints(draft_lens, i32, B, "draft_lens"),
+        _ints(uniforms, t["f32"], B * (K + 1), "uniforms"), B, K, V,
+        _ints(tokens, i32, B * (K + 1), "tokens"), _ints(num_accepted, i32, B, "num_accepted"),
+        0 if seq_lens is None else _ints(seq_lens, i32, B, "seq_lens"),
+        0 if kept_lens is None else _ints(kept_lens, i32, B, "kept_lens"),
+        _flags(t, status_flags), _raw_stream(t, stream, target_probs)))

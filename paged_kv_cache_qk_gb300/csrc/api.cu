@@ -563,13 +563,38 @@ void rope_constants(float theta, double (&inv_freq)[64], float (&tab)[pkvqk::kSi
   std::memcpy(tab, s_tab, sizeof(s_tab));
 }
 
+// What pkvqk_norm_rope_append_axes adds to the append's arguments.
+struct AxesCall {
+  void* q_out;
+  int64_t q_out_stride_t, q_out_stride_h;
+  int64_t axis_stride;
+  int32_t num_axes;
+  const uint8_t* freq_axes;
+};
+
+pkvqk_status check_axes(const AxesCall& x) {
+  if (x.num_axes < 1 || x.num_axes > pkvqk::kMaxRopeAxes)
+    return fail(PKVQK_ERR_INVALID_ARG, "num_axes %d (1..%d)", x.num_axes, pkvqk::kMaxRopeAxes);
+  if (x.freq_axes == nullptr) return fail(PKVQK_ERR_INVALID_ARG, "freq_axes is NULL");
+  for (int i = 0; i < 64; ++i)
+    if (x.freq_axes[i] >= x.num_axes)
+      return fail(PKVQK_ERR_INVALID_ARG, "freq_axes[%d] %d, with %d axes", i, x.freq_axes[i],
+                  x.num_axes);
+  if (x.q_out_stride_t < 0 || x.q_out_stride_h < 0 || x.q_out_stride_t % 8 || x.q_out_stride_h % 8)
+    return fail(PKVQK_ERR_INVALID_ARG, "q_out strides must be non-negative multiples of 8");
+  if (x.axis_stride < 0 || x.axis_stride >= (int64_t(1) << 40))
+    return fail(PKVQK_ERR_INVALID_ARG, "axis stride %lld", static_cast<long long>(x.axis_stride));
+  return PKVQK_OK;
+}
+
 pkvqk_status run_append(void* q, int64_t q_stride_t, int64_t q_stride_h, const void* k,
                         int64_t k_stride_t, int64_t k_stride_h, const void* v, int64_t v_stride_t,
                         int64_t v_stride_h, const int64_t* positions, const int64_t* slot_mapping,
                         const void* gamma_q, const void* gamma_k, float theta, float eps,
                         int32_t num_tokens, int32_t num_q_heads, void* k_cache, void* v_cache,
                         const pkvqk_cache_layout* layout, const void* rope_table,
-                        int32_t table_positions, int32_t* status_flags, pkvqk_stream_t stream) {
+                        int32_t table_positions, int32_t* status_flags, pkvqk_stream_t stream,
+                        const AxesCall* axes = nullptr) {
   PKVQK_TRY(check_layout(layout));
   const pkvqk_cache_layout& L = *layout;
   if (num_tokens < 0 || num_tokens > (1 << 30))
@@ -582,8 +607,13 @@ pkvqk_status run_append(void* q, int64_t q_stride_t, int64_t q_stride_h, const v
   for (int i = 0; i < 6; ++i)
     if (st[i] < 0 || (st[i] % 8) != 0)
       return fail(PKVQK_ERR_INVALID_ARG, "q/k/v strides must be non-negative multiples of 8");
+  if (axes != nullptr) PKVQK_TRY(check_axes(*axes));
   if (num_tokens == 0) return ok();
   PKVQK_TRY(check_device_ptr(q, "q"));
+  if (axes != nullptr) {
+    PKVQK_TRY(check_device_ptr(axes->q_out, "q_out"));
+    if (!aligned16(axes->q_out)) return fail(PKVQK_ERR_INVALID_ARG, "q_out not 16-byte aligned");
+  }
   PKVQK_TRY(check_device_ptr(k, "k"));
   PKVQK_TRY(check_device_ptr(v, "v"));
   PKVQK_TRY(check_device_ptr(positions, "positions"));
@@ -603,7 +633,7 @@ pkvqk_status run_append(void* q, int64_t q_stride_t, int64_t q_stride_h, const v
     if (!aligned16(rope_table)) return fail(PKVQK_ERR_INVALID_ARG, "rope_table not 16-byte aligned");
   }
 
-  pkvqk::NormRopeAppendArgs a;
+  pkvqk::NormRopeAppendAxesArgs a = {};
   a.q = static_cast<__nv_bfloat16*>(q);
   a.q_stride_t = q_stride_t;
   a.q_stride_h = q_stride_h;
@@ -632,7 +662,22 @@ pkvqk_status run_append(void* q, int64_t q_stride_t, int64_t q_stride_h, const v
   a.status_flags = status_flags;
   a.rope_table = table_positions > 0 ? static_cast<const float4*>(rope_table) : nullptr;
   a.table_positions = table_positions > 0 ? table_positions : 0;
-  cudaError_t e = pkvqk::launch_norm_rope_append(a, reinterpret_cast<cudaStream_t>(stream));
+  cudaError_t e;
+  if (axes == nullptr) {
+    e = pkvqk::launch_norm_rope_append(a, reinterpret_cast<cudaStream_t>(stream));
+  } else {
+    a.q_out = static_cast<__nv_bfloat16*>(axes->q_out);
+    a.q_out_stride_t = axes->q_out_stride_t;
+    a.q_out_stride_h = axes->q_out_stride_h;
+    a.axis_stride = axes->axis_stride;
+    a.num_axes = axes->num_axes;
+    a.lane_axes = 1;
+    for (int i = 0; i < 64; ++i) {
+      (i < 32 ? a.axes_lo : a.axes_hi) |= static_cast<uint64_t>(axes->freq_axes[i]) << (2 * (i & 31));
+      if (axes->freq_axes[i] != axes->freq_axes[i & ~3]) a.lane_axes = 0;
+    }
+    e = pkvqk::launch_norm_rope_append_axes(a, reinterpret_cast<cudaStream_t>(stream));
+  }
   if (e != cudaSuccess) return cuda_fail(e, "norm_rope_append launch");
   return ok();
 }
@@ -749,6 +794,25 @@ pkvqk_status pkvqk_norm_rope_append_cached(
                     v_stride_h, positions, slot_mapping, gamma_q, gamma_k, theta, eps, num_tokens,
                     num_q_heads, k_cache, v_cache, layout, rope_table, table_positions,
                     status_flags, stream);
+}
+
+pkvqk_status pkvqk_norm_rope_append_axes(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, void* q_out, int64_t q_out_stride_t,
+    int64_t q_out_stride_h, const void* k, int64_t k_stride_t, int64_t k_stride_h, const void* v,
+    int64_t v_stride_t, int64_t v_stride_h, const int64_t* positions, int64_t positions_stride_a,
+    int32_t num_axes, const uint8_t* freq_axes, const int64_t* slot_mapping, const void* gamma_q,
+    const void* gamma_k, float theta, float eps, int32_t num_tokens, int32_t num_q_heads,
+    void* k_cache, void* v_cache, const pkvqk_cache_layout* layout, const void* rope_table,
+    int32_t table_positions, int32_t* status_flags, pkvqk_stream_t stream) {
+  if (table_positions < 0 || table_positions > kRopeTableMaxPositions)
+    return fail(PKVQK_ERR_INVALID_ARG, "table_positions %d (0..%d)", table_positions,
+                kRopeTableMaxPositions);
+  const AxesCall axes{q_out,    q_out_stride_t, q_out_stride_h, positions_stride_a,
+                      num_axes, freq_axes};
+  return run_append(const_cast<void*>(q), q_stride_t, q_stride_h, k, k_stride_t, k_stride_h, v,
+                    v_stride_t, v_stride_h, positions, slot_mapping, gamma_q, gamma_k, theta, eps,
+                    num_tokens, num_q_heads, k_cache, v_cache, layout, rope_table,
+                    table_positions, status_flags, stream, &axes);
 }
 
 pkvqk_status pkvqk_norm_rope_append_q8(
@@ -921,6 +985,60 @@ pkvqk_status pkvqk_lse_combine(const float* ws_o, const float* ws_lse, int32_t r
                                             static_cast<__nv_bfloat16*>(out), lse_out,
                                             reinterpret_cast<cudaStream_t>(stream));
   if (e != cudaSuccess) return cuda_fail(e, "lse combine launch");
+  return ok();
+}
+
+pkvqk_status pkvqk_verify_drafts(const void* target_probs, int64_t target_stride_b,
+                                 int64_t target_stride_t, const void* draft_probs,
+                                 int64_t draft_stride_b, int64_t draft_stride_t, int32_t type,
+                                 const int32_t* draft_tokens, const int32_t* draft_lens,
+                                 const float* uniforms, int32_t batch, int32_t max_drafts,
+                                 int32_t vocab_size, int32_t* tokens, int32_t* num_accepted,
+                                 const int32_t* seq_lens, int32_t* kept_lens,
+                                 int32_t* status_flags, pkvqk_stream_t stream) {
+  if (type != PKVQK_PROB_FP32 && type != PKVQK_PROB_BF16 && type != PKVQK_PROB_FP16)
+    return fail(PKVQK_ERR_UNSUPPORTED, "type %d (pkvqk_prob_type)", type);
+  if (batch < 0 || batch > 65535) return fail(PKVQK_ERR_INVALID_ARG, "batch %d", batch);
+  if (max_drafts < 0 || max_drafts > 255)
+    return fail(PKVQK_ERR_INVALID_ARG, "max_drafts %d (0..255)", max_drafts);
+  if (vocab_size < 1 || vocab_size >= (1 << 20))
+    return fail(PKVQK_ERR_INVALID_ARG, "vocab_size %d (1..2^20 - 1)", vocab_size);
+  const int64_t st[4] = {target_stride_b, target_stride_t, draft_stride_b, draft_stride_t};
+  for (int i = 0; i < (draft_probs != nullptr ? 4 : 2); ++i)
+    if (st[i] < 0 || st[i] >= (int64_t(1) << 40))
+      return fail(PKVQK_ERR_INVALID_ARG, "row strides must not be negative");
+  if ((seq_lens == nullptr) != (kept_lens == nullptr))
+    return fail(PKVQK_ERR_INVALID_ARG, "seq_lens and kept_lens go together");
+  if (batch == 0) return ok();
+  const uintptr_t size = type == PKVQK_PROB_FP32 ? 4 : 2;
+  PKVQK_TRY(check_device_ptr(target_probs, "target_probs"));
+  if (reinterpret_cast<uintptr_t>(target_probs) % size)
+    return fail(PKVQK_ERR_INVALID_ARG, "target_probs not aligned to its type");
+  if (draft_probs != nullptr) {
+    PKVQK_TRY(check_device_ptr(draft_probs, "draft_probs"));
+    if (reinterpret_cast<uintptr_t>(draft_probs) % size)
+      return fail(PKVQK_ERR_INVALID_ARG, "draft_probs not aligned to its type");
+  }
+  const void* ptr[7] = {uniforms,   tokens,   num_accepted, draft_tokens,
+                        draft_lens, seq_lens, kept_lens};
+  const char* nm[7] = {"uniforms",   "tokens",   "num_accepted", "draft_tokens",
+                       "draft_lens", "seq_lens", "kept_lens"};
+  for (int i = 0; i < 7; ++i) {
+    // the last three may be left out, draft_tokens where there are none
+    if (ptr[i] == nullptr && (i > 3 || (i == 3 && max_drafts == 0))) continue;
+    PKVQK_TRY(check_device_ptr(ptr[i], nm[i]));
+    if (reinterpret_cast<uintptr_t>(ptr[i]) & 3u)
+      return fail(PKVQK_ERR_INVALID_ARG, "%s not 4-byte aligned", nm[i]);
+  }
+  if (status_flags != nullptr) PKVQK_TRY(check_device_ptr(status_flags, "status_flags"));
+  const pkvqk::VerifyArgs a{target_probs,   target_stride_b, target_stride_t, draft_probs,
+                            draft_stride_b, draft_stride_t,  draft_tokens,    draft_lens,
+                            uniforms,       batch,           max_drafts,      vocab_size,
+                            tokens,         num_accepted,    seq_lens,        kept_lens,
+                            status_flags};
+  const cudaError_t e = pkvqk::launch_verify_drafts(a, type, sm_count_current(),
+                                                    reinterpret_cast<cudaStream_t>(stream));
+  if (e != cudaSuccess) return cuda_fail(e, "verify_drafts launch");
   return ok();
 }
 

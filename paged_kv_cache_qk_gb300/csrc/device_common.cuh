@@ -15,25 +15,33 @@
 
 namespace pkvqk {
 
-// Launch with programmatic stream serialization: the kernel may begin while
-// the previous kernel in the stream finishes; it calls pdl_wait() before
-// touching anything that kernel may have written.
-// Raises `kern`'s dynamic shared-memory limit to `bytes` on the current
-// device once: `done` (one per kernel instance) keeps a bit per device (the
-// attribute belongs to the device's context; setting it twice is harmless,
-// so racing threads need no lock).
-template <typename K>
-inline cudaError_t set_smem_limit_once(K kern, int bytes, std::atomic<uint64_t>& done) {
+// Calls `set` (a function attribute of one kernel instance) once per device: `done`
+// (one per kernel instance) keeps a bit per device (the attribute belongs to the
+// device's context; setting it twice is harmless, so racing threads need no lock).
+template <typename F>
+inline cudaError_t set_once(F&& set, std::atomic<uint64_t>& done) {
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) dev = -1;
   const uint64_t bit = (dev >= 0 && dev < 64) ? (uint64_t(1) << dev) : 0;
   if (bit != 0 && (done.load(std::memory_order_acquire) & bit) != 0) return cudaSuccess;
-  const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                             bytes);
+  const cudaError_t e = set();
   if (e == cudaSuccess && bit != 0) done.fetch_or(bit, std::memory_order_release);
   return e;
 }
 
+// Raises `kern`'s dynamic shared-memory limit to `bytes` on the current device once.
+template <typename K>
+inline cudaError_t set_smem_limit_once(K kern, int bytes, std::atomic<uint64_t>& done) {
+  return set_once(
+      [&] {
+        return cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+      },
+      done);
+}
+
+// Launch with programmatic stream serialization: the kernel may begin while
+// the previous kernel in the stream finishes; it calls pdl_wait() before
+// touching anything that kernel may have written.
 template <typename... KArgs, typename... Args>
 inline cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
                               cudaStream_t stream, Args&&... args) {
@@ -59,6 +67,7 @@ constexpr int kFlagBadSlot = 0x1;
 constexpr int kFlagBadBlock = 0x2;
 constexpr int kFlagTimeout = 0x4;
 constexpr int kFlagBadValue = 0x8;
+constexpr int kFlagBadToken = 0x10;
 
 __device__ __forceinline__ uint32_t smem_addr(const void* p) {
   return static_cast<uint32_t>(__cvta_generic_to_shared(p));

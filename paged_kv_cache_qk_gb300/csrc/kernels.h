@@ -38,6 +38,21 @@ struct NormRopeAppendArgs {
 
 cudaError_t launch_norm_rope_append(const NormRopeAppendArgs& a, cudaStream_t stream);
 
+// Positions of several axes (pkvqk_norm_rope_append_axes): axis k's position of token t is
+// positions[k * axis_stride + t]; q goes to q_out.
+constexpr int kMaxRopeAxes = 4;
+
+struct NormRopeAppendAxesArgs : NormRopeAppendArgs {
+  __nv_bfloat16* q_out;
+  int64_t q_out_stride_t, q_out_stride_h;
+  int64_t axis_stride;
+  int32_t num_axes;
+  int32_t lane_axes;               // every four frequencies 4l .. 4l+3 share an axis
+  uint64_t axes_lo, axes_hi;       // axis of frequency i: two bits at 2 (i % 32)
+};
+
+cudaError_t launch_norm_rope_append_axes(const NormRopeAppendAxesArgs& a, cudaStream_t stream);
+
 // Fills table[pos][l][4] (l < 16: float4s cos_hi, cos_lo, sin_hi, sin_lo of
 // frequencies 4l .. 4l+3) for pos < positions with the values the append
 // kernel computes for a token at pos.
@@ -70,6 +85,28 @@ struct AppendQ8Args {
 };
 
 cudaError_t launch_norm_rope_append_q8(const AppendQ8Args& a, int sm_count, cudaStream_t stream);
+
+// pkvqk_verify_drafts: probabilities of the given type, strides in elements.
+constexpr int kProbFp32 = 0, kProbBf16 = 1, kProbFp16 = 2;
+
+struct VerifyArgs {
+  const void* target;              // row (b, t) at b * target_stride_b + t * target_stride_t
+  int64_t target_stride_b, target_stride_t;
+  const void* draft;               // or nullptr: every draft was certain
+  int64_t draft_stride_b, draft_stride_t;
+  const int32_t* draft_tokens;     // [batch, max_drafts]
+  const int32_t* draft_lens;       // [batch] or nullptr
+  const float* uniforms;           // [batch, max_drafts + 1]
+  int32_t batch, max_drafts, vocab;
+  int32_t* tokens;                 // [batch, max_drafts + 1]
+  int32_t* num_accepted;           // [batch]
+  const int32_t* seq_lens;         // [batch], with kept_lens
+  int32_t* kept_lens;              // [batch] or nullptr
+  int32_t* status_flags;
+};
+
+cudaError_t launch_verify_drafts(const VerifyArgs& a, int type, int sm_count,
+                                 cudaStream_t stream);
 
 struct DecodeArgs {
   const __nv_bfloat16* q;

@@ -36,6 +36,13 @@
 // whose position is in it loads its lane's 64 bytes with the q/k/v loads and
 // skips the angle phase; any other token computes its angles as above.  Both
 // ways give the same bits.
+//
+// With positions of several axes (NormRopeAppendAxesArgs: time, height and width of
+// an image's tokens) frequency i turns by the position of its axis, two bits of a
+// 128-bit word.  A lane whose four frequencies share an axis reads that position's
+// table row as above; where frequencies of one lane lie on different axes
+// (interleaved axes) it reads its 16 numbers one by one, each from the row of its
+// own axis' position.
 #include "device_common.cuh"
 #include "kernels.h"
 #include "rope_math.cuh"
@@ -67,6 +74,88 @@ struct Loaded {
   uint2 x0, x1, v0, v1;
 };
 
+// ---- where a token stands, and where its q goes: one position, q in place ...
+
+struct OnePosition {
+  int64_t p;
+};
+__device__ __forceinline__ OnePosition position_of(const NormRopeAppendArgs& a, int t) {
+  return {a.positions[t]};
+}
+__device__ __forceinline__ int64_t position_at(const NormRopeAppendArgs&, const OnePosition& pos,
+                                               int) {
+  return pos.p;
+}
+__device__ __forceinline__ bool in_table(const NormRopeAppendArgs& a, const OnePosition& pos) {
+  return pos.p >= 0 && pos.p < a.table_positions;
+}
+__device__ __forceinline__ Trig table_trig(const NormRopeAppendArgs& a, const OnePosition& pos,
+                                           int l) {
+  const float4* row = a.rope_table + (pos.p * (kHeadDim / 8) + l) * 4;
+  Trig tr;
+  tr.ch = __ldg(row);
+  tr.cl = __ldg(row + 1);
+  tr.sh = __ldg(row + 2);
+  tr.sl = __ldg(row + 3);
+  return tr;
+}
+__device__ __forceinline__ __nv_bfloat16* q_row_out(const NormRopeAppendArgs& a, int t, int h) {
+  return a.q + t * a.q_stride_t + static_cast<int64_t>(h) * a.q_stride_h;
+}
+
+// ---- ... or a position for each axis, q to a place of its own
+
+struct AxisPositions {
+  int64_t p[kMaxRopeAxes];
+};
+__device__ __forceinline__ AxisPositions position_of(const NormRopeAppendAxesArgs& a, int t) {
+  AxisPositions pos;
+#pragma unroll
+  for (int k = 0; k < kMaxRopeAxes; ++k)
+    pos.p[k] = k < a.num_axes ? a.positions[k * a.axis_stride + t] : 0;
+  return pos;
+}
+__device__ __forceinline__ int64_t on_axis(const AxisPositions& pos, uint32_t axis) {
+  int64_t p = pos.p[0];
+#pragma unroll
+  for (int k = 1; k < kMaxRopeAxes; ++k) p = axis == k ? pos.p[k] : p;
+  return p;
+}
+// axes of frequencies i .. (two bits each, frequency i's lowest)
+__device__ __forceinline__ uint32_t axis_bits(const NormRopeAppendAxesArgs& a, int i) {
+  return static_cast<uint32_t>((i < 32 ? a.axes_lo : a.axes_hi) >> (2 * (i & 31)));
+}
+__device__ __forceinline__ int64_t position_at(const NormRopeAppendAxesArgs& a,
+                                               const AxisPositions& pos, int i) {
+  return on_axis(pos, axis_bits(a, i) & 3);
+}
+__device__ __forceinline__ bool in_table(const NormRopeAppendAxesArgs& a,
+                                         const AxisPositions& pos) {
+  bool in = true;                              // an unused axis has position 0
+#pragma unroll
+  for (int k = 0; k < kMaxRopeAxes; ++k) in = in && pos.p[k] >= 0 && pos.p[k] < a.table_positions;
+  return in;
+}
+__device__ __forceinline__ Trig table_trig(const NormRopeAppendAxesArgs& a,
+                                           const AxisPositions& pos, int l) {
+  const uint32_t bits = axis_bits(a, 4 * l);
+  if (a.lane_axes) return table_trig(a, OnePosition{on_axis(pos, bits & 3)}, l);
+  float4 c[4];
+  float* f = reinterpret_cast<float*>(c);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const float* row = reinterpret_cast<const float*>(
+        a.rope_table + (on_axis(pos, (bits >> (2 * j)) & 3) * (kHeadDim / 8) + l) * 4);
+#pragma unroll
+    for (int u = 0; u < 4; ++u) f[4 * u + j] = __ldg(row + 4 * u + j);
+  }
+  return {c[0], c[1], c[2], c[3]};
+}
+__device__ __forceinline__ __nv_bfloat16* q_row_out(const NormRopeAppendAxesArgs& a, int t,
+                                                    int h) {
+  return a.q_out + t * a.q_out_stride_t + static_cast<int64_t>(h) * a.q_out_stride_h;
+}
+
 // Loads x (and for k heads the v row) of head vector h of token t.
 __device__ __forceinline__ Loaded load_vector(const NormRopeAppendArgs& a, int t, int h, int l) {
   Loaded r;
@@ -89,7 +178,8 @@ __device__ __forceinline__ Loaded load_vector(const NormRopeAppendArgs& a, int t
 
 // Norm + rotation + stores of one head vector; both half-warps of the warp
 // call it together (the sum-of-squares shuffles are warp-wide).
-__device__ __forceinline__ void finish_vector(const NormRopeAppendArgs& a, int t, int h, int l,
+template <typename Args>
+__device__ __forceinline__ void finish_vector(const Args& a, int t, int h, int l,
                                               const Loaded& in, const uint2 (&gq)[2],
                                               const uint2 (&gk)[2], int64_t cache_row,
                                               bool write_cache, const Trig& tr) {
@@ -107,7 +197,7 @@ __device__ __forceinline__ void finish_vector(const NormRopeAppendArgs& a, int t
 
   if (h >= num_vec) return;
   if (is_q) {
-    __nv_bfloat16* dst = a.q + t * a.q_stride_t + static_cast<int64_t>(h) * a.q_stride_h;
+    __nv_bfloat16* dst = q_row_out(a, t, h);
     *reinterpret_cast<uint2*>(dst + 4 * l) = w0;
     *reinterpret_cast<uint2*>(dst + 64 + 4 * l) = w1;
   } else if (write_cache) {
@@ -123,7 +213,8 @@ __device__ __forceinline__ void finish_vector(const NormRopeAppendArgs& a, int t
 // The token's sin/cos through shared memory: the knots copied in, 64 angles
 // (one per lane of warps 0 and 1: every lane of a float64 instruction busy),
 // float64 angle and quarter-turn reduction, float-float sin/cos.  CTA-wide.
-__device__ __forceinline__ Trig angles_in_cta(const NormRopeAppendArgs& a, int64_t pos, int l,
+template <typename Args, typename Position>
+__device__ __forceinline__ Trig angles_in_cta(const Args& a, const Position& pos, int l,
                                               float (*s_tab)[4], float* s_cos_hi,
                                               float* s_cos_lo, float* s_sin_hi,
                                               float* s_sin_lo) {
@@ -137,7 +228,7 @@ __device__ __forceinline__ Trig angles_in_cta(const NormRopeAppendArgs& a, int64
   if (threadIdx.x < kHeadDim / 2) {
     const int i = threadIdx.x;
     FF x, sn, cs;
-    const int quadrant = reduce_angle(static_cast<double>(pos), a.inv_freq[i], &x);
+    const int quadrant = reduce_angle(static_cast<double>(position_at(a, pos, i)), a.inv_freq[i], &x);
     sincos_ff(x, quadrant, s_tab, &sn, &cs);
     s_cos_hi[i] = cs.hi;
     s_cos_lo[i] = cs.lo;
@@ -154,9 +245,9 @@ __device__ __forceinline__ Trig angles_in_cta(const NormRopeAppendArgs& a, int64
   return tr;
 }
 
-template <int kThreadsBound, int kMinBlocks, bool kTable>
+template <int kThreadsBound, int kMinBlocks, bool kTable, typename Args>
 __global__ void __launch_bounds__(kThreadsBound, kMinBlocks)
-norm_rope_append_kernel(const __grid_constant__ NormRopeAppendArgs a) {
+norm_rope_append_kernel(const __grid_constant__ Args a) {
   __shared__ __align__(16) float s_cos_hi[kHeadDim / 2], s_cos_lo[kHeadDim / 2];
   __shared__ __align__(16) float s_sin_hi[kHeadDim / 2], s_sin_lo[kHeadDim / 2];
   __shared__ float s_tab[kSinCosKnots][4];
@@ -174,7 +265,7 @@ norm_rope_append_kernel(const __grid_constant__ NormRopeAppendArgs a) {
   pdl_wait();
 
   // every independent global load first
-  const int64_t pos = a.positions[t];
+  const auto pos = position_of(a, t);
   const int64_t slot = a.slot_mapping[t];
   Loaded in[kHoist];
 #pragma unroll
@@ -185,14 +276,10 @@ norm_rope_append_kernel(const __grid_constant__ NormRopeAppendArgs a) {
   const uint2 gk[2] = {__ldg(reinterpret_cast<const uint2*>(a.gamma_k + 4 * l)),
                        __ldg(reinterpret_cast<const uint2*>(a.gamma_k + 64 + 4 * l))};
   // uniform over the CTA (one token)
-  const bool from_table = kTable && pos >= 0 && pos < a.table_positions;
+  const bool from_table = kTable && in_table(a, pos);
   Trig tr;
   if (from_table) {
-    const float4* row = a.rope_table + (pos * (kHeadDim / 8) + l) * 4;
-    tr.ch = __ldg(row);
-    tr.cl = __ldg(row + 1);
-    tr.sh = __ldg(row + 2);
-    tr.sl = __ldg(row + 3);
+    tr = table_trig(a, pos, l);
   } else {
     tr = angles_in_cta(a, pos, l, s_tab, s_cos_hi, s_cos_lo, s_sin_hi, s_sin_lo);
   }
@@ -219,9 +306,8 @@ norm_rope_append_kernel(const __grid_constant__ NormRopeAppendArgs a) {
   }
 }
 
-}  // namespace
-
-cudaError_t launch_norm_rope_append(const NormRopeAppendArgs& a, cudaStream_t stream) {
+template <typename Args>
+cudaError_t launch_append(const Args& a, cudaStream_t stream) {
   if (a.num_tokens == 0) return cudaSuccess;
   // few tokens: one half-warp per head vector; many: up to kHoist vectors per
   // half-warp; at least 2 warps (one angle per lane of warps 0 and 1)
@@ -232,12 +318,22 @@ cudaError_t launch_norm_rope_append(const NormRopeAppendArgs& a, cudaStream_t st
   warps = warps < 2 ? 2 : (warps > kMaxThreads / 32 ? kMaxThreads / 32 : warps);
   const bool table = a.rope_table != nullptr && a.table_positions > 0;
   if (many && warps * 32 <= kManyThreads)
-    return launch_pdl(table ? norm_rope_append_kernel<kManyThreads, kTableMinBlocks, true>
-                            : norm_rope_append_kernel<kManyThreads, kManyMinBlocks, false>,
+    return launch_pdl(table ? norm_rope_append_kernel<kManyThreads, kTableMinBlocks, true, Args>
+                            : norm_rope_append_kernel<kManyThreads, kManyMinBlocks, false, Args>,
                       dim3(a.num_tokens), dim3(warps * 32), 0, stream, a);
-  return launch_pdl(table ? norm_rope_append_kernel<kMaxThreads, 1, true>
-                          : norm_rope_append_kernel<kMaxThreads, 1, false>,
+  return launch_pdl(table ? norm_rope_append_kernel<kMaxThreads, 1, true, Args>
+                          : norm_rope_append_kernel<kMaxThreads, 1, false, Args>,
                     dim3(a.num_tokens), dim3(warps * 32), 0, stream, a);
+}
+
+}  // namespace
+
+cudaError_t launch_norm_rope_append(const NormRopeAppendArgs& a, cudaStream_t stream) {
+  return launch_append(a, stream);
+}
+
+cudaError_t launch_norm_rope_append_axes(const NormRopeAppendAxesArgs& a, cudaStream_t stream) {
+  return launch_append(a, stream);
 }
 
 namespace {
