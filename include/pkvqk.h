@@ -133,6 +133,30 @@ typedef struct pkvqk_q8_cache {
   int64_t scale_head_stride;
 } pkvqk_q8_cache;
 
+/*
+ * Rules that the scored attention calls (pkvqk_paged_decode_scored,
+ * pkvqk_paged_prefill_scored, pkvqk_paged_prefill_varlen_scored) put on scores and on
+ * what a row sees.  All zero: plain causal attention.  For the row at position
+ * p = seq_len - q_len + t of sequence b, q head h and key n:
+ *   s = scale * <q, K_n>
+ *   s = softcap * tanh(s / softcap)          where softcap > 0
+ *   s = s - slopes[h] * |p - n|              where slopes is given
+ *   n is visible where lo <= n < hi:
+ *     lo = max(0, p - window + 1 (where window > 0), first_keys[row])
+ *     hi = max(p + 1, min(prefix_lens[b], seq_len))
+ * So a window keeps the last `window` keys of a row, its own among them; first_keys
+ * gives each token row the first key of its document (or of what is not padding); a
+ * prefix is seen whole by every row of the sequence, also by those inside it, unless the
+ * window or the document hides it.
+ */
+typedef struct pkvqk_score_rules {
+  float softcap;                     /* 0 (none) or 2^-20 .. 2^20 */
+  int32_t window;                    /* keys; 0: none */
+  const float* slopes;               /* device fp32 [num_q_heads] or NULL */
+  const int32_t* first_keys;         /* device int32, one per token row of q, or NULL */
+  const int32_t* prefix_lens;        /* device int32 [batch] or NULL */
+} pkvqk_score_rules;
+
 /* Message of the last failing call made on this thread ("" if none). */
 PKVQK_API const char* pkvqk_last_error(void);
 
@@ -393,6 +417,29 @@ PKVQK_API pkvqk_status pkvqk_paged_decode(
     int32_t* status_flags, pkvqk_stream_t stream);
 
 /*
+ * pkvqk_paged_decode under score rules (pkvqk_score_rules), with the same schedules,
+ * workspace and limits.  Of a sequence only the pages from its rows' first visible key
+ * on are read, and splits are counted from the page of that key: block-table entries
+ * before it may hold anything, and max_seq_len_hint bounds the keys from there to the
+ * sequence's end (a window bounds them too, without a hint); give
+ * pkvqk_choose_num_splits such spans in place of lengths.  Slots past seq_lens[b] and before the first
+ * visible key may hold anything, NaN included.  A V that is not finite, of a key between
+ * them, may make NaN of any row of its sequence and kv head.
+ * A row with no visible key outputs 0 and lse = -inf.
+ */
+PKVQK_API pkvqk_status pkvqk_paged_decode_scored(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k_cache, const void* v_cache, const pkvqk_cache_layout* layout,
+    const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens,
+    int32_t batch, int32_t q_len, int32_t num_q_heads,
+    int32_t num_splits, int32_t max_seq_len_hint, float scale,
+    const pkvqk_score_rules* rules,
+    void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+/*
  * pkvqk_paged_decode over an 8-bit cache: the same definition with K_n and V_n
  * = code * scale, the same schedules (the balanced one with a CTA per SM),
  * pkvqk_choose_num_splits and pkvqk_decode_workspace_bytes.  Codes and q enter
@@ -635,6 +682,39 @@ PKVQK_API pkvqk_status pkvqk_paged_prefill_varlen(
     const int32_t* seq_lens,
     int32_t batch, int32_t num_q_heads,
     int32_t num_splits, int32_t max_seq_len_hint, float scale,
+    void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+/*
+ * pkvqk_paged_prefill and pkvqk_paged_prefill_varlen under score rules
+ * (pkvqk_score_rules; first_keys has one entry per row of q), with the same split choice
+ * and workspace.  Each row tile (256 / group tokens, at least one) reads the keys from its
+ * rows' first visible one to their last, and its splits are counted from the page of the
+ * first; hint, slots that no row sees and V that is not finite as for
+ * pkvqk_paged_decode_scored.
+ */
+PKVQK_API pkvqk_status pkvqk_paged_prefill_scored(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const void* k_cache, const void* v_cache, const pkvqk_cache_layout* layout,
+    const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens,
+    int32_t batch, int32_t q_len, int32_t num_q_heads,
+    int32_t num_splits, int32_t max_seq_len_hint, float scale,
+    const pkvqk_score_rules* rules,
+    void* out, float* lse_out,
+    void* workspace, size_t workspace_bytes,
+    int32_t* status_flags, pkvqk_stream_t stream);
+
+PKVQK_API pkvqk_status pkvqk_paged_prefill_varlen_scored(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h,
+    const int32_t* cu_seqlens_q, int32_t max_q_len, int64_t total_q,
+    const void* k_cache, const void* v_cache, const pkvqk_cache_layout* layout,
+    const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens,
+    int32_t batch, int32_t num_q_heads,
+    int32_t num_splits, int32_t max_seq_len_hint, float scale,
+    const pkvqk_score_rules* rules,
     void* out, float* lse_out,
     void* workspace, size_t workspace_bytes,
     int32_t* status_flags, pkvqk_stream_t stream);

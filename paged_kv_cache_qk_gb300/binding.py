@@ -64,6 +64,17 @@ class CacheLayout(ctypes.Structure):
     ]
 
 
+class ScoreRules(ctypes.Structure):
+    """Mirror of ``pkvqk_score_rules``."""
+    _fields_ = [
+        ("softcap", c_f32),
+        ("window", c_i32),
+        ("slopes", c_vp),
+        ("first_keys", c_vp),
+        ("prefix_lens", c_vp),
+    ]
+
+
 class Q8Cache(ctypes.Structure):
     """Mirror of ``pkvqk_q8_cache``."""
     _fields_ = [
@@ -204,6 +215,19 @@ pkvqk_verify_drafts = _sig("pkvqk_verify_drafts", ctypes.c_int, [
     c_vp, c_vp,                         # seq_lens, kept_lens
     c_vp, c_vp])                        # status_flags, stream
 
+_rules_args = [ctypes.POINTER(ScoreRules), c_vp, c_vp, c_vp, c_size, c_vp, c_vp]
+pkvqk_paged_decode_scored = _sig("pkvqk_paged_decode_scored", ctypes.c_int,
+                                 _decode_args + _rules_args)
+pkvqk_paged_prefill_scored = _sig("pkvqk_paged_prefill_scored", ctypes.c_int,
+                                  _decode_args + _rules_args)
+pkvqk_paged_prefill_varlen_scored = _sig("pkvqk_paged_prefill_varlen_scored", ctypes.c_int, [
+    c_vp, c_i64, c_i64,                 # q, strides
+    c_vp, c_i32, c_i64,                 # cu_seqlens_q, max_q_len, total_q
+    c_vp, c_vp, ctypes.POINTER(CacheLayout),
+    c_vp, c_i32, c_vp,                  # block_tables, max_blocks_per_seq, seq_lens
+    c_i32, c_i32,                       # batch, num_q_heads
+    c_i32, c_i32, c_f32] + _rules_args)  # num_splits, max_seq_len_hint, scale
+
 EXPORTED = [
     "pkvqk_last_error", "pkvqk_abi_version", "pkvqk_norm_rope_append",
     "pkvqk_choose_num_splits", "pkvqk_decode_workspace_bytes", "pkvqk_paged_decode",
@@ -213,6 +237,8 @@ EXPORTED = [
     "pkvqk_rope_table_bytes", "pkvqk_rope_table_build", "pkvqk_norm_rope_append_cached",
     "pkvqk_norm_rope_append_q8", "pkvqk_paged_decode_q8", "pkvqk_paged_prefill_q8",
     "pkvqk_paged_prefill_varlen_q8", "pkvqk_norm_rope_append_axes", "pkvqk_verify_drafts",
+    "pkvqk_paged_decode_scored", "pkvqk_paged_prefill_scored",
+    "pkvqk_paged_prefill_varlen_scored",
 ]
 
 
@@ -434,11 +460,11 @@ def _q8_names():
     return _q8
 
 
-_STRUCTS = (ctypes.POINTER(Q8Cache), ctypes.POINTER(CacheLayout))
+_STRUCTS = (ctypes.POINTER(Q8Cache), ctypes.POINTER(CacheLayout), ctypes.POINTER(ScoreRules))
 
 
 def _fast(name, args):
-    """The entry point with the cache (or its layout) passed as packed bytes."""
+    """The entry point with its structs passed as packed bytes."""
     f = _lib[name]
     f.restype = ctypes.c_int
     f.argtypes = [ctypes.c_char_p if a in _STRUCTS else a for a in args]
@@ -698,6 +724,89 @@ def norm_rope_append_axes(q, k, v, positions, freq_axes, slot_mapping, gamma_q, 
         _gains(t, gamma_q, "gamma_q"), _gains(t, gamma_k, "gamma_k"), theta, eps, T, Hq,
         k_cache.data_ptr(), v_cache.data_ptr(), _pack_layout(t, k_cache, v_cache),
         _ptr(rope_table), table_positions, _flags(t, status_flags), _raw_stream(t, stream, q)))
+
+
+# -------------------------------------------------------------- score rules
+
+_RULES_PACK = struct.Struct("=fi3Q")           # pkvqk_score_rules, no padding
+assert _RULES_PACK.size == ctypes.sizeof(ScoreRules)
+_paged_decode_scored = _fast("pkvqk_paged_decode_scored", pkvqk_paged_decode_scored.argtypes)
+_paged_prefill_scored = _fast("pkvqk_paged_prefill_scored", pkvqk_paged_prefill_scored.argtypes)
+_paged_prefill_varlen_scored = _fast("pkvqk_paged_prefill_varlen_scored",
+                                     pkvqk_paged_prefill_varlen_scored.argtypes)
+
+
+def _pack_rules(t, softcap, window, slopes, first_keys, prefix_lens, rows, batch, heads):
+    return _RULES_PACK.pack(
+        softcap, window,
+        0 if slopes is None else _ints(slopes, t["f32"], heads, "slopes"),
+        0 if first_keys is None else _ints(first_keys, t["i32"], rows, "first_keys"),
+        0 if prefix_lens is None else _ints(prefix_lens, t["i32"], batch, "prefix_lens"))
+
+
+def _attend_scored(f, q, k_cache, v_cache, block_tables, seq_lens, out, q_len, num_splits,
+                   max_seq_len_hint, scale, rules, lse_out, workspace, status_flags, stream):
+    t = _q8 or _q8_names()
+    rows, Hq, qs, qh = _heads(t, q, "q")
+    batch = seq_lens.shape[0]
+    if q_len * batch != rows:
+        raise ValueError("q must hold q_len rows for each sequence of seq_lens")
+    table, width = _table(t, block_tables, batch)
+    o, lse = _results(t, out, lse_out, rows, Hq)
+    check(f(
+        q.data_ptr(), qs, qh, k_cache.data_ptr(), v_cache.data_ptr(),
+        _pack_layout(t, k_cache, v_cache), table, width,
+        _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, q_len, Hq, num_splits,
+        max_seq_len_hint, scale, _pack_rules(t, *rules, rows, batch, Hq), o, lse,
+        *_workspace(workspace), _flags(t, status_flags), _raw_stream(t, stream, q)))
+
+
+def paged_decode_scored(q, k_cache, v_cache, block_tables, seq_lens, out, *, q_len=1,
+                        softcap=0.0, window=0, slopes=None, first_keys=None, prefix_lens=None,
+                        num_splits=1, max_seq_len_hint=0, scale=0.0, lse_out=None,
+                        workspace=None, status_flags=None, stream=None):
+    """paged_decode under score rules.
+
+    softcap c > 0: s -> c tanh(s / c); slopes fp32 [Hq]: s - slope |p - n| for the row at
+    position p and key n; window w > 0: only the last w keys of a row; first_keys int32, one
+    per row of q: no key before it; prefix_lens int32 [B]: keys that every row of the
+    sequence sees, also those before them.
+    """
+    _attend_scored(_paged_decode_scored, q, k_cache, v_cache, block_tables, seq_lens, out, q_len,
+                   num_splits, max_seq_len_hint, scale,
+                   (softcap, window, slopes, first_keys, prefix_lens), lse_out, workspace,
+                   status_flags, stream)
+
+
+def paged_prefill_scored(q, k_cache, v_cache, block_tables, seq_lens, out, *, q_len, softcap=0.0,
+                         window=0, slopes=None, first_keys=None, prefix_lens=None, num_splits=1,
+                         max_seq_len_hint=0, scale=0.0, lse_out=None, workspace=None,
+                         status_flags=None, stream=None):
+    """paged_prefill under score rules (see paged_decode_scored)."""
+    _attend_scored(_paged_prefill_scored, q, k_cache, v_cache, block_tables, seq_lens, out, q_len,
+                   num_splits, max_seq_len_hint, scale,
+                   (softcap, window, slopes, first_keys, prefix_lens), lse_out, workspace,
+                   status_flags, stream)
+
+
+def paged_prefill_varlen_scored(q, cu_seqlens_q, max_q_len, k_cache, v_cache, block_tables,
+                                seq_lens, out, *, softcap=0.0, window=0, slopes=None,
+                                first_keys=None, prefix_lens=None, num_splits=1,
+                                max_seq_len_hint=0, scale=0.0, lse_out=None, workspace=None,
+                                status_flags=None, stream=None):
+    """paged_prefill_varlen under score rules (see paged_decode_scored)."""
+    t = _q8 or _q8_names()
+    total_q, Hq, qs, qh = _heads(t, q, "q")
+    batch = seq_lens.shape[0]
+    table, width = _table(t, block_tables, batch)
+    o, lse = _results(t, out, lse_out, total_q, Hq)
+    check(_paged_prefill_varlen_scored(
+        q.data_ptr(), qs, qh, _ints(cu_seqlens_q, t["i32"], batch + 1, "cu_seqlens_q"), max_q_len,
+        total_q, k_cache.data_ptr(), v_cache.data_ptr(), _pack_layout(t, k_cache, v_cache), table,
+        width, _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, Hq, num_splits,
+        max_seq_len_hint, scale,
+        _pack_rules(t, softcap, window, slopes, first_keys, prefix_lens, total_q, batch, Hq), o,
+        lse, *_workspace(workspace), _flags(t, status_flags), _raw_stream(t, stream, q)))
 
 
 # ----------------------------------------------------------- drafted tokens

@@ -23,7 +23,8 @@ BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpkvqk.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "norm_rope_append.cu", "decode.cu", "combine.cu", "decode_static_ws.cu",
-           "prefill.cu", "norm_rope_append_q8.cu", "decode_q8.cu", "verify_drafts.cu"]
+           "prefill.cu", "norm_rope_append_q8.cu", "decode_q8.cu", "verify_drafts.cu",
+           "decode_scored.cu", "prefill_scored.cu"]
 
 
 def nvcc() -> str:

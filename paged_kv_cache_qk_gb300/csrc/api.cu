@@ -253,7 +253,53 @@ struct DecodeCall {
   cudaStream_t stream;
   bool partials_only;
   const pkvqk_q8_cache* q8 = nullptr;          // 8-bit cache (k_cache, v_cache, layout are its)
+  const pkvqk_score_rules* rules = nullptr;    // scored calls
 };
+
+pkvqk_status check_rules(const pkvqk_score_rules* r) {
+  if (r == nullptr) return fail(PKVQK_ERR_INVALID_ARG, "rules is NULL");
+  if (r->softcap != 0.f && !(r->softcap >= 0x1p-20f && r->softcap <= 0x1p20f))
+    return fail(PKVQK_ERR_INVALID_ARG, "softcap %g (0, or 2^-20 .. 2^20)", r->softcap);
+  if (r->window < 0) return fail(PKVQK_ERR_INVALID_ARG, "window %d", r->window);
+  return PKVQK_OK;
+}
+
+// The rules' device pointers.
+pkvqk_status check_rule_ptrs(const pkvqk_score_rules& r) {
+  const void* ptr[3] = {r.slopes, r.first_keys, r.prefix_lens};
+  const char* nm[3] = {"slopes", "first_keys", "prefix_lens"};
+  for (int i = 0; i < 3; ++i) {
+    if (ptr[i] == nullptr) continue;
+    PKVQK_TRY(check_device_ptr(ptr[i], nm[i]));
+    if (reinterpret_cast<uintptr_t>(ptr[i]) & 3u)
+      return fail(PKVQK_ERR_INVALID_ARG, "%s not 4-byte aligned", nm[i]);
+  }
+  return PKVQK_OK;
+}
+
+pkvqk::ScoreRules kernel_rules(const pkvqk_score_rules& r) {
+  pkvqk::ScoreRules k = {};
+  if (r.softcap > 0.f) {
+    k.cap = r.softcap * 1.4426950408889634f;
+    k.inv_cap = 1.f / k.cap;
+  }
+  k.window = r.window;
+  k.slopes = r.slopes;
+  k.first_keys = r.first_keys;
+  k.prefix_lens = r.prefix_lens;
+  return k;
+}
+
+// Pages that the longest span of keys of `tokens` neighbouring rows fills, by the hint and
+// by a window.  A span that starts inside a page touches one more, and a prefix reaches past
+// a window: the last split takes what is over.
+int span_pages(const DecodeCall& c, int hint, int64_t tokens) {
+  const int bs = c.layout->block_size;
+  int64_t keys = hint;
+  if (c.rules != nullptr && c.rules->window > 0)
+    keys = std::min(keys, c.rules->window + tokens - 1);
+  return static_cast<int>((keys + bs - 1) / bs);
+}
 
 pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64_t total_q);
 
@@ -342,6 +388,7 @@ pkvqk_status run_decode(const DecodeCall& c) {
   }
   if (c.status_flags != nullptr) PKVQK_TRY(check_device_ptr(c.status_flags, "status_flags"));
   if (c.q8 != nullptr) PKVQK_TRY(check_q8_scales(*c.q8));
+  if (c.rules != nullptr) PKVQK_TRY(check_rule_ptrs(*c.rules));
 
   CUtensorMap kmap, vmap;
   const auto encode = [&](CUtensorMap* m, const void* base) {
@@ -351,7 +398,7 @@ pkvqk_status run_decode(const DecodeCall& c) {
   PKVQK_TRY(encode(&kmap, c.k_cache));
   PKVQK_TRY(encode(&vmap, c.v_cache));
 
-  const int hint_pages = (hint + L.block_size - 1) / L.block_size;
+  const int hint_pages = span_pages(c, hint, c.q_len);
   pkvqk::DecodeArgs a;
   a.q = static_cast<const __nv_bfloat16*>(c.q);
   a.q_stride_t = c.q_stride_t;
@@ -387,12 +434,16 @@ pkvqk_status run_decode(const DecodeCall& c) {
     a.ws_lse = a.ws_o + nrows * S * 128;
   }
   a.status_flags = c.status_flags;
+  a.rules = c.rules != nullptr ? kernel_rules(*c.rules) : pkvqk::ScoreRules{};
 
-  cudaError_t e =
-      c.q8 != nullptr
-          ? pkvqk::launch_paged_decode_q8(plan, kmap, vmap, a, scale_view(*c.q8), c.q8->format,
-                                          grid_ctas, c.stream)
-          : pkvqk::launch_paged_decode(plan, kmap, vmap, a, grid_ctas, c.stream);
+  cudaError_t e;
+  if (c.q8 != nullptr)
+    e = pkvqk::launch_paged_decode_q8(plan, kmap, vmap, a, scale_view(*c.q8), c.q8->format,
+                                      grid_ctas, c.stream);
+  else if (c.rules != nullptr)
+    e = pkvqk::launch_paged_decode_scored(plan, kmap, vmap, a, grid_ctas, c.stream);
+  else
+    e = pkvqk::launch_paged_decode(plan, kmap, vmap, a, grid_ctas, c.stream);
   if (e != cudaSuccess) return cuda_fail(e, "paged decode launch");
   if (S == 0) {
     e = pkvqk::launch_balanced_combine(a, plan.heads_per_cta, c.stream);
@@ -478,6 +529,7 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
   if (c.status_flags != nullptr) PKVQK_TRY(check_device_ptr(c.status_flags, "status_flags"));
 
   if (c.q8 != nullptr) PKVQK_TRY(check_q8_scales(*c.q8));
+  if (c.rules != nullptr) PKVQK_TRY(check_rule_ptrs(*c.rules));
 
   CUtensorMap kmap, vmap;
   // largest power of two dividing the page size, at most 128 (the kernel's key
@@ -492,7 +544,9 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
   }
 
   const int hint = c.max_seq_len_hint > 0 ? c.max_seq_len_hint : static_cast<int>(cap_tokens);
-  const int hint_pages = (hint + L.block_size - 1) / L.block_size;
+  // a row tile's rows share their keys
+  const int hint_pages =
+      span_pages(c, hint, std::min<int64_t>(c.q_len, pkvqk::kPrefillRowsPerCta / group + 1));
   pkvqk::PrefillArgs a = {};
   a.q = static_cast<const __nv_bfloat16*>(c.q);
   a.q_stride_t = c.q_stride_t;
@@ -527,9 +581,15 @@ pkvqk_status run_prefill(const DecodeCall& c, const int32_t* cu_seqlens_q, int64
     a.groups_per_page_inv = static_cast<uint32_t>(
         ((uint64_t(1) << 32) + a.groups_per_page - 1) / a.groups_per_page);
   }
-  cudaError_t e = c.q8 != nullptr
-                      ? pkvqk::launch_paged_prefill_q8(kmap, vmap, a, c.q8->format, c.stream)
-                      : pkvqk::launch_paged_prefill(kmap, vmap, a, c.stream);
+  cudaError_t e;
+  if (c.q8 != nullptr) {
+    e = pkvqk::launch_paged_prefill_q8(kmap, vmap, a, c.q8->format, c.stream);
+  } else if (c.rules != nullptr) {
+    a.rules = kernel_rules(*c.rules);
+    e = pkvqk::launch_paged_prefill_scored(kmap, vmap, a, c.stream);
+  } else {
+    e = pkvqk::launch_paged_prefill(kmap, vmap, a, c.stream);
+  }
   if (e != cudaSuccess) return cuda_fail(e, "paged prefill launch");
   if (S > 1 && !c.partials_only) {
     e = pkvqk::launch_lse_combine(a.ws_o, a.ws_lse, static_cast<int>(nrows), S, a.out, c.lse_out,
@@ -1095,6 +1155,62 @@ pkvqk_status pkvqk_paged_prefill_varlen(const void* q, int64_t q_stride_t, int64
                max_q_len,  num_q_heads, num_splits,       max_seq_len_hint, scale,
                out,        lse_out,     workspace,        workspace_bytes_, status_flags,
                reinterpret_cast<cudaStream_t>(stream), false};
+  return run_prefill(c, cu_seqlens_q, total_q);
+}
+
+pkvqk_status pkvqk_paged_decode_scored(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                       const void* k_cache, const void* v_cache,
+                                       const pkvqk_cache_layout* layout,
+                                       const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                       const int32_t* seq_lens, int32_t batch, int32_t q_len,
+                                       int32_t num_q_heads, int32_t num_splits,
+                                       int32_t max_seq_len_hint, float scale,
+                                       const pkvqk_score_rules* rules, void* out, float* lse_out,
+                                       void* workspace, size_t workspace_bytes_,
+                                       int32_t* status_flags, pkvqk_stream_t stream) {
+  PKVQK_TRY(check_rules(rules));
+  DecodeCall c{q,          q_stride_t,  q_stride_h,       k_cache,    v_cache,
+               layout,     block_tables, max_blocks_per_seq, seq_lens, batch,
+               q_len,      num_q_heads, num_splits,       max_seq_len_hint, scale,
+               out,        lse_out,     workspace,        workspace_bytes_, status_flags,
+               reinterpret_cast<cudaStream_t>(stream), false, nullptr, rules};
+  return run_decode(c);
+}
+
+pkvqk_status pkvqk_paged_prefill_scored(const void* q, int64_t q_stride_t, int64_t q_stride_h,
+                                        const void* k_cache, const void* v_cache,
+                                        const pkvqk_cache_layout* layout,
+                                        const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                        const int32_t* seq_lens, int32_t batch, int32_t q_len,
+                                        int32_t num_q_heads, int32_t num_splits,
+                                        int32_t max_seq_len_hint, float scale,
+                                        const pkvqk_score_rules* rules, void* out, float* lse_out,
+                                        void* workspace, size_t workspace_bytes_,
+                                        int32_t* status_flags, pkvqk_stream_t stream) {
+  PKVQK_TRY(check_rules(rules));
+  DecodeCall c{q,          q_stride_t,  q_stride_h,       k_cache,    v_cache,
+               layout,     block_tables, max_blocks_per_seq, seq_lens, batch,
+               q_len,      num_q_heads, num_splits,       max_seq_len_hint, scale,
+               out,        lse_out,     workspace,        workspace_bytes_, status_flags,
+               reinterpret_cast<cudaStream_t>(stream), false, nullptr, rules};
+  return run_prefill(c, nullptr, static_cast<int64_t>(batch) * q_len);
+}
+
+pkvqk_status pkvqk_paged_prefill_varlen_scored(
+    const void* q, int64_t q_stride_t, int64_t q_stride_h, const int32_t* cu_seqlens_q,
+    int32_t max_q_len, int64_t total_q, const void* k_cache, const void* v_cache,
+    const pkvqk_cache_layout* layout, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens, int32_t batch, int32_t num_q_heads, int32_t num_splits,
+    int32_t max_seq_len_hint, float scale, const pkvqk_score_rules* rules, void* out,
+    float* lse_out, void* workspace, size_t workspace_bytes_, int32_t* status_flags,
+    pkvqk_stream_t stream) {
+  PKVQK_TRY(check_rules(rules));
+  if (cu_seqlens_q == nullptr) return fail(PKVQK_ERR_INVALID_ARG, "cu_seqlens_q is NULL");
+  DecodeCall c{q,          q_stride_t,  q_stride_h,       k_cache,    v_cache,
+               layout,     block_tables, max_blocks_per_seq, seq_lens, batch,
+               max_q_len,  num_q_heads, num_splits,       max_seq_len_hint, scale,
+               out,        lse_out,     workspace,        workspace_bytes_, status_flags,
+               reinterpret_cast<cudaStream_t>(stream), false, nullptr, rules};
   return run_prefill(c, cu_seqlens_q, total_q);
 }
 

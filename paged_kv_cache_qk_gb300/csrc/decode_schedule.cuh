@@ -5,6 +5,7 @@
 
 #include "device_common.cuh"
 #include "kernels.h"
+#include "score_rules.cuh"
 
 namespace pkvqk {
 
@@ -17,6 +18,7 @@ constexpr int kDestSlot = 2;    // partial at [slot][row in unit] (balanced sche
 // A run of 16-key tiles of one (sequence, head group): keys [k0, k1).
 struct Segment {
   int b, hg, seq_len, k0, k1, ntiles, dest, split;
+  int first;                // scored: keys below it are visible to no row of the sequence
   long long slot;
 };
 
@@ -31,9 +33,37 @@ __device__ __forceinline__ int clamped_len(const DecodeArgs& a, int b) {
   return L;
 }
 
+// Pages of a sequence of L keys that the call walks: all of them, or with score rules
+// those from the first key that a row sees.
+struct PageSpan {
+  int first_key, first_page, pages;
+};
+
+template <bool kScored>
+__device__ __forceinline__ PageSpan page_span(const DecodeArgs& a, int b, int L) {
+  const int P = (L + a.block_size - 1) / a.block_size;
+  if constexpr (!kScored) {
+    return {0, 0, P};
+  } else {
+    const int p = L - a.q_len;                 // position of the sequence's first row
+    int lo = window_start(a.rules, p);
+    if (a.rules.first_keys != nullptr) {
+      int least = L;
+      for (int t = 0; t < a.q_len; ++t)
+        least = min(least, max(window_start(a.rules, p + t),
+                               a.rules.first_keys[static_cast<long long>(b) * a.q_len + t]));
+      lo = max(least, 0);
+    }
+    lo = min(lo, L);
+    const int first_page = lo < L ? lo / a.block_size : P;
+    return {lo, first_page, P - first_page};
+  }
+}
+
+template <bool kScored = false>
 __device__ __forceinline__ long long unit_pages(const DecodeArgs& a, int u) {
-  const int L = clamped_len(a, u % a.batch);
-  return (L + a.block_size - 1) / a.block_size;
+  const int b = u % a.batch;
+  return page_span<kScored>(a, b, clamped_len(a, b)).pages;
 }
 
 __device__ __forceinline__ void set_range(Segment& s, int k0, int k1, int tk) {
@@ -52,7 +82,8 @@ struct Plan {
 
 // Produces the CTA's segments in order; producer and consumers each run
 // their own copy and see the same sequence.
-struct SegmentSource {
+template <bool kScored = false>
+struct SegmentSourceOf {
   const DecodeArgs* a;
   const Plan* plan;
   int tk;                   // keys per tile
@@ -75,6 +106,14 @@ struct SegmentSource {
     }
   }
 
+  // pages [p0, p1) of the span; a scored sequence starts at its first key's tile
+  __device__ __forceinline__ void set_pages(Segment& seg, const PageSpan& span, int p0, int p1) {
+    int k0 = (span.first_page + p0) * a->block_size;
+    if (kScored) k0 = max(k0, span.first_key & ~(tk - 1));
+    seg.first = span.first_key;
+    set_range(seg, k0, min((span.first_page + p1) * a->block_size, seg.seq_len), tk);
+  }
+
   __device__ bool next(Segment& seg) {
     if (!balanced) {
       if (done) return false;
@@ -84,12 +123,13 @@ struct SegmentSource {
       seg.split = blockIdx.x;
       seg.slot = 0;
       seg.seq_len = clamped_len(*a, seg.b);
-      const int P = (seg.seq_len + a->block_size - 1) / a->block_size;
+      const PageSpan span = page_span<kScored>(*a, seg.b, seg.seq_len);
+      const int P = span.pages;
       int p0 = seg.split * a->chunk_pages;
       int p1 = (seg.split == a->num_splits - 1) ? P : p0 + a->chunk_pages;
       p0 = min(p0, P);
       p1 = min(p1, P);
-      set_range(seg, p0 * a->block_size, min(p1 * a->block_size, seg.seq_len), tk);
+      set_pages(seg, span, p0, p1);
       seg.dest = a->num_splits == 1 ? kDestFinal : kDestSplit;
       return true;
     }
@@ -97,7 +137,9 @@ struct SegmentSource {
     while (u < U && s < plan->hi) {
       const int cur = u;
       const long long start = s;
-      const long long P = unit_pages(*a, cur);
+      const int len = clamped_len(*a, cur % a->batch);
+      const PageSpan span = page_span<kScored>(*a, cur % a->batch, len);
+      const long long P = span.pages;
       u += 1;
       s += P;
       const long long plo = max(start, plan->lo) - start;
@@ -106,9 +148,8 @@ struct SegmentSource {
       seg.b = cur % a->batch;
       seg.hg = cur / a->batch;
       seg.split = 0;
-      seg.seq_len = clamped_len(*a, seg.b);
-      set_range(seg, static_cast<int>(plo) * a->block_size,
-                min(static_cast<int>(phi) * a->block_size, seg.seq_len), tk);
+      seg.seq_len = len;
+      set_pages(seg, span, static_cast<int>(plo), static_cast<int>(phi));
       const bool whole = plo == 0 && phi == P;
       seg.dest = whole ? kDestFinal : kDestSlot;
       seg.slot = static_cast<long long>(blockIdx.x) + cur;
@@ -124,7 +165,10 @@ struct SegmentSource {
   }
 };
 
+using SegmentSource = SegmentSourceOf<>;
+
 // Block-wide plan of the balanced schedule (every thread takes part).
+template <bool kScored = false>
 __device__ inline void make_plan(const DecodeArgs& a, Plan* plan, long long* wsum) {
   const int U = a.batch * a.groups;
   const int nt = blockDim.x, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -132,7 +176,7 @@ __device__ inline void make_plan(const DecodeArgs& a, Plan* plan, long long* wsu
   const int chunk = (U + nt - 1) / nt;
   const int u_lo = min(U, tid * chunk), u_hi = min(U, u_lo + chunk);
   long long mine = 0;
-  for (int u = u_lo; u < u_hi; ++u) mine += unit_pages(a, u);
+  for (int u = u_lo; u < u_hi; ++u) mine += unit_pages<kScored>(a, u);
   long long v = mine;                                       // inclusive warp scan
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
@@ -161,7 +205,7 @@ __device__ inline void make_plan(const DecodeArgs& a, Plan* plan, long long* wsu
   const long long lo = c < G ? c * tp / G : tp, hi = c < G ? (c + 1) * tp / G : tp;
   long long run = before;
   for (int u = u_lo; u < u_hi; ++u) {
-    const long long P = unit_pages(a, u);
+    const long long P = unit_pages<kScored>(a, u);
     if (run + P > lo) {
       atomicMin(&plan->u_start, u);
       break;
@@ -172,7 +216,7 @@ __device__ inline void make_plan(const DecodeArgs& a, Plan* plan, long long* wsu
   run = before;
   for (int u = u_lo; u < u_hi; ++u) {
     if (u == plan->u_start) plan->s_start = run;
-    run += unit_pages(a, u);
+    run += unit_pages<kScored>(a, u);
   }
   if (tid == 0) {
     plan->tp = tp;
@@ -186,10 +230,11 @@ __device__ inline void make_plan(const DecodeArgs& a, Plan* plan, long long* wsu
 
 // Units without any key: zero output, lse -inf, nothing to combine.  Unit u
 // is handled by CTA u mod G (all threads of the CTA).
+template <bool kScored = false>
 __device__ inline void write_empty_units(const DecodeArgs& a, int hpc) {
   const int U = a.batch * a.groups;
   for (int u = blockIdx.x; u < U; u += gridDim.x) {
-    if (unit_pages(a, u) != 0) continue;
+    if (unit_pages<kScored>(a, u) != 0) continue;
     const int b = u % a.batch, hg = u / a.batch;
     const int rows = a.rows_per_unit;
     for (int idx = threadIdx.x; idx < rows * (kHeadDim / 8); idx += blockDim.x) {

@@ -108,6 +108,17 @@ struct VerifyArgs {
 cudaError_t launch_verify_drafts(const VerifyArgs& a, int type, int sm_count,
                                  cudaStream_t stream);
 
+// Score rules of the scored attention kernels (score_rules.cuh); the plain ones do not
+// look at them.
+struct ScoreRules {
+  float cap;                       // softcap * log2(e); 0: none
+  float inv_cap;                   // 1 / cap
+  int32_t window;                  // 0: none
+  const float* slopes;             // [num_q_heads] or nullptr
+  const int32_t* first_keys;       // [token rows] or nullptr
+  const int32_t* prefix_lens;      // [batch] or nullptr
+};
+
 struct DecodeArgs {
   const __nv_bfloat16* q;
   int64_t q_stride_t, q_stride_h;
@@ -128,6 +139,7 @@ struct DecodeArgs {
   float* ws_lse;                 // partial lse
   int2* unit_info;               // balanced: first and last CTA of every (seq, group) unit
   int32_t* status_flags;
+  ScoreRules rules;              // scored kernels only
 };
 
 // Kernel family chosen by the host for a decode call.
@@ -145,6 +157,11 @@ DecodePlan plan_decode(int num_kv_heads, int rows);
 cudaError_t launch_paged_decode(const DecodePlan& plan, const CUtensorMap& kmap,
                                 const CUtensorMap& vmap, const DecodeArgs& a, int grid_ctas,
                                 cudaStream_t stream);
+
+// The same with a.rules.
+cudaError_t launch_paged_decode_scored(const DecodePlan& plan, const CUtensorMap& kmap,
+                                       const CUtensorMap& vmap, const DecodeArgs& a,
+                                       int grid_ctas, cudaStream_t stream);
 
 // The same over an 8-bit cache (rows = q_len * group <= 16): kernel family,
 // ring geometry and launch.  The maps are 4-D views (dims, slots, kv heads,

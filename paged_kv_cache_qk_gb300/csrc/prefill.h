@@ -50,16 +50,25 @@ struct PrefillArgs {
   ScaleView scales;
   uint32_t groups_per_page;        // block_size / 16, 1 .. 16, and
   uint32_t groups_per_page_inv;    // ceil(2^32 / it): exact quotients up to 2^28 groups
+  ScoreRules rules;                // scored kernels only
 };
 
 // Shared-memory bytes one CTA of the kernel takes (one CTA per SM).
 int prefill_smem_bytes();
+
+// A row-tile map of q or out (prefill.cu); false where the layout does not allow one.
+bool encode_rows_map(CUtensorMap* map, const void* base, long long tokens, int heads,
+                     long long stride_h, long long stride_t, int group);
 
 // Tensor maps: 5-D cache views with a box of (64 dims, b slots, 1 half, 1 head,
 // 1 block), b = the largest power of two dividing block_size, at most 128.
 // The q and out row-tile maps are built here (where the layouts allow them).
 cudaError_t launch_paged_prefill(const CUtensorMap& kmap, const CUtensorMap& vmap,
                                  const PrefillArgs& a, cudaStream_t stream);
+
+// The same with a.rules.
+cudaError_t launch_paged_prefill_scored(const CUtensorMap& kmap, const CUtensorMap& vmap,
+                                        const PrefillArgs& a, cudaStream_t stream);
 
 // The same over an 8-bit cache of the given format; 4-D maps of its codes with a
 // box of (128 dims, b slots, 1 head, 1 block), b as above.

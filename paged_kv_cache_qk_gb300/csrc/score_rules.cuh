@@ -1,0 +1,90 @@
+// What the scored attention kernels do to a score, and which keys a row sees.
+//
+// A score s = scale <q, K_n> of the row at position p becomes, in this order,
+//     s = c tanh(s / c)          (a cap c > 0)
+//     s = s - slope_h |p - n|    (a bias by distance)
+// and counts where lo <= n < hi, with
+//     lo = max(0, p - window + 1, first_key of the row),
+//     hi = max(p + 1, min(prefix_len of the sequence, seq_len)):
+// every combination of a causal mask, a window, documents and a prefix leaves a row one
+// interval of keys.  Scores are kept in units of log2(e), so that the softmax's 2^x takes
+// them as they are.
+//
+// tanh without cancellation: below |x| = 0.6 it is x Q(x^2), Q of degree 5 fitted to
+// tanh(x) / x at Chebyshev nodes (largest relative error 2.6e-9, 4.7e-8 evaluated in
+// fp32), which takes no special-function unit; beyond, 1 - 2 / (1 + e^2x), whose absolute
+// error of ~1.2e-7 is relative there.  The units' exponentials and reciprocals are what
+// the softmax itself is short of, so a warp computes the second form only where one of
+// its scores is that large.
+#pragma once
+
+#include "device_common.cuh"
+#include "kernels.h"
+
+namespace pkvqk {
+
+constexpr float kTanhSquare = 0.36f;           // x^2 up to which the polynomial serves
+__device__ __forceinline__ constexpr float tanh_q(int i) {
+  return i == 0   ? 1.0f
+         : i == 1 ? -0.33333284f
+         : i == 2 ? 0.13331705f
+         : i == 3 ? -0.053769923f
+         : i == 4 ? 0.020757476f
+                  : -0.0058564278f;
+}
+
+// 1 - 2 / (1 + e^(2 x)), e^(2 x) = 2^(2 log2(e) x)
+__device__ __forceinline__ float tanh_far(float x) {
+  float e, r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(e) : "f"(x * 2.885390081777927f));
+  asm("rcp.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(1.f + e));
+  return fmaf(-2.f, r, 1.f);
+}
+
+__device__ __forceinline__ float tanh_near(float x, float u) {
+  float q = tanh_q(5);
+#pragma unroll
+  for (int i = 4; i >= 0; --i) q = fmaf(q, u, tanh_q(i));
+  return q * x;
+}
+
+// N scores of every lane of a warp capped in place.
+template <int N>
+__device__ __forceinline__ void cap_scores(const ScoreRules& r, float (&z)[N]) {
+  float x[N];
+  bool far = false;
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    x[i] = z[i] * r.inv_cap;
+    const float u = x[i] * x[i];
+    z[i] = tanh_near(x[i], u) * r.cap;
+    far = far || !(u <= kTanhSquare);
+  }
+  if (__any_sync(0xffffffffu, far)) {
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+      if (!(x[i] * x[i] <= kTanhSquare)) z[i] = tanh_far(x[i]) * r.cap;
+  }
+}
+
+// The keys [lo, hi) that the row at position p sees; row: its place among the call's
+// token rows, L: its sequence's keys.
+struct Interval {
+  int lo, hi;
+};
+__device__ __forceinline__ int window_start(const ScoreRules& r, int p) {
+  return r.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(p) - r.window + 1)) : 0;
+}
+__device__ __forceinline__ int prefix_end(const ScoreRules& r, int b, int L) {
+  return r.prefix_lens != nullptr ? min(r.prefix_lens[b], L) : 0;
+}
+__device__ __forceinline__ Interval visible_keys(const ScoreRules& r, int b, long long row, int p,
+                                                 int L) {
+  Interval v;
+  v.lo = window_start(r, p);
+  if (r.first_keys != nullptr) v.lo = max(v.lo, r.first_keys[row]);
+  v.hi = max(p + 1, prefix_end(r, b, L));
+  return v;
+}
+
+}  // namespace pkvqk

@@ -1,5 +1,6 @@
-"""Refusals of the append with positions of several axes and of the verdict on drafts (no
-GPU needed): every case fails before a pointer is looked at."""
+"""Refusals of the append with positions of several axes, of attention under score rules
+and of the verdict on drafts (no GPU needed): every case fails before a pointer is looked
+at."""
 
 import ctypes
 
@@ -147,3 +148,70 @@ def _draft_tensors():
 def test_draft_tensors_refused(lib, name, value, words):
     with pytest.raises(ValueError, match=words):
         lib.verify_drafts(**(_draft_tensors() | {name: value}))
+
+
+def _scored(lib, name, softcap=0.0, window=0, rules=True, B=4, T=1, Hq=16, S=1, ws=0, scale=0.0,
+            d=128):
+    lay = _layout(lib, d=d)
+    r = lib.ScoreRules(softcap, window, None, None, None)
+    rules = ctypes.byref(r) if rules else None
+    if name == "pkvqk_paged_prefill_varlen_scored":
+        return getattr(lib, name)(FAKE, 2048, 128, FAKE, T, B * T, FAKE, FAKE, ctypes.byref(lay),
+                                  FAKE, 16, FAKE, B, Hq, S, 256, scale, rules, FAKE, None, FAKE,
+                                  ws, None, None)
+    return getattr(lib, name)(FAKE, 2048, 128, FAKE, FAKE, ctypes.byref(lay), FAKE, 16, FAKE, B, T,
+                              Hq, S, 256, scale, rules, FAKE, None, FAKE, ws, None, None)
+
+
+SCORED = ["pkvqk_paged_decode_scored", "pkvqk_paged_prefill_scored",
+          "pkvqk_paged_prefill_varlen_scored"]
+
+
+@pytest.mark.parametrize("name", SCORED)
+@pytest.mark.parametrize("more,code,words", [
+    (dict(rules=False), "INVALID_ARG", "rules is NULL"),
+    (dict(softcap=-1.0), "INVALID_ARG", "softcap"),
+    (dict(softcap=float("nan")), "INVALID_ARG", "softcap"),
+    (dict(softcap=float("inf")), "INVALID_ARG", "softcap"),
+    (dict(softcap=2.0 ** -21), "INVALID_ARG", "softcap"),
+    (dict(softcap=2.0 ** 21), "INVALID_ARG", "softcap"),
+    (dict(window=-1), "INVALID_ARG", "window"),
+    (dict(Hq=12), "INVALID_ARG", "num_q_heads"), (dict(T=0), "INVALID_ARG", "q_len"),
+    (dict(S=257), "INVALID_ARG", "num_splits"), (dict(S=2), "WORKSPACE_TOO_SMALL", "workspace"),
+    (dict(scale=float("nan")), "INVALID_ARG", "scale"), (dict(d=64), "UNSUPPORTED", "head_dim"),
+])
+def test_scored_refusals(lib, name, more, code, words):
+    _refused(lib, _scored(lib, name, **more), code, words)
+
+
+@pytest.mark.parametrize("name", SCORED)
+def test_scored_attention_of_nothing(lib, name):
+    assert _scored(lib, name, softcap=5.0, window=3, B=0) == lib.PKVQK_OK
+
+
+@pytest.mark.parametrize("name,value,words", [
+    ("slopes", torch.zeros(3), "slopes"), ("slopes", torch.zeros(4, dtype=torch.float64), "slopes"),
+    ("first_keys", torch.zeros(2, dtype=torch.int32), "first_keys"),
+    ("first_keys", torch.zeros(6, dtype=torch.int64), "first_keys"),
+    ("prefix_lens", torch.zeros(6, dtype=torch.int32), "prefix_lens"),
+    ("out", torch.zeros(6, 4, 128), "out"), ("lse_out", torch.zeros(5, 4), "lse_out"),
+    ("k_cache", torch.zeros(3, 16, 2, 128), "bfloat16"),
+    ("seq_lens", torch.zeros(2, dtype=torch.int64), "seq_lens"),
+    ("block_tables", torch.zeros(3, 2, dtype=torch.int32), "block_tables"),
+    ("q_len", 2, "q_len"),
+])
+def test_scored_tensors_refused(lib, name, value, words):
+    h = dict(dtype=torch.bfloat16)
+    args = dict(q=torch.zeros(6, 4, 128, **h), k_cache=torch.zeros(3, 16, 2, 128, **h),
+                v_cache=torch.zeros(3, 16, 2, 128, **h),
+                block_tables=torch.zeros(2, 2, dtype=torch.int32),
+                seq_lens=torch.zeros(2, dtype=torch.int32), out=torch.zeros(6, 4, 128, **h),
+                q_len=3) | {name: value}
+    for f in (lib.paged_decode_scored, lib.paged_prefill_scored):
+        with pytest.raises(ValueError, match=words):
+            f(**args)
+    if name != "q_len":
+        del args["q_len"]
+        cu = torch.tensor([0, 3, 6], dtype=torch.int32)
+        with pytest.raises(ValueError, match=words):
+            lib.paged_prefill_varlen_scored(args.pop("q"), cu, 3, **args)
