@@ -24,46 +24,99 @@
 
 #include <cuda_fp16.h>
 
+#include <type_traits>
+
 namespace pkvqk {
 
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
-constexpr int kCtasPerSm = 2;
+constexpr int kCtasPerSm = 4;
 constexpr int kMaxCluster = 16;
-constexpr int kDepth = 4;                      // vectors of p (and of q) in flight a lane
-constexpr float kOne = 17592186044416.f;       // 2^44: weight 1
+constexpr int kDepth = 4;                      // loads of p (and of q) in flight a lane
+constexpr int kGroups = 64;                    // sums kept a warp, of equal runs of its part
 
-__device__ __forceinline__ float as_float(float x) { return x; }
-__device__ __forceinline__ float as_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-__device__ __forceinline__ float as_float(__half x) { return __half2float(x); }
+// A value's bits, and value i of words that hold them one after another.
+template <typename T>
+__device__ __forceinline__ uint32_t bits_at(const T* p) {
+  if constexpr (sizeof(T) == 4) return *reinterpret_cast<const uint32_t*>(p);
+  else return *reinterpret_cast<const uint16_t*>(p);
+}
+template <typename T>
+__device__ __forceinline__ float value_in(const uint32_t* words, int i) {
+  if constexpr (sizeof(T) == 4) {
+    return __uint_as_float(words[i]);
+  } else if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    return (i & 1) ? bf16hi(words[i >> 1]) : bf16lo(words[i >> 1]);
+  } else {
+    return __half2float(__ushort_as_half(static_cast<uint16_t>(words[i >> 1] >> (16 * (i & 1)))));
+  }
+}
+template <typename T>
+__device__ __forceinline__ float value_at(const T* p) {
+  const uint32_t w = bits_at(p);
+  return value_in<T>(&w, 0);
+}
 
-// A probability as a multiple of 2^-44: NaN and below 0 count as 0, above 1 as 1.
-__device__ __forceinline__ unsigned long long fixed(float x) {
-  return __float2ull_rn(fminf(fmaxf(x, 0.f), 1.f) * kOne);
+// A probability as a multiple of 2^-44, in two parts of fp32 and integer instructions
+// (float to 64-bit integer runs at a small fraction of their rate: 64 sequences over 131072
+// tokens took 50 us with it): x 2^22 rounded to a whole number h, the low bits of
+// x 2^22 + 2^23, and what is left, x - h 2^-22 (exact), times 2^44 rounded to a whole number
+// l, |l| <= 2^21, the low bits above 3 * 2^22.  The value is h 2^22 + l; the magic
+// numbers' own bits stay in h and l until sums are formed.  NaN and below 0 count as 0,
+// above 1 as 1.
+struct Fixed {
+  uint32_t h, l;
+};
+constexpr float kMagicH = 8388608.f, kMagicL = 12582912.f;
+constexpr uint32_t kBitsH = 0x4b000000u, kBitsL = 0x4b400000u;
+
+__device__ __forceinline__ Fixed fixed(float x) {
+  const float s = __saturatef(x);
+  const float h = fmaf(s, 4194304.f, kMagicH);
+  const float rest = fmaf(kMagicH - h, 2.384185791015625e-07f, s);     // 2^-22
+  return {__float_as_uint(h), __float_as_uint(fmaf(rest, 17592186044416.f, kMagicL))};
 }
 
 // 16 bytes of a row (kVec: it starts on a 16-byte boundary), or one value.
 template <typename T, bool kVec>
 struct Loaded {
   static constexpr int kCount = kVec ? 16 / static_cast<int>(sizeof(T)) : 1;
-  union {
-    uint4 raw;
-    T t[kCount];
-  };
+  uint32_t words[kVec ? 4 : 1];
 
-  __device__ __forceinline__ Loaded() {}
-  // elements at .. at + kCount - 1 of row; those from end on are 0
-  __device__ __forceinline__ void load(const T* row, int at, int end) {
-    if (kVec && at + kCount <= end) {
-      raw = *reinterpret_cast<const uint4*>(row + at);
+  // elements at .. at + kCount - 1 of row
+  __device__ __forceinline__ void load(const T* row, int at) {
+    if constexpr (kVec) {
+      const uint4 u = *reinterpret_cast<const uint4*>(row + at);
+      words[0] = u.x;
+      words[1] = u.y;
+      words[2] = u.z;
+      words[3] = u.w;
     } else {
-#pragma unroll
-      for (int i = 0; i < kCount; ++i) t[i] = at + i < end ? row[at + i] : T(0.f);
+      words[0] = bits_at(row + at);
     }
   }
-  __device__ __forceinline__ float operator[](int i) const { return as_float(t[i]); }
+  // the same; those from end on are 0
+  __device__ __forceinline__ void load(const T* row, int at, int end) {
+    if constexpr (kVec) {
+      if (at + kCount <= end) {
+        load(row, at);
+      } else {
+        constexpr int kEach = 4 / static_cast<int>(sizeof(T));       // values a word
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+          words[k] = 0;
+#pragma unroll
+          for (int i = 0; i < kEach; ++i)
+            if (at + k * kEach + i < end) words[k] |= bits_at(row + at + k * kEach + i) << (16 * i);
+        }
+      }
+    } else {
+      words[0] = at < end ? bits_at(row + at) : 0u;
+    }
+  }
+  __device__ __forceinline__ float operator[](int i) const { return value_in<T>(words, i); }
 };
 
 // What the token is drawn from: p less `less` (a row of q, or one token's whole weight).
@@ -73,20 +126,32 @@ struct Weights {
   const T* q;                                  // or nullptr
   int token;                                   // weighs nothing; -1: none
 
-  template <bool kVec>
-  __device__ __forceinline__ unsigned long long weigh(const Loaded<T, kVec>& a,
-                                                      const Loaded<T, kVec>& b, int at, int i,
-                                                      bool& bad) const {
-    bad = bad || !(a[i] >= 0.f);
-    unsigned long long w = fixed(a[i]);
-    if (q != nullptr) {
-      bad = bad || !(b[i] >= 0.f);
-      const unsigned long long less = fixed(b[i]);
-      w = w > less ? w - less : 0ull;
+  // Adds the weight of value i of a (and b) to h 2^22 + l (up to 512 weights: 32 bits each).
+  template <bool kVec, bool kBoth>
+  __device__ __forceinline__ void weigh(const Loaded<T, kVec>& a, const Loaded<T, kVec>& b, int at,
+                                        int i, uint32_t& h, int32_t& l, bool& bad) const {
+    const float x = a[i];
+    bad = bad || !(x >= 0.f);
+    const Fixed f = fixed(x);
+    if (kBoth) {
+      const float y = b[i];
+      bad = bad || !(y >= 0.f);
+      const Fixed less = fixed(y);
+      // rounding keeps the order: above 0 only where x > y
+      if (__saturatef(x) > __saturatef(y)) {
+        h += f.h - less.h;
+        l += static_cast<int32_t>(f.l - less.l);
+      }
+    } else if (at + i != token) {
+      h += f.h - kBitsH;
+      l += static_cast<int32_t>(f.l - kBitsL);
     }
-    return at + i == token ? 0ull : w;
   }
 };
+
+__device__ __forceinline__ unsigned long long joined(uint32_t h, int32_t l) {
+  return (static_cast<unsigned long long>(h) << 22) + static_cast<long long>(l);
+}
 
 __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
 #pragma unroll
@@ -94,98 +159,242 @@ __device__ __forceinline__ unsigned long long warp_sum(unsigned long long v) {
   return v;
 }
 
-// This warp's sum of the weights of [begin, end).
-template <typename T, bool kVec>
+// The parts of two probabilities of [0, 1] at once (fixed, in packed instructions).
+__device__ __forceinline__ void fixed2(float x0, float x1, uint32_t (&h)[2], uint32_t (&l)[2]) {
+  const uint64_t x = pack2(x0, x1);
+  const uint64_t hi = fma2(x, pack2(4194304.f, 4194304.f), pack2(kMagicH, kMagicH));
+  // x - (hi - 2^23) 2^-22, each step exact
+  const uint64_t whole = add2(hi, pack2(-kMagicH, -kMagicH));
+  const uint64_t rest = fma2(whole, pack2(-2.384185791015625e-07f, -2.384185791015625e-07f), x);
+  const uint64_t lo = fma2(rest, pack2(17592186044416.f, 17592186044416.f),
+                           pack2(kMagicL, kMagicL));
+  float f0, f1;
+  unpack2(hi, f0, f1);
+  h[0] = __float_as_uint(f0);
+  h[1] = __float_as_uint(f1);
+  unpack2(lo, f0, f1);
+  l[0] = __float_as_uint(f0);
+  l[1] = __float_as_uint(f1);
+}
+
+// Largest value by its bits, which order as whole numbers; negative ones and NaN come last.
+template <typename T>
+__device__ __forceinline__ uint32_t largest(uint32_t m, uint32_t word) {
+  if constexpr (sizeof(T) == 4) return max(m, word);
+  else return __vmaxu2(m, word);
+}
+// whether it (of both halves, for 16-bit types) is at most 1
+template <typename T>
+__device__ __forceinline__ bool at_most_one(uint32_t m) {
+  constexpr uint32_t kOne = sizeof(T) == 4 ? 0x3f800000u
+                            : std::is_same<T, __nv_bfloat16>::value ? 0x3f80u
+                                                                    : 0x3c00u;
+  if constexpr (sizeof(T) == 4) return m <= kOne;
+  else return (m & 0xffffu) <= kOne && (m >> 16) <= kOne;
+}
+
+// This warp's sum of the weights of [begin, end), run by run: sums[g] holds the g-th run of
+// `run` values, a multiple of what the warp takes in one step.  A lane's values of a step
+// that all lie in [0, 1], none of them the token without weight, go in packed
+// instructions; others one by one.
+template <typename T, bool kVec, bool kBoth>
 __device__ __forceinline__ unsigned long long sum_part(const Weights<T>& w, int begin, int end,
+                                                       int run, unsigned long long* sums,
                                                        bool& bad) {
   using Vec = Loaded<T, kVec>;
   constexpr int kStep = 32 * Vec::kCount;
+  constexpr int kWords = sizeof(Vec) / 4;
   const int lane = threadIdx.x & 31;
-  unsigned long long sum = 0;
-  for (int at = begin + lane * Vec::kCount; at < end; at += kDepth * kStep) {
-    Vec a[kDepth], b[kDepth];
+  unsigned long long total = 0;
+  for (int from = begin, g = 0; from < end; from += run, ++g) {
+    const int to = min(end, from + run);
+    const bool holds_token = !kBoth && w.token >= from && w.token < to;
+    unsigned long long sum = 0;
+    for (int at = from + lane * Vec::kCount; at < to; at += kDepth * kStep) {
+      Vec a[kDepth], b[kDepth];
+      if (at + (kDepth - 1) * kStep + Vec::kCount <= to) {
 #pragma unroll
-    for (int d = 0; d < kDepth; ++d) a[d].load(w.p, at + d * kStep, end);
-    if (w.q != nullptr) {
+        for (int d = 0; d < kDepth; ++d) a[d].load(w.p, at + d * kStep);
+        if (kBoth) {
 #pragma unroll
-      for (int d = 0; d < kDepth; ++d) b[d].load(w.q, at + d * kStep, end);
+          for (int d = 0; d < kDepth; ++d) b[d].load(w.q, at + d * kStep);
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d) a[d].load(w.p, at + d * kStep, to);
+        if (kBoth) {
+#pragma unroll
+          for (int d = 0; d < kDepth; ++d) b[d].load(w.q, at + d * kStep, to);
+        }
+      }
+      uint32_t most = 0;
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+        for (int k = 0; k < kWords; ++k) {
+          most = largest<T>(most, a[d].words[k]);
+          if (kBoth) most = largest<T>(most, b[d].words[k]);
+        }
+      uint32_t h = 0;
+      int32_t l = 0;
+      if (at_most_one<T>(most) && !holds_token) {
+        constexpr int kValues = kDepth * Vec::kCount;
+#pragma unroll
+        for (int e = 0; e < kValues; e += 2) {
+          const float x0 = a[e / Vec::kCount][e % Vec::kCount];
+          const float x1 = a[(e + 1) / Vec::kCount][(e + 1) % Vec::kCount];
+          uint32_t ph[2], pl[2];
+          fixed2(x0, x1, ph, pl);
+          if (kBoth) {
+            const float y0 = b[e / Vec::kCount][e % Vec::kCount];
+            const float y1 = b[(e + 1) / Vec::kCount][(e + 1) % Vec::kCount];
+            uint32_t qh[2], ql[2];
+            fixed2(y0, y1, qh, ql);
+            if (x0 > y0) {
+              h += ph[0] - qh[0];
+              l += static_cast<int32_t>(pl[0] - ql[0]);
+            }
+            if (x1 > y1) {
+              h += ph[1] - qh[1];
+              l += static_cast<int32_t>(pl[1] - ql[1]);
+            }
+          } else {                             // the magic numbers' bits come out below
+            h += ph[0] + ph[1];
+            l += static_cast<int32_t>(pl[0] + pl[1]);
+          }
+        }
+        if (!kBoth) {
+          h -= kValues * kBitsH;
+          l -= static_cast<int32_t>(kValues * kBitsL);
+        }
+      } else {
+#pragma unroll
+        for (int d = 0; d < kDepth; ++d)
+#pragma unroll
+          for (int i = 0; i < Vec::kCount; ++i)
+            w.template weigh<kVec, kBoth>(a[d], b[d], at + d * kStep, i, h, l, bad);
+      }
+      sum += joined(h, l);
     }
-#pragma unroll
-    for (int d = 0; d < kDepth; ++d)
-#pragma unroll
-      for (int i = 0; i < Vec::kCount; ++i) sum += w.weigh(a[d], b[d], at + d * kStep, i, bad);
+    sum = warp_sum(sum);
+    if (lane == 0) sums[g] = sum;
+    total += sum;
   }
-  return warp_sum(sum);
+  __syncwarp();
+  return total;
+}
+
+// Inclusive sums over the lanes.
+__device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) {
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const unsigned long long n = __shfl_up_sync(0xffffffffu, v, o);
+    if ((threadIdx.x & 31) >= o) v += n;
+  }
+  return v;
 }
 
 // The first element of [begin, end) at which `before` and the weights so far pass t
-// (one warp, all lanes; the caller knows that there is one).
-template <typename T, bool kVec>
-__device__ __forceinline__ int find_in_part(const Weights<T>& w, int begin, int end,
+// (one warp, all lanes; the caller knows that there is one).  sums, run: sum_part's.
+template <typename T, bool kVec, bool kBoth>
+__device__ __noinline__ int find_in_part(const Weights<T>& w, int begin, int end, int run,
+                                            const unsigned long long* sums,
                                             unsigned long long before, unsigned long long t) {
   using Vec = Loaded<T, kVec>;
+  constexpr int kStep = 32 * Vec::kCount;
   const int lane = threadIdx.x & 31;
   bool bad = false;
-  for (int from = begin; from < end; from += 32 * Vec::kCount) {
-    const int at = from + lane * Vec::kCount;
-    Vec a, b;
-    a.load(w.p, at, end);
-    if (w.q != nullptr) b.load(w.q, at, end);
+  while (end - begin > run && before + *sums <= t) {     // the run that holds it
+    before += *sums++;
+    begin += run;
+  }
+  end = min(end, begin + run);
+  for (int from = begin; from < end; from += kDepth * kStep) {
+    // the step that holds it, then the vector again
+    unsigned long long sums_of[kDepth];
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      const int at = from + lane * Vec::kCount + d * kStep;
+      Vec a, b;
+      a.load(w.p, at, end);
+      if (kBoth) b.load(w.q, at, end);
+      uint32_t h = 0;
+      int32_t l = 0;
+#pragma unroll
+      for (int i = 0; i < Vec::kCount; ++i) w.template weigh<kVec, kBoth>(a, b, at, i, h, l, bad);
+      sums_of[d] = joined(h, l);
+    }
+    int step = -1;
     unsigned long long mine = 0;
 #pragma unroll
-    for (int i = 0; i < Vec::kCount; ++i) mine += w.weigh(a, b, at, i, bad);
-    unsigned long long upto = mine;            // inclusive scan over the lanes
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const unsigned long long n = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += n;
-    }
-    const unsigned passed = __ballot_sync(0xffffffffu, before + upto > t);
-    if (passed != 0) {
-      int found = 0;
-      if (lane == __ffs(passed) - 1) {
-        unsigned long long run = before + upto - mine;
-        bool done = false;
-#pragma unroll
-        for (int i = 0; i < Vec::kCount; ++i) {
-          run += w.weigh(a, b, at, i, bad);
-          if (!done && run > t) {
-            found = at + i;
-            done = true;
-          }
+    for (int d = 0; d < kDepth; ++d) {
+      const unsigned long long sum = warp_sum(sums_of[d]);
+      if (step < 0) {
+        if (before + sum > t) {
+          step = d;
+          mine = sums_of[d];
+        } else {
+          before += sum;
         }
       }
-      return __shfl_sync(0xffffffffu, found, __ffs(passed) - 1);
     }
-    before += __shfl_sync(0xffffffffu, upto, 31);
+    if (step < 0) continue;
+    const unsigned long long upto = warp_scan(mine);
+    const int owner = __ffs(__ballot_sync(0xffffffffu, before + upto > t)) - 1;
+    const int at = from + lane * Vec::kCount + step * kStep;
+    int found = at;
+    if (lane == owner) {
+      Vec a, b;
+      a.load(w.p, at, end);
+      if (kBoth) b.load(w.q, at, end);
+      uint32_t h = 0;
+      int32_t l = 0;
+#pragma unroll
+      for (int i = 0; i < Vec::kCount; ++i) {
+        if (before + upto - mine + joined(h, l) <= t) found = at + i;   // not passed before i
+        w.template weigh<kVec, kBoth>(a, b, at, i, h, l, bad);
+      }
+    }
+    return __shfl_sync(0xffffffffu, found, owner);
   }
   return -1;
 }
 
-// How many drafts are kept (one warp, all lanes).
+// How many drafts are kept (one warp, all lanes).  The drafts are asked for beside their
+// number, so that two loads follow each other and not three.
 template <typename T>
-__device__ __forceinline__ int kept_drafts(const VerifyArgs& a, int b, int n, bool& bad_token) {
+__device__ __forceinline__ int kept_drafts(const VerifyArgs& a, int b, int& n, int& token,
+                                           bool& bad_token) {
   const int lane = threadIdx.x & 31;
   const T* p = static_cast<const T*>(a.target) + b * a.target_stride_b;
   const T* q = static_cast<const T*>(a.draft) + b * a.draft_stride_b;
+  const int32_t* drafts = a.draft_tokens + static_cast<int64_t>(b) * a.max_drafts;
+  const float* uniforms = a.uniforms + static_cast<int64_t>(b) * (a.max_drafts + 1);
+  const int32_t* lens = a.draft_lens != nullptr ? a.draft_lens + b : nullptr;
+  n = a.max_drafts;
   for (int i0 = 0; i0 < n; i0 += 32) {
     const int i = i0 + lane;
-    bool keep = false, known = true;
-    if (i < n) {
-      const int x = a.draft_tokens[static_cast<int64_t>(b) * a.max_drafts + i];
-      const float u = a.uniforms[static_cast<int64_t>(b) * (a.max_drafts + 1) + i];
-      known = x >= 0 && x < a.vocab;
-      if (known) {
-        const float px = as_float(p[i * a.target_stride_t + x]);
-        const float qx = a.draft != nullptr ? as_float(q[i * a.draft_stride_t + x]) : 1.f;
-        keep = static_cast<double>(u) * qx < px;
-      }
+    int x = -1;
+    float u = 0.f;
+    if (i < a.max_drafts) {
+      x = drafts[i];
+      u = uniforms[i];
+    }
+    if (i0 == 0 && lens != nullptr) n = max(0, min(n, *lens));
+    bool keep = false;
+    const bool known = x >= 0 && x < a.vocab;
+    if (i < n && known) {
+      const float px = value_at(p + i * a.target_stride_t + x);
+      const float qx = a.draft != nullptr ? value_at(q + i * a.draft_stride_t + x) : 1.f;
+      keep = static_cast<double>(u) * qx < px;
     }
     const unsigned refused = __ballot_sync(0xffffffffu, !keep);
     if (refused != 0) {
       const int first = __ffs(refused) - 1;
-      bad_token = __shfl_sync(0xffffffffu, static_cast<int>(!known), first) != 0;
-      return min(n, i0 + first);
+      if (i0 + first >= n) return n;           // the lanes past the last draft
+      token = __shfl_sync(0xffffffffu, x, first);
+      bad_token = token < 0 || token >= a.vocab;
+      return i0 + first;
     }
   }
   return n;
@@ -217,8 +426,9 @@ __device__ __forceinline__ void push(unsigned long long* to, uint32_t rank, unsi
 template <typename T, bool kVec>
 __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(const VerifyArgs a) {
   __shared__ unsigned long long warp_sums[kWarps];
+  __shared__ unsigned long long run_sums[kWarps][kGroups];
   __shared__ unsigned long long cta_sums[2][kMaxCluster];   // [round][rank]
-  __shared__ int s_kept, s_bad_token;
+  __shared__ int s_kept, s_drafts, s_token, s_bad_token;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int rank = static_cast<int>(cluster_rank()), ranks = static_cast<int>(cluster_size());
   const int b = blockIdx.y;
@@ -226,19 +436,23 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
 
   pdl_launch_dependents();
   pdl_wait();
-  int n = a.max_drafts;
-  if (a.draft_lens != nullptr) n = max(0, min(n, a.draft_lens[b]));
+  // what the end needs, on its way from the start
+  float u = a.uniforms[static_cast<int64_t>(b) * (a.max_drafts + 1) + a.max_drafts];
+  const int seq_len = a.kept_lens != nullptr && rank == 0 ? a.seq_lens[b] : 0;
   if (warp == 0) {
     bool bad_token = false;
-    const int j = kept_drafts<T>(a, b, n, bad_token);
+    int n, token = -1;
+    const int j = kept_drafts<T>(a, b, n, token, bad_token);
     if (lane == 0) {
       s_kept = j;
+      s_drafts = n;
+      s_token = token;
       s_bad_token = bad_token;
     }
   }
   cluster_wait();
   __syncthreads();
-  const int j = s_kept;
+  const int j = s_kept, n = s_drafts;
   const bool refused = j < n;
   const int64_t draft_row = static_cast<int64_t>(b) * a.max_drafts;
 
@@ -247,7 +461,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
   w.q = refused && a.draft != nullptr
             ? static_cast<const T*>(a.draft) + b * a.draft_stride_b + j * a.draft_stride_t
             : nullptr;
-  w.token = refused && a.draft == nullptr ? a.draft_tokens[draft_row + j] : -1;
+  w.token = refused && a.draft == nullptr ? s_token : -1;
 
   // slices of whole 16-byte pieces
   constexpr int kPiece = 16 / static_cast<int>(sizeof(T));
@@ -258,10 +472,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
                                          static_cast<long long>(part) * per_warp));
   const int end = min(a.vocab, begin + per_warp);
 
+  // runs of whole steps, at most kGroups of them
+  constexpr int kStep = kDepth * 32 * Loaded<T, kVec>::kCount;
+  const int run = (per_warp + kGroups * kStep - 1) / (kGroups * kStep) * kStep;
+
   unsigned long long total = 0, before = 0;
   bool bad = false;
   for (int round = 0; round < 2; ++round) {
-    const unsigned long long mine = sum_part<T, kVec>(w, begin, end, bad);
+    const unsigned long long mine =
+        w.q != nullptr ? sum_part<T, kVec, true>(w, begin, end, run, run_sums[warp], bad)
+                       : sum_part<T, kVec, false>(w, begin, end, run, run_sums[warp], bad);
     if (lane == 0) warp_sums[warp] = mine;
     __syncthreads();
     if (warp == 0) {
@@ -286,14 +506,16 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
 
   int32_t* tokens = a.tokens + static_cast<int64_t>(b) * (a.max_drafts + 1);
   if (total != 0) {
-    float u = a.uniforms[static_cast<int64_t>(b) * (a.max_drafts + 1) + a.max_drafts];
     u = fminf(fmaxf(u, 0.f), 1.f);             // NaN: 0
     const double at = static_cast<double>(u) * static_cast<double>(total);
     const unsigned long long t =
         at >= static_cast<double>(total) ? total - 1 : min(total - 1, static_cast<unsigned long long>(at));
     for (int k = 0; k < warp; ++k) before += warp_sums[k];
     if (t >= before && t - before < warp_sums[warp]) {
-      const int v = find_in_part<T, kVec>(w, begin, end, before, t);
+      const int v =
+          w.q != nullptr
+              ? find_in_part<T, kVec, true>(w, begin, end, run, run_sums[warp], before, t)
+              : find_in_part<T, kVec, false>(w, begin, end, run, run_sums[warp], before, t);
       if (lane == 0) tokens[j] = v;
     }
   } else if (rank == 0 && threadIdx.x == 0) {
@@ -305,7 +527,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
       if (i != j) tokens[i] = i < j ? a.draft_tokens[draft_row + i] : -1;
     if (threadIdx.x == 0) {
       a.num_accepted[b] = j;
-      if (a.kept_lens != nullptr) a.kept_lens[b] = a.seq_lens[b] - (n - j);
+      if (a.kept_lens != nullptr) a.kept_lens[b] = seq_len - (n - j);
       if (s_bad_token) report(a.status_flags, kFlagBadToken);
     }
   }
