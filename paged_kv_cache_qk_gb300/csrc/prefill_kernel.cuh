@@ -115,7 +115,9 @@ constexpr int kGroupsPerTile = kN / kScaleGroup;
 constexpr float kLn2 = 0.6931471805599453f;
 
 // Score rules a kernel is built for: intervals of keys alone, and what scores go through.
-constexpr int kRuleIntervals = 1, kRuleCap = 2, kRuleBias = 4;
+// kRuleBounded: a cap without a bias, small enough for one reference (bounded_half_tile).
+constexpr int kRuleIntervals = 1, kRuleCap = 2, kRuleBias = 4, kRuleBounded = 8;
+constexpr float kBoundedCap = 80.f;            // log2 units: caps up to 55.4
 
 struct Bars {
   uint64_t full_k[kStages], full_v[kStages];     // TMA landed
@@ -1006,32 +1008,81 @@ __device__ __forceinline__ float half_tile(uint32_t scol, uint32_t pcol, int kba
   return psum;
 }
 
-// 32 raw scores v to cap * tanh(k v), k = scale log2(e) / cap: two at a time by the
-// polynomial, and again by the exponential where one of the warp's lies beyond it.
-__device__ __forceinline__ void cap_chunk(float (&v)[32], float k, float cap) {
-  // the largest |v| decides; a NaN that is masked later does not count
-  float big = 0.f;
+// add + cap * tanh(k v) of 32 raw scores, k = scale log2(e) / cap: two at a time by the
+// polynomial that the largest of the warp's scores allows, or one by one.
+template <int kDegree>
+__device__ __forceinline__ void cap_pairs(float (&v)[32], float k, float cap, float add) {
+  const uint64_t k2 = pack2(k, k), add2_ = pack2(add, add);
+  uint64_t c[kDegree + 1];                     // the cap is in the coefficients
 #pragma unroll
-  for (int e = 0; e < 32; e += 2) big = max3(big, fabsf(v[e]), fabsf(v[e + 1]));
-  big *= k;
-  if (__any_sync(0xffffffffu, big * big > kTanhSquare)) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float x = v[e] * k, u = x * x;
-      v[e] = cap * (u <= kTanhSquare ? tanh_near(x, u) : tanh_far(x));
-    }
-    return;
-  }
-  const uint64_t k2 = pack2(k, k), c2 = pack2(cap, cap);
+  for (int i = 0; i <= kDegree; ++i)
+    c[i] = pack2(cap * tanh_q<kDegree>(i), cap * tanh_q<kDegree>(i));
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     const uint64_t x = mul2(pack2(v[e], v[e + 1]), k2);
     const uint64_t u = mul2(x, x);
-    uint64_t q = pack2(tanh_q(5), tanh_q(5));
+    uint64_t q = c[kDegree];
 #pragma unroll
-    for (int i = 4; i >= 0; --i) q = fma2(q, u, pack2(tanh_q(i), tanh_q(i)));
-    unpack2(mul2(mul2(x, c2), q), v[e], v[e + 1]);
+    for (int i = kDegree - 1; i >= 0; --i) q = fma2(q, u, c[i]);
+    unpack2(fma2(x, q, add2_), v[e], v[e + 1]);
   }
+}
+__device__ __forceinline__ void cap_chunk(float (&v)[32], float k, float cap, float add) {
+  // the largest |v| decides; a NaN that is masked later does not count
+  float b4[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+  for (int e = 0; e < 32; e += 2)
+    b4[(e >> 1) & 3] = max3(b4[(e >> 1) & 3], fabsf(v[e]), fabsf(v[e + 1]));
+  const float big = max3(b4[0], b4[1], fmaxf(b4[2], b4[3])) * k;
+  if (!__any_sync(0xffffffffu, big * big > kTanhSmall)) {
+    cap_pairs<3>(v, k, cap, add);
+  } else if (!__any_sync(0xffffffffu, big * big > kTanhSquare)) {
+    cap_pairs<5>(v, k, cap, add);
+  } else {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) {
+      const float x = v[e] * k, u = x * x;
+      v[e] = fmaf(cap, u <= kTanhSquare ? tanh_near(x, u) : tanh_far(x), add);
+    }
+  }
+}
+
+// half_tile under a cap without a bias.  Capped scores lie in [-cap, cap], so one
+// reference serves every row, ref = cap / 4 (log2 units): P = 2^(s - ref) stays between
+// 2^-100 and 2^60, where bf16 and fp32 keep all their bits, and 2^20 of them with values up
+// to 2^46 fit the accumulators.  So no maximum is taken, O is never rescaled, and the row's
+// halves need not meet before the end.
+template <bool kMasked>
+__device__ __forceinline__ float bounded_half_tile(uint32_t scol, uint32_t pcol, int kbase,
+                                                   int nlo, int nvis, float k, float cap,
+                                                   float ref) {
+  uint64_t acc[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) acc[j] = pack2(0.f, 0.f);
+#pragma unroll
+  for (int c = 0; c < 2; ++c) {
+    float v[32];
+    tc5::tmem_ld32(scol + c * 32, v);
+    tc5::wait_ld();
+    cap_chunk(v, k, cap, -ref);
+    if (kMasked) {
+      const int k0 = kbase + c * 32;
+#pragma unroll
+      for (int e = 0; e < 32; ++e)
+        v[e] = (k0 + e < nvis && k0 + e >= nlo) ? v[e] : -INFINITY;
+    }
+    uint32_t pk[16];
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const float p0 = ex2_approx(v[2 * q]), p1 = ex2_approx(v[2 * q + 1]);
+      acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
+      pk[q] = pack_bf16x2(p0, p1);
+    }
+    tc5::tmem_st16(pcol + c * 16, pk);
+  }
+  float t0, t1;
+  unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), t0, t1);
+  return t0 + t1;
 }
 
 // half_tile over a bf16 cache under score rules: scores go through the cap and the
@@ -1053,7 +1104,7 @@ __device__ __forceinline__ float scored_half_tile(uint32_t scol, uint32_t pcol, 
     tc5::wait_ld();
     const int k0 = kbase + c * 32;
     if (kRules & kRuleCap) {
-      cap_chunk(v, sl2 * rules.inv_cap, rules.cap);
+      cap_chunk(v, sl2 * rules.inv_cap, rules.cap, 0.f);
     } else if (kRules & kRuleBias) {
       const uint64_t scale2 = pack2(sl2, sl2);
 #pragma unroll
@@ -1292,7 +1343,7 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
     } else {
       lim = w.k0;
     }
-    if ((kRules & kRuleBias) && inside)
+    if ((kRules & kRuleBias) && inside && a.rules.slopes != nullptr)
       slope = a.rules.slopes[w.g * a.group + rg - t * a.group] * 1.4426950408889634f;
   }
   const uint32_t lanes = tmem + (static_cast<uint32_t>(wq * 32) << 16);
@@ -1323,7 +1374,8 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
   const int tail_tile = (kFormat == 0 && x == 0 && k0 + n * kN > w.key_end) ? n - 1 : -1;
   const int head_tile = (kRules != 0 && x == 0 && k0 < w.key_begin) ? 0 : -1;
 
-  float m_ref = -INFINITY;                     // reference max (log2 units), integer once set
+  // reference max (log2 units), integer once set
+  float m_ref = kRules & kRuleBounded ? 0.25f * a.rules.cap : -INFINITY;
   float l = 0.f;                               // this half's sum of P
   // the first tiles; K(1) by tile B's warps, whose scores come after tile A's
   if (kFormat != 0 && n > 0)
@@ -1353,7 +1405,12 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
     const float m_start = m_ref;
     auto publish = [&](float m) { swap_publish(m, slots, xbar, uses, half, r); };
     float psum;
-    if constexpr (kRules != 0)
+    if constexpr ((kRules & kRuleBounded) != 0)
+      psum = whole ? bounded_half_tile<false>(s_cols, s_cols, half * (kN / 2), 0, nvis,
+                                              sl2 * a.rules.inv_cap, a.rules.cap, m_ref)
+                   : bounded_half_tile<true>(s_cols, s_cols, half * (kN / 2), lo - kb, nvis,
+                                             sl2 * a.rules.inv_cap, a.rules.cap, m_ref);
+    else if constexpr (kRules != 0)
       psum = whole ? scored_half_tile<kRules, false>(s_cols, s_cols, half * (kN / 2), 0, nvis, sl2,
                                                      a.rules, slope, kb - pos, m_ref, publish)
                    : scored_half_tile<kRules, true>(s_cols, s_cols, half * (kN / 2), lo - kb, nvis,
@@ -1364,9 +1421,10 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
                    : half_tile<kFormat, true>(s_cols, s_cols, half * (kN / 2), nvis, sl2,
                                               scales, m_ref, publish);
     // one reference per row: the higher of the two halves'
-    const float m_other = swap_read(slots, xbar, uses, half, r, ok);
+    const float m_other =
+        kRules & kRuleBounded ? m_ref : swap_read(slots, xbar, uses, half, r, ok);
     if (!ok) break;
-    if (__all_sync(0xffffffffu, m_ref == m_start && m_other == m_start)) {
+    if ((kRules & kRuleBounded) || __all_sync(0xffffffffu, m_ref == m_start && m_other == m_start)) {
       l += psum;                               // neither half moved (the usual tile)
     } else {
       const float m_row = fmaxf(m_ref, m_other);

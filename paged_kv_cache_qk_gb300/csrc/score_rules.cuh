@@ -10,12 +10,12 @@
 // interval of keys.  Scores are kept in units of log2(e), so that the softmax's 2^x takes
 // them as they are.
 //
-// tanh without cancellation: below |x| = 0.6 it is x Q(x^2), Q of degree 5 fitted to
-// tanh(x) / x at Chebyshev nodes (largest relative error 2.6e-9, 4.7e-8 evaluated in
-// fp32), which takes no special-function unit; beyond, 1 - 2 / (1 + e^2x), whose absolute
-// error of ~1.2e-7 is relative there.  The units' exponentials and reciprocals are what
-// the softmax itself is short of, so a warp computes the second form only where one of
-// its scores is that large.
+// tanh without cancellation: x Q(x^2), Q fitted to tanh(x) / x at Chebyshev nodes: of
+// degree 5 up to |x| = 0.75 (largest relative error 3.0e-8, 1.0e-7 evaluated in fp32), of
+// degree 3 up to 0.35 (3.5e-8, 9.1e-8), which takes no special-function unit; beyond,
+// 1 - 2 / (1 + e^2x), whose absolute error of ~1.2e-7 is relative there.  The units'
+// exponentials and reciprocals are what the softmax itself is short of, so a warp computes
+// the last form only where one of its scores is that large.
 #pragma once
 
 #include "device_common.cuh"
@@ -23,14 +23,20 @@
 
 namespace pkvqk {
 
-constexpr float kTanhSquare = 0.36f;           // x^2 up to which the polynomial serves
+constexpr float kTanhSquare = 0.5625f;         // x^2 up to which the polynomials serve:
+constexpr float kTanhSmall = 0.1225f;          // of degree 3, above it of degree 5
+
+// Coefficient i of the polynomial of the given degree.
+template <int kDegree>
 __device__ __forceinline__ constexpr float tanh_q(int i) {
+  if (kDegree == 3)
+    return i == 0 ? 0.99999994f : i == 1 ? -0.33332425f : i == 2 ? 0.13295884f : -0.04896282f;
   return i == 0   ? 1.0f
-         : i == 1 ? -0.33333284f
-         : i == 2 ? 0.13331705f
-         : i == 3 ? -0.053769923f
-         : i == 4 ? 0.020757476f
-                  : -0.0058564278f;
+         : i == 1 ? -0.33332968f
+         : i == 2 ? 0.13325515f
+         : i == 3 ? -0.05334982f
+         : i == 4 ? 0.019593786f
+                  : -0.004723952f;
 }
 
 // 1 - 2 / (1 + e^(2 x)), e^(2 x) = 2^(2 log2(e) x)
@@ -42,9 +48,9 @@ __device__ __forceinline__ float tanh_far(float x) {
 }
 
 __device__ __forceinline__ float tanh_near(float x, float u) {
-  float q = tanh_q(5);
+  float q = tanh_q<5>(5);
 #pragma unroll
-  for (int i = 4; i >= 0; --i) q = fmaf(q, u, tanh_q(i));
+  for (int i = 4; i >= 0; --i) q = fmaf(q, u, tanh_q<5>(i));
   return q * x;
 }
 
