@@ -1047,6 +1047,28 @@ __device__ __forceinline__ void cap_chunk(float (&v)[32], float k, float cap, fl
   }
 }
 
+// Scores of the keys outside [lo, hi) to -inf.  Most masked tiles are cut at one end: the
+// other's comparisons are skipped where none of the warp's rows needs them.
+__device__ __forceinline__ void hide_keys(float (&v)[32], int lo, int hi) {
+  if (__any_sync(0xffffffffu, hi < 32)) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = e < hi ? v[e] : -INFINITY;
+  }
+  if (__any_sync(0xffffffffu, lo > 0)) {
+#pragma unroll
+    for (int e = 0; e < 32; ++e) v[e] = e >= lo ? v[e] : -INFINITY;
+  }
+}
+
+// P of a half tile of which none of the warp's rows sees a key.
+__device__ __forceinline__ void zero_half_tile(uint32_t pcol) {
+  uint32_t z[16];
+#pragma unroll
+  for (int j = 0; j < 16; ++j) z[j] = 0u;
+  tc5::tmem_st16(pcol, z);
+  tc5::tmem_st16(pcol + 16, z);
+}
+
 // half_tile under a cap without a bias.  Capped scores lie in [-cap, cap], so one
 // reference serves every row, ref = cap / 4 (log2 units): P = 2^(s - ref) stays between
 // 2^-100 and 2^60, where bf16 and fp32 keep all their bits, and 2^20 of them with values up
@@ -1065,12 +1087,7 @@ __device__ __forceinline__ float bounded_half_tile(uint32_t scol, uint32_t pcol,
     tc5::tmem_ld32(scol + c * 32, v);
     tc5::wait_ld();
     cap_chunk(v, k, cap, -ref);
-    if (kMasked) {
-      const int k0 = kbase + c * 32;
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        v[e] = (k0 + e < nvis && k0 + e >= nlo) ? v[e] : -INFINITY;
-    }
+    if (kMasked) hide_keys(v, nlo - kbase - c * 32, nvis - kbase - c * 32);
     uint32_t pk[16];
 #pragma unroll
     for (int q = 0; q < 16; ++q) {
@@ -1127,11 +1144,7 @@ __device__ __forceinline__ float scored_half_tile(uint32_t scol, uint32_t pcol, 
         shift = slope * d0;
       }
     }
-    if (kMasked) {
-#pragma unroll
-      for (int e = 0; e < 32; ++e)
-        v[e] = (k0 + e < nvis && k0 + e >= nlo) ? v[e] : -INFINITY;
-    }
+    if (kMasked) hide_keys(v, nlo - k0, nvis - k0);
     float m4[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) m4[j] = -INFINITY;
@@ -1367,6 +1380,9 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
   for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
   // scored: the first key that all of the warp's rows see, and their least position's end
   const int lo_max = kRules != 0 ? __reduce_max_sync(0xffffffffu, lo) : 0;
+  const int lo_least =
+      kRules != 0 ? __reduce_min_sync(0xffffffffu, lim > w.k0 ? lo : INT_MAX) : 0;
+  const int lim_most = kRules != 0 ? __reduce_max_sync(0xffffffffu, lim) : 0;
   if (kRules & kRuleBias)
     lim_min = min(lim_min, __reduce_min_sync(0xffffffffu, valid ? pos + 1 : w.k0));
   const int n = w.ntiles;
@@ -1404,8 +1420,14 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
     const bool whole = lim_min >= kb + kN && (kRules == 0 || lo_max <= kb);
     const float m_start = m_ref;
     auto publish = [&](float m) { swap_publish(m, slots, xbar, uses, half, r); };
-    float psum;
-    if constexpr ((kRules & kRuleBounded) != 0)
+    float psum = 0.f;
+    // scored: nothing of this half tile is visible to the warp's rows
+    const int h0 = kb + half * (kN / 2);
+    const bool hidden = kRules != 0 && (lim_most <= h0 || lo_least >= h0 + kN / 2);
+    if (hidden) {
+      zero_half_tile(s_cols);
+      if (!(kRules & kRuleBounded)) publish(m_ref);
+    } else if constexpr ((kRules & kRuleBounded) != 0)
       psum = whole ? bounded_half_tile<false>(s_cols, s_cols, half * (kN / 2), 0, nvis,
                                               sl2 * a.rules.inv_cap, a.rules.cap, m_ref)
                    : bounded_half_tile<true>(s_cols, s_cols, half * (kN / 2), lo - kb, nvis,
