@@ -616,7 +616,15 @@ namespace {
 // theta^(-2i/D) in float64 and the float-float sin/cos knots: the inputs of
 // both the append kernel's angle phase and the table build.
 void rope_constants(float theta, double (&inv_freq)[64], float (&tab)[pkvqk::kSinCosKnots][4]) {
-  for (int i = 0; i < 64; ++i) inv_freq[i] = std::pow(static_cast<double>(theta), -2.0 * i / 128.0);
+  // 64 powers are microseconds of a call: the last theta's are kept (by its value)
+  thread_local float last_theta = 0.f;         // no call has it
+  thread_local double last_freq[64];
+  if (theta != last_theta) {
+    for (int i = 0; i < 64; ++i)
+      last_freq[i] = std::pow(static_cast<double>(theta), -2.0 * i / 128.0);
+    last_theta = theta;
+  }
+  std::memcpy(inv_freq, last_freq, sizeof(last_freq));
   static float s_tab[pkvqk::kSinCosKnots][4];
   static std::once_flag s_tab_once;
   std::call_once(s_tab_once, [] { pkvqk::build_sincos_table(s_tab); });

@@ -41,8 +41,9 @@
 // an image's tokens) frequency i turns by the position of its axis, two bits of a
 // 128-bit word.  A lane whose four frequencies share an axis reads that position's
 // table row as above; where frequencies of one lane lie on different axes
-// (interleaved axes) it reads its 16 numbers one by one, each from the row of its
-// own axis' position.
+// (interleaved axes) the CTA gathers the token's 256 numbers from their axes' rows into
+// shared memory once (each half-warp reading its lanes' 16 numbers one by one took 16
+// ragged prompts of 32 q and 4 kv heads 75 us and, with the launch below, this 53).
 #include "device_common.cuh"
 #include "kernels.h"
 #include "rope_math.cuh"
@@ -66,6 +67,12 @@ constexpr int kManyMinBlocks = 8;
 // rotation 34.0 us at 8 per SM, 32.2 at 9, 31.0 at 10, 33.8 at 11; with the
 // packed rotation 31.6 at 8, 31.1 at 9, 29.0 at 10 (measured on GB300).
 constexpr int kTableMinBlocks = 10;
+// More head vectors than those take at four a half-warp (24): CTAs of at most kWideThreads
+// threads, kWideMinBlocks per SM, at 64 registers, their half-warps with as many passes as
+// it takes.  8192 tokens from a table, 32 q and 4 kv heads: 37.2 us (42.5 at 4 per SM, 50.0
+// without the bound, at 106 registers); 64 and 8: 74.1 (158 with 288 threads unbounded).
+constexpr int kWideThreads = 192;
+constexpr int kWideMinBlocks = 5;
 
 // A lane's part of one head vector: elements [4l, 4l + 4) and their
 // rotate-half partners [64 + 4l, 64 + 4l + 4), as raw bf16 (x, and v for kv
@@ -99,6 +106,7 @@ __device__ __forceinline__ Trig table_trig(const NormRopeAppendArgs& a, const On
   tr.sl = __ldg(row + 3);
   return tr;
 }
+__device__ __forceinline__ bool lanes_mix_axes(const NormRopeAppendArgs&) { return false; }
 __device__ __forceinline__ __nv_bfloat16* q_row_out(const NormRopeAppendArgs& a, int t, int h) {
   return a.q + t * a.q_stride_t + static_cast<int64_t>(h) * a.q_stride_h;
 }
@@ -138,18 +146,10 @@ __device__ __forceinline__ bool in_table(const NormRopeAppendAxesArgs& a,
 }
 __device__ __forceinline__ Trig table_trig(const NormRopeAppendAxesArgs& a,
                                            const AxisPositions& pos, int l) {
-  const uint32_t bits = axis_bits(a, 4 * l);
-  if (a.lane_axes) return table_trig(a, OnePosition{on_axis(pos, bits & 3)}, l);
-  float4 c[4];
-  float* f = reinterpret_cast<float*>(c);
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    const float* row = reinterpret_cast<const float*>(
-        a.rope_table + (on_axis(pos, (bits >> (2 * j)) & 3) * (kHeadDim / 8) + l) * 4);
-#pragma unroll
-    for (int u = 0; u < 4; ++u) f[4 * u + j] = __ldg(row + 4 * u + j);
-  }
-  return {c[0], c[1], c[2], c[3]};
+  return table_trig(a, OnePosition{on_axis(pos, axis_bits(a, 4 * l) & 3)}, l);
+}
+__device__ __forceinline__ bool lanes_mix_axes(const NormRopeAppendAxesArgs& a) {
+  return !a.lane_axes;
 }
 __device__ __forceinline__ __nv_bfloat16* q_row_out(const NormRopeAppendAxesArgs& a, int t,
                                                     int h) {
@@ -245,6 +245,32 @@ __device__ __forceinline__ Trig angles_in_cta(const Args& a, const Position& pos
   return tr;
 }
 
+// The token's sin/cos from the table rows of its axes' positions, through shared memory.
+__device__ __forceinline__ Trig gathered_trig(const NormRopeAppendAxesArgs& a,
+                                              const AxisPositions& pos, int l, float* s_cos_hi,
+                                              float* s_cos_lo, float* s_sin_hi,
+                                              float* s_sin_lo) {
+  float* const part[4] = {s_cos_hi, s_cos_lo, s_sin_hi, s_sin_lo};
+  for (int e = threadIdx.x; e < 4 * (kHeadDim / 2); e += blockDim.x) {
+    const int u = e >> 6, i = e & 63;
+    const float* row = reinterpret_cast<const float*>(
+        a.rope_table + (position_at(a, pos, i) * (kHeadDim / 8) + i / 4) * 4);
+    float* to = u == 0 ? part[0] : u == 1 ? part[1] : u == 2 ? part[2] : part[3];
+    to[i] = __ldg(row + 4 * u + (i & 3));
+  }
+  __syncthreads();
+  Trig tr;
+  tr.ch = *reinterpret_cast<const float4*>(s_cos_hi + 4 * l);
+  tr.cl = *reinterpret_cast<const float4*>(s_cos_lo + 4 * l);
+  tr.sh = *reinterpret_cast<const float4*>(s_sin_hi + 4 * l);
+  tr.sl = *reinterpret_cast<const float4*>(s_sin_lo + 4 * l);
+  return tr;
+}
+__device__ __forceinline__ Trig gathered_trig(const NormRopeAppendArgs& a, const OnePosition& pos,
+                                              int l, float*, float*, float*, float*) {
+  return table_trig(a, pos, l);
+}
+
 template <int kThreadsBound, int kMinBlocks, bool kTable, typename Args>
 __global__ void __launch_bounds__(kThreadsBound, kMinBlocks)
 norm_rope_append_kernel(const __grid_constant__ Args a) {
@@ -279,7 +305,8 @@ norm_rope_append_kernel(const __grid_constant__ Args a) {
   const bool from_table = kTable && in_table(a, pos);
   Trig tr;
   if (from_table) {
-    tr = table_trig(a, pos, l);
+    tr = lanes_mix_axes(a) ? gathered_trig(a, pos, l, s_cos_hi, s_cos_lo, s_sin_hi, s_sin_lo)
+                           : table_trig(a, pos, l);
   } else {
     tr = angles_in_cta(a, pos, l, s_tab, s_cos_hi, s_cos_lo, s_sin_hi, s_sin_lo);
   }
@@ -321,6 +348,12 @@ cudaError_t launch_append(const Args& a, cudaStream_t stream) {
     return launch_pdl(table ? norm_rope_append_kernel<kManyThreads, kTableMinBlocks, true, Args>
                             : norm_rope_append_kernel<kManyThreads, kManyMinBlocks, false, Args>,
                       dim3(a.num_tokens), dim3(warps * 32), 0, stream, a);
+  if (many) {
+    warps = warps > kWideThreads / 32 ? kWideThreads / 32 : warps;
+    return launch_pdl(table ? norm_rope_append_kernel<kWideThreads, kWideMinBlocks, true, Args>
+                            : norm_rope_append_kernel<kWideThreads, kWideMinBlocks, false, Args>,
+                      dim3(a.num_tokens), dim3(warps * 32), 0, stream, a);
+  }
   return launch_pdl(table ? norm_rope_append_kernel<kMaxThreads, 1, true, Args>
                           : norm_rope_append_kernel<kMaxThreads, 1, false, Args>,
                     dim3(a.num_tokens), dim3(warps * 32), 0, stream, a);
