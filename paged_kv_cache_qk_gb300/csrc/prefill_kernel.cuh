@@ -54,13 +54,6 @@
 // convert the codes between their tiles, Q is brought in as f16 before the
 // roles begin, and scales enter at the softmax (half_tile).
 //
-// Score rules (kRules != 0, bf16 caches): a row sees the interval of keys that
-// score_rules.cuh gives it, a CTA walks the key tiles from its rows' first visible key
-// to their last, and its splits are counted from there (a window's row tiles differ in
-// their keys, not in how many).  Scores are capped and biased in registers before
-// their maximum is taken (scored_half_tile); a kernel is built for each of cap and bias,
-// so that a call pays for what it asks for.
-//
 // Shared memory (1024-byte aligned, 128-byte swizzle everywhere, the layout
 // the MMA descriptors describe):
 //   Q_A, Q_B  [2 dim halves][128 rows][64 bf16]      2 x 32 KiB
@@ -79,10 +72,7 @@
 #include "device_common.cuh"
 #include "q8_common.cuh"
 #include "prefill.h"
-#include "score_rules.cuh"
 #include "tc5.cuh"
-
-#include <climits>
 
 namespace pkvqk {
 
@@ -113,11 +103,6 @@ constexpr float kBiasQ8 = 10.f;
 constexpr int kScaleSlots = 4;                 // key tiles whose scales are held at once
 constexpr int kGroupsPerTile = kN / kScaleGroup;
 constexpr float kLn2 = 0.6931471805599453f;
-
-// Score rules a kernel is built for: intervals of keys alone, and what scores go through.
-// kRuleBounded: a cap without a bias, small enough for one reference (bounded_half_tile).
-constexpr int kRuleIntervals = 1, kRuleCap = 2, kRuleBias = 4, kRuleBounded = 8;
-constexpr float kBoundedCap = 80.f;            // log2 units: caps up to 55.4
 
 struct Bars {
   uint64_t full_k[kStages], full_v[kStages];     // TMA landed
@@ -165,6 +150,13 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 // 8-row groups 1024 bytes apart.
 __device__ __forceinline__ uint64_t desc_k_major(uint32_t tile, int kk) {
   return tc5::smem_desc_sw128(tile + (kk >> 2) * kHalf + (kk & 3) * 32, 16, 1024);
+}
+
+// Slots per cache box: the largest power of two dividing the page size, at
+// most a key tile; a tile's boxes start at multiples of it, so none crosses a
+// page.  Returns log2.
+__device__ __forceinline__ int box_shift(int block_size) {
+  return __ffs(min(block_size & -block_size, kN)) - 1;
 }
 
 // V stage as the MN-major B operand of O += P V (N = dims, K = keys), one
@@ -236,18 +228,18 @@ struct Work {
   long long q0;  // row of q/out holding its token 0
   int rows;      // q_len * group
   bool has_b;    // row tile B holds rows
-  int key_begin; // scored: keys below it are visible to no row of the CTA
 };
 
-// What the grid and the row offsets say; L is the sequence's length as read.
-__device__ __forceinline__ Work place_work(const PrefillArgs& a) {
+// What the place (bx, by) in the grid and the row offsets say; L is the sequence's length
+// as read.
+__device__ __forceinline__ Work place_work(const PrefillArgs& a, int bx, int by) {
   Work w;
   if (a.mt_major) {
     // the launch order runs over all sequences' last row tiles first: for
     // fresh prompts a row tile's keys grow with its index, so this hands the
     // longest work out first (row_tile_major: the CTA's number fits an int)
     const int per_mt = gridDim.y * a.num_kv_heads * a.num_splits;
-    int x = blockIdx.y * gridDim.x + blockIdx.x;
+    int x = by * gridDim.x + bx;
     w.mt = a.m_tiles - 1 - x / per_mt;
     x %= per_mt;
     w.b = x / (a.num_kv_heads * a.num_splits);
@@ -256,12 +248,12 @@ __device__ __forceinline__ Work place_work(const PrefillArgs& a) {
     w.j = x % a.num_splits;
   } else {
     // within a (sequence, kv head) the last row tile (the most keys) first
-    int x = blockIdx.x;
+    int x = bx;
     w.mt = a.m_tiles - 1 - x % a.m_tiles;
     x /= a.m_tiles;
     w.g = x % a.num_kv_heads;
     w.j = x / a.num_kv_heads;
-    w.b = blockIdx.y;
+    w.b = by;
   }
   w.L = a.seq_lens[w.b];
   if (a.cu_seqlens_q != nullptr) {
@@ -276,58 +268,19 @@ __device__ __forceinline__ Work place_work(const PrefillArgs& a) {
   return w;
 }
 
-// Slots per cache box: the largest power of two dividing the page size, at
-// most a key tile; a tile's boxes start at multiples of it, so none crosses a
-// page.  Returns log2.
-__device__ __forceinline__ int box_shift(int block_size) {
-  return __ffs(min(block_size & -block_size, kN)) - 1;
-}
-
-// The least first key of the CTA's rows (every thread takes part; a token's rows share it).
-__device__ __forceinline__ int least_first_key(const PrefillArgs& a, const Work& w,
-                                               int* shared_least) {
-  if (threadIdx.x == 0) *shared_least = INT_MAX;
-  __syncthreads();
-  const int row0 = w.mt * 2 * kM;
-  const int t0 = div_group(a, row0), t1 = div_group(a, min(row0 + 2 * kM, w.rows) - 1);
-  int least = INT_MAX;
-  for (int t = t0 + static_cast<int>(threadIdx.x); t <= t1; t += kThreads) {
-    const long long row = w.q0 + t;
-    if (row >= 0 && row < a.total_q) least = min(least, a.rules.first_keys[row]);
-  }
-  least = __reduce_min_sync(0xffffffffu, least);
-  if ((threadIdx.x & 31) == 0 && least != INT_MAX) atomicMin(shared_least, least);
-  __syncthreads();
-  return *shared_least;
-}
-
-// The keys of the CTA's rows.  first_key: least_first_key (scored; 0 without documents).
-template <int kRules>
-__device__ __forceinline__ void find_keys(const PrefillArgs& a, Work& w, int first_key) {
+// The keys of the CTA's rows.
+__device__ __forceinline__ void find_keys(const PrefillArgs& a, Work& w) {
   const long long cap = static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
   const long long L = min(static_cast<long long>(max(w.L, 0)), cap);
   w.L = static_cast<int>(L);
   const long long chunk_keys = static_cast<long long>(a.chunk_pages) * a.block_size;
+  w.k0 = static_cast<int>(min(L, w.j * chunk_keys));
+  w.k1 = (w.j == a.num_splits - 1) ? w.L : static_cast<int>(min(L, (w.j + 1) * chunk_keys));
   const int row0 = w.mt * 2 * kM;
-  w.key_begin = 0;
-  if (kRules != 0) {
-    const int p0 = w.L - w.q_len + div_group(a, row0);   // the CTA's first row's position
-    w.key_begin = min(w.L, max(window_start(a.rules, p0), first_key));
-  }
-  // the page that splits are counted from
-  const long long base = kRules != 0 ? w.key_begin / a.block_size * a.block_size : 0;
-  w.k0 = static_cast<int>(min(L, base + w.j * chunk_keys));
-  w.k1 = (w.j == a.num_splits - 1) ? w.L
-                                   : static_cast<int>(min(L, base + (w.j + 1) * chunk_keys));
-  if (kRules != 0)                             // boxes start at multiples of their slots
-    w.k0 = max(w.k0, w.key_begin >> box_shift(a.block_size) << box_shift(a.block_size));
   w.has_b = row0 + kM < w.rows;
   const int last_row = min(row0 + 2 * kM - 1, w.rows - 1);
   const int t_last = div_group(a, max(last_row, 0));   // rows == 0: no tiles either way
-  int end = w.L - w.q_len + t_last + 1;
-  if (kRules != 0) end = max(end, prefix_end(a.rules, w.b, w.L));
-  w.key_end = max(w.k0, min(w.k1, end));
-  if (kRules != 0 && w.key_end <= w.key_begin) w.key_end = w.k0;   // nothing to see
+  w.key_end = max(w.k0, min(w.k1, w.L - w.q_len + t_last + 1));
   w.ntiles = row0 < w.rows ? (w.key_end - w.k0 + kN - 1) / kN : 0;
 }
 
@@ -1008,183 +961,6 @@ __device__ __forceinline__ float half_tile(uint32_t scol, uint32_t pcol, int kba
   return psum;
 }
 
-// add + cap * tanh(k v) of 32 raw scores, k = scale log2(e) / cap: two at a time by the
-// polynomial that the largest of the warp's scores allows, or one by one.
-template <int kDegree>
-__device__ __forceinline__ void cap_pairs(float (&v)[32], float k, float cap, float add) {
-  const uint64_t k2 = pack2(k, k), add2_ = pack2(add, add);
-  uint64_t c[kDegree + 1];                     // the cap is in the coefficients
-#pragma unroll
-  for (int i = 0; i <= kDegree; ++i)
-    c[i] = pack2(cap * tanh_q<kDegree>(i), cap * tanh_q<kDegree>(i));
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    const uint64_t x = mul2(pack2(v[e], v[e + 1]), k2);
-    const uint64_t u = mul2(x, x);
-    uint64_t q = c[kDegree];
-#pragma unroll
-    for (int i = kDegree - 1; i >= 0; --i) q = fma2(q, u, c[i]);
-    unpack2(fma2(x, q, add2_), v[e], v[e + 1]);
-  }
-}
-__device__ __forceinline__ void cap_chunk(float (&v)[32], float k, float cap, float add) {
-  // the largest |v| decides; a NaN that is masked later does not count
-  float b4[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-  for (int e = 0; e < 32; e += 2)
-    b4[(e >> 1) & 3] = max3(b4[(e >> 1) & 3], fabsf(v[e]), fabsf(v[e + 1]));
-  const float big = max3(b4[0], b4[1], fmaxf(b4[2], b4[3])) * k;
-  if (!__any_sync(0xffffffffu, big * big > kTanhSmall)) {
-    cap_pairs<3>(v, k, cap, add);
-  } else if (!__any_sync(0xffffffffu, big * big > kTanhSquare)) {
-    cap_pairs<5>(v, k, cap, add);
-  } else {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float x = v[e] * k, u = x * x;
-      v[e] = fmaf(cap, u <= kTanhSquare ? tanh_near(x, u) : tanh_far(x), add);
-    }
-  }
-}
-
-// Scores of the keys outside [lo, hi) to -inf.  Most masked tiles are cut at one end: the
-// other's comparisons are skipped where none of the warp's rows needs them.
-__device__ __forceinline__ void hide_keys(float (&v)[32], int lo, int hi) {
-  if (__any_sync(0xffffffffu, hi < 32)) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = e < hi ? v[e] : -INFINITY;
-  }
-  if (__any_sync(0xffffffffu, lo > 0)) {
-#pragma unroll
-    for (int e = 0; e < 32; ++e) v[e] = e >= lo ? v[e] : -INFINITY;
-  }
-}
-
-// P of a half tile of which none of the warp's rows sees a key.
-__device__ __forceinline__ void zero_half_tile(uint32_t pcol) {
-  uint32_t z[16];
-#pragma unroll
-  for (int j = 0; j < 16; ++j) z[j] = 0u;
-  tc5::tmem_st16(pcol, z);
-  tc5::tmem_st16(pcol + 16, z);
-}
-
-// half_tile under a cap without a bias.  Capped scores lie in [-cap, cap], so one
-// reference serves every row, ref = cap / 4 (log2 units): P = 2^(s - ref) stays between
-// 2^-100 and 2^60, where bf16 and fp32 keep all their bits, and 2^20 of them with values up
-// to 2^46 fit the accumulators.  So no maximum is taken, O is never rescaled, and the row's
-// halves need not meet before the end.
-template <bool kMasked>
-__device__ __forceinline__ float bounded_half_tile(uint32_t scol, uint32_t pcol, int kbase,
-                                                   int nlo, int nvis, float k, float cap,
-                                                   float ref) {
-  uint64_t acc[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) acc[j] = pack2(0.f, 0.f);
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    float v[32];
-    tc5::tmem_ld32(scol + c * 32, v);
-    tc5::wait_ld();
-    cap_chunk(v, k, cap, -ref);
-    if (kMasked) hide_keys(v, nlo - kbase - c * 32, nvis - kbase - c * 32);
-    uint32_t pk[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const float p0 = ex2_approx(v[2 * q]), p1 = ex2_approx(v[2 * q + 1]);
-      acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
-      pk[q] = pack_bf16x2(p0, p1);
-    }
-    tc5::tmem_st16(pcol + c * 16, pk);
-  }
-  float t0, t1;
-  unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), t0, t1);
-  return t0 + t1;
-}
-
-// half_tile over a bf16 cache under score rules: scores go through the cap and the
-// bias (log2 units) before their maximum is taken.  Keys kbase + e with nlo <= kbase + e <
-// nvis count (kMasked); `at` is the tile's first key less the row's position.  An
-// unmasked tile has no key past any of the warp's positions, where the bias
-// -slope (p - n) = slope e + slope (base - p) is one packed FMA a pair of keys, its constant
-// part joined with the reference; a masked one may (a prefix), and takes |p - n|.
-template <int kRules, bool kMasked, typename Publish>
-__device__ __forceinline__ float scored_half_tile(uint32_t scol, uint32_t pcol, int kbase, int nlo,
-                                                  int nvis, float sl2, const ScoreRules& rules,
-                                                  float slope, int at, float& m_ref,
-                                                  Publish&& publish) {
-  float psum = 0.f;
-#pragma unroll
-  for (int c = 0; c < 2; ++c) {
-    float v[32];
-    tc5::tmem_ld32(scol + c * 32, v);
-    tc5::wait_ld();
-    const int k0 = kbase + c * 32;
-    if (kRules & kRuleCap) {
-      cap_chunk(v, sl2 * rules.inv_cap, rules.cap, 0.f);
-    } else if (kRules & kRuleBias) {
-      const uint64_t scale2 = pack2(sl2, sl2);
-#pragma unroll
-      for (int e = 0; e < 32; e += 2)
-        unpack2(mul2(pack2(v[e], v[e + 1]), scale2), v[e], v[e + 1]);
-    }
-    float shift = 0.f;                         // what the chunk's scores still lack
-    if (kRules & kRuleBias) {
-      const float d0 = static_cast<float>(at + k0);        // exact: |d| < 2^24 or far away
-      if (kMasked) {
-#pragma unroll
-        for (int e = 0; e < 32; ++e) v[e] = fmaf(-slope, fabsf(d0 + static_cast<float>(e)), v[e]);
-      } else {
-        const uint64_t slope2 = pack2(slope, slope);
-#pragma unroll
-        for (int e = 0; e < 32; e += 2)
-          unpack2(fma2(slope2, pack2(static_cast<float>(e), static_cast<float>(e + 1)),
-                       pack2(v[e], v[e + 1])),
-                  v[e], v[e + 1]);
-        shift = slope * d0;
-      }
-    }
-    if (kMasked) hide_keys(v, nlo - k0, nvis - k0);
-    float m4[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) m4[j] = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < 32; e += 2) m4[(e >> 1) & 3] = max3(m4[(e >> 1) & 3], v[e], v[e + 1]);
-    float mt = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
-    if (kRules == kRuleIntervals) mt *= sl2;
-    else mt += shift;
-    const bool grow = mt > m_ref + kRescaleLog2;
-    if (__any_sync(0xffffffffu, grow)) {
-      const float m_new = grow ? ceilf(mt) : m_ref;
-      const float f = grow ? pow2_int(m_ref - m_new) : 1.f;
-      if (c == 1) scale_p<0, 16>(pcol, f);
-      psum *= f;
-      m_ref = m_new;
-    }
-    if (c == 1) publish(m_ref);
-    const float u = shift - ((m_ref == -INFINITY) ? 0.f : m_ref);
-    const uint64_t scale2 = pack2(sl2, sl2), shift2 = pack2(u, u);
-    uint64_t acc[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = pack2(0.f, 0.f);
-    uint32_t pk[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      const uint64_t z = pack2(v[2 * q], v[2 * q + 1]);
-      float x0, x1;
-      unpack2(kRules == kRuleIntervals ? fma2(z, scale2, shift2) : add2(z, shift2), x0, x1);
-      const float p0 = ex2_approx(x0), p1 = ex2_approx(x1);
-      acc[q & 3] = add2(acc[q & 3], pack2(p0, p1));
-      pk[q] = pack_bf16x2(p0, p1);
-    }
-    tc5::tmem_st16(pcol + c * 16, pk);
-    float t0, t1;
-    unpack2(add2(add2(acc[0], acc[1]), add2(acc[2], acc[3])), t0, t1);
-    psum += t0 + t1;
-  }
-  return psum;
-}
-
 // Swap one value per row with the other half of the warp pair, in two parts
 // so that work can run in between: publish v in this half's slot of the
 // current parity and arrive on the pair's barrier; then wait (bounded) for
@@ -1331,7 +1107,7 @@ __device__ __forceinline__ void write_rows(const PrefillArgs& a, const Work& w, 
   }
 }
 
-template <int kFormat, int kRules>
+template <int kFormat>
 __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem, Bars* bars,
                              const CUtensorMap* omap, float* xslots, uint32_t tmem, int x,
                              int half) {
@@ -1341,24 +1117,7 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
   const bool valid = rg < w.rows;
   const int t = valid ? div_group(a, rg) : 0;
   // keys [k0, lim) are visible to this row
-  int lim = valid ? max(w.k0, min(w.k1, w.L - w.q_len + t + 1)) : w.k0;
-  // scored: keys [lo, lim), the row's position, its slope (log2 units)
-  int lo = 0, pos = 0;
-  float slope = 0.f;
-  if (kRules != 0) {
-    pos = w.L - w.q_len + t;
-    // a row outside q has no first key to read (and is not written)
-    const bool inside = valid && w.q0 + t >= 0 && w.q0 + t < a.total_q;
-    if (inside) {
-      const Interval seen = visible_keys(a.rules, w.b, w.q0 + t, pos, w.L);
-      lo = seen.lo;
-      lim = max(w.k0, min(w.k1, seen.hi));
-    } else {
-      lim = w.k0;
-    }
-    if ((kRules & kRuleBias) && inside && a.rules.slopes != nullptr)
-      slope = a.rules.slopes[w.g * a.group + rg - t * a.group] * 1.4426950408889634f;
-  }
+  const int lim = valid ? max(w.k0, min(w.k1, w.L - w.q_len + t + 1)) : w.k0;
   const uint32_t lanes = tmem + (static_cast<uint32_t>(wq * 32) << 16);
   const uint32_t s_cols = lanes + kColS + x * kN + half * (kN / 2);
   const uint32_t o_cols = lanes + kColO + x * kN + half * (kHeadDim / 2);
@@ -1378,20 +1137,11 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
   int lim_min = lim;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) lim_min = min(lim_min, __shfl_xor_sync(0xffffffffu, lim_min, o));
-  // scored: the first key that all of the warp's rows see, and their least position's end
-  const int lo_max = kRules != 0 ? __reduce_max_sync(0xffffffffu, lo) : 0;
-  const int lo_least =
-      kRules != 0 ? __reduce_min_sync(0xffffffffu, lim > w.k0 ? lo : INT_MAX) : 0;
-  const int lim_most = kRules != 0 ? __reduce_max_sync(0xffffffffu, lim) : 0;
-  if (kRules & kRuleBias)
-    lim_min = min(lim_min, __reduce_min_sync(0xffffffffu, valid ? pos + 1 : w.k0));
   const int n = w.ntiles;
   const int k0 = w.k0;
   const int tail_tile = (kFormat == 0 && x == 0 && k0 + n * kN > w.key_end) ? n - 1 : -1;
-  const int head_tile = (kRules != 0 && x == 0 && k0 < w.key_begin) ? 0 : -1;
 
-  // reference max (log2 units), integer once set
-  float m_ref = kRules & kRuleBounded ? 0.25f * a.rules.cap : -INFINITY;
+  float m_ref = -INFINITY;                     // reference max (log2 units), integer once set
   float l = 0.f;                               // this half's sum of P
   // the first tiles; K(1) by tile B's warps, whose scores come after tile A's
   if (kFormat != 0 && n > 0)
@@ -1417,36 +1167,17 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
     const int kb = k0 + i * kN;
     const int nvis = min(kN, max(0, lim - kb));   // keys kb .. kb + nvis - 1 visible
     // interior tiles (every row of the warp sees all 128 keys) skip the masks
-    const bool whole = lim_min >= kb + kN && (kRules == 0 || lo_max <= kb);
+    const bool whole = lim_min >= kb + kN;
     const float m_start = m_ref;
     auto publish = [&](float m) { swap_publish(m, slots, xbar, uses, half, r); };
-    float psum = 0.f;
-    // scored: nothing of this half tile is visible to the warp's rows
-    const int h0 = kb + half * (kN / 2);
-    const bool hidden = kRules != 0 && (lim_most <= h0 || lo_least >= h0 + kN / 2);
-    if (hidden) {
-      zero_half_tile(s_cols);
-      if (!(kRules & kRuleBounded)) publish(m_ref);
-    } else if constexpr ((kRules & kRuleBounded) != 0)
-      psum = whole ? bounded_half_tile<false>(s_cols, s_cols, half * (kN / 2), 0, nvis,
-                                              sl2 * a.rules.inv_cap, a.rules.cap, m_ref)
-                   : bounded_half_tile<true>(s_cols, s_cols, half * (kN / 2), lo - kb, nvis,
-                                             sl2 * a.rules.inv_cap, a.rules.cap, m_ref);
-    else if constexpr (kRules != 0)
-      psum = whole ? scored_half_tile<kRules, false>(s_cols, s_cols, half * (kN / 2), 0, nvis, sl2,
-                                                     a.rules, slope, kb - pos, m_ref, publish)
-                   : scored_half_tile<kRules, true>(s_cols, s_cols, half * (kN / 2), lo - kb, nvis,
-                                                    sl2, a.rules, slope, kb - pos, m_ref, publish);
-    else
-      psum = whole ? half_tile<kFormat, false>(s_cols, s_cols, half * (kN / 2), nvis, sl2,
-                                               scales, m_ref, publish)
-                   : half_tile<kFormat, true>(s_cols, s_cols, half * (kN / 2), nvis, sl2,
-                                              scales, m_ref, publish);
+    float psum = whole ? half_tile<kFormat, false>(s_cols, s_cols, half * (kN / 2), nvis, sl2,
+                                                   scales, m_ref, publish)
+                       : half_tile<kFormat, true>(s_cols, s_cols, half * (kN / 2), nvis, sl2,
+                                                  scales, m_ref, publish);
     // one reference per row: the higher of the two halves'
-    const float m_other =
-        kRules & kRuleBounded ? m_ref : swap_read(slots, xbar, uses, half, r, ok);
+    const float m_other = swap_read(slots, xbar, uses, half, r, ok);
     if (!ok) break;
-    if ((kRules & kRuleBounded) || __all_sync(0xffffffffu, m_ref == m_start && m_other == m_start)) {
+    if (__all_sync(0xffffffffu, m_ref == m_start && m_other == m_start)) {
       l += psum;                               // neither half moved (the usual tile)
     } else {
       const float m_row = fmaxf(m_ref, m_other);
@@ -1474,14 +1205,14 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
     // Tail tile: cache slots past the last visible key may hold anything
     // (stale or never-written rows); P is 0 there, but 0 x NaN is NaN, so
     // their V rows are zeroed (by tile A, each half its dims, before either
-    // PV reads them).  Scored: likewise the slots before the first visible key.
-    if (i == tail_tile || i == head_tile) {
+    // PV reads them).
+    if (i == tail_tile) {
       const int s = i & 1;
       if (!warp_wait(&bars->full_v[s], (i >> 1) & 1)) {
         ok = false;
         break;
       }
-      if (kb + r >= w.key_end || (kRules != 0 && kb + r < w.key_begin)) {
+      if (kb + r >= w.key_end) {
         uint8_t* vrow = smem + kOffV + s * kTile + v_row_offset(r, half, box_shift(a.block_size));
         const uint4 z = make_uint4(0u, 0u, 0u, 0u);
 #pragma unroll
@@ -1520,7 +1251,7 @@ __device__ void softmax_rows(const PrefillArgs& a, const Work& w, uint8_t* smem,
 
 // 18 warps: two of the SM's four sub-partitions hold five of them, so a
 // thread gets at most 96 registers (16,384 per sub-partition).
-template <int kFormat, int kRules = 0>
+template <int kFormat>
 __global__ void __maxnreg__(96)
 paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
                      const __grid_constant__ CUtensorMap vmap,
@@ -1537,18 +1268,13 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
   // launched as a programmatic dependent: q, the appended K/V, the tables and
   // the lengths may come from the previous kernel in the stream
   pdl_wait();
-  Work w = place_work(a);
+  Work w = place_work(a, blockIdx.x, blockIdx.y);
   // row tiles past this sequence's rows (varlen grids cover the longest
   // sequence): nothing to compute or write; leave before any set-up
   if (w.mt * 2 * kM >= w.rows) return;
   uint4 q_row[kQRowsEach];                     // 8-bit: Q on its way before the length is known
   if (kFormat != 0 && warp < kSoftmaxWarps) load_q_rows(a, w, q_row);
-  int first_key = 0;
-  if constexpr (kRules != 0) {
-    __shared__ int shared_least;
-    if (a.rules.first_keys != nullptr) first_key = least_first_key(a, w, &shared_least);
-  }
-  find_keys<kRules>(a, w, first_key);
+  find_keys(a, w);
 
   if (threadIdx.x == kProducerWarp * 32) {
     prefetch_tensormap(&kmap);
@@ -1634,8 +1360,8 @@ paged_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     const int x = warp >> 3, half = (warp >> 2) & 1;
     if (x == 0 || w.has_b)
       // 8-bit: the work's fields stay in shared memory, for the registers' sake
-      softmax_rows<kFormat, kRules>(a, kFormat == 0 ? w : shared_work, smem, bars, &omap,
-                                    reinterpret_cast<float*>(smem + kOffSlots), tmem, x, half);
+      softmax_rows<kFormat>(a, kFormat == 0 ? w : shared_work, smem, bars, &omap,
+                            reinterpret_cast<float*>(smem + kOffSlots), tmem, x, half);
     else if (kFormat != 0)                     // no tile B: codes are all its warps do
       convert_without_b<kFormat>(a, w, smem, bars);
   } else if (warp == kProducerWarp) {

@@ -366,3 +366,31 @@ def test_nan_rows_stay_alone(lib):
         out, lse = run(q, k)
         assert torch.isnan(out.float())[rows].all() and torch.isnan(lse)[rows].all()
         assert torch.equal(out[~rows], clean[0][~rows]) and torch.equal(lse[~rows], clean[1][~rows])
+
+
+@pytest.mark.parametrize("rules", ["none", "cap", "slopes", "window", "documents", "all"])
+def test_more_places_than_sms(lib, rules):
+    """Grids that each SM works through several places of: even and packed batches (listed
+    and, past 256 sequences, not), with and without boxes of q, whole and split."""
+    rng = np.random.default_rng(5)
+    lens = [int(rng.integers(1, 400)) for _ in range(40)]
+    new = [int(rng.integers(0, n + 1)) for n in lens]
+    for Hq, Hkv in ((16, 8), (12, 4)):
+        c = Case(Hq, Hkv, 16, lens, new, 90, gain=2.0)
+        for S in (1, 3):
+            c.check(lib, "paged_prefill_scored", S, seqs=[0, 7, 19, 39], **_rules(rules, c, S))
+    lens = [int(rng.integers(1, 40)) for _ in range(300)]
+    c = Case(4, 2, 16, lens, [int(rng.integers(0, n + 1)) for n in lens], 91, gain=2.0)
+    c.check(lib, "paged_prefill_scored", 1, seqs=list(range(0, 300, 29)), **_rules(rules, c, 1))
+    c = Case(16, 8, 16, [300 + 5 * i for i in range(30)], 260, 92, gain=2.0)
+    c.check(lib, "paged_prefill_scored", 1, seqs=[0, 17, 29], **_rules(rules, c, 1))
+
+
+def test_places_in_order_give_the_same_bits(lib):
+    """Which SM takes which place is decided as they come free: the results do not show it."""
+    rng = np.random.default_rng(6)
+    lens = [int(rng.integers(100, 900)) for _ in range(24)]
+    c = Case(16, 8, 16, lens, lens, 93, gain=2.0)
+    r = _rules("all", c)
+    outs = [c.check(lib, "paged_prefill_scored", 1, seqs=[3], **r) for _ in range(4)]
+    assert all(torch.equal(o[0], outs[0][0]) and torch.equal(o[1], outs[0][1]) for o in outs)
