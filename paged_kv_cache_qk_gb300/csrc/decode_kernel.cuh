@@ -53,6 +53,7 @@
 #include "kernels.h"
 #include "score_rules.cuh"
 
+#include <climits>
 #include <cmath>
 
 namespace pkvqk {
@@ -194,6 +195,15 @@ __device__ void consume_simt(const DecodeArgs& a, const Plan* plan, const uint8_
         slope[rr] = row_slope(a, kvh * a.group + gi);
       }
     }
+    // scored: tiles within [begin_most, limit_least) are visible to every row
+    int begin_most = 0, limit_least = INT_MAX;
+    if constexpr (kScored) {
+#pragma unroll
+      for (int rr = 0; rr < R; ++rr) {
+        begin_most = max(begin_most, begin[rr]);
+        limit_least = min(limit_least, limit[rr]);
+      }
+    }
 
     for (int i = 0; i < seg.ntiles; ++i, ++it) {
       const int s = it % STAGES;
@@ -236,15 +246,31 @@ __device__ void consume_simt(const DecodeArgs& a, const Plan* plan, const uint8_
         }
       }
       if constexpr (kScored) {
+        if (a.rules.cap > 0.f) {
+          float z[R * kQuads];
 #pragma unroll
-        for (int rr = 0; rr < R; ++rr) {
-          if (a.rules.cap > 0.f) cap_scores(a.rules, sc[rr]);
+          for (int e = 0; e < R * kQuads; ++e) z[e] = sc[e / kQuads][e % kQuads];
+          cap_scores(a.rules, z);
 #pragma unroll
-          for (int q4 = 0; q4 < kQuads; ++q4) {
-            const int n = key0 + q4 * 4 + kg;
-            const float d = fmaf(-slope[rr], fabsf(static_cast<float>(pos[rr] - n)), sc[rr][q4]);
-            sc[rr][q4] = (n >= begin[rr] && n < limit[rr]) ? d : -INFINITY;
+          for (int e = 0; e < R * kQuads; ++e) sc[e / kQuads][e % kQuads] = z[e];
+        }
+        if (a.rules.slopes != nullptr) {
+#pragma unroll
+          for (int rr = 0; rr < R; ++rr) {
+            const float d0 = static_cast<float>(pos[rr] - key0 - kg);
+#pragma unroll
+            for (int q4 = 0; q4 < kQuads; ++q4)
+              sc[rr][q4] = fmaf(-slope[rr], fabsf(d0 - 4.f * q4), sc[rr][q4]);
           }
+        }
+        if (key0 < begin_most || key0 + TK > limit_least) {
+#pragma unroll
+          for (int rr = 0; rr < R; ++rr)
+#pragma unroll
+            for (int q4 = 0; q4 < kQuads; ++q4) {
+              const int n = key0 + q4 * 4 + kg;
+              if (n < begin[rr] || n >= limit[rr]) sc[rr][q4] = -INFINITY;
+            }
         }
       }
 
@@ -429,6 +455,13 @@ __device__ void consume_tc(const DecodeArgs& a, const Plan* plan, const uint8_t*
       if (vA) row_rules(rA, limA, posA, loA, slopeA);
       if (vB) row_rules(rB, limB, posB, loB, slopeB);
     }
+    // scored: tiles within [lo_most, lim_least) are visible to all of the warp's rows (rows
+    // past R have no say: what they compute is not written)
+    int lo_most = 0, lim_least = 0;
+    if constexpr (kScored) {
+      lo_most = __reduce_max_sync(0xffffffffu, max(loA, loB));
+      lim_least = __reduce_min_sync(0xffffffffu, min(vA ? limA : INT_MAX, vB ? limB : INT_MAX));
+    }
 
     uint32_t qa[8][4];
 #pragma unroll
@@ -491,20 +524,30 @@ __device__ void consume_tc(const DecodeArgs& a, const Plan* plan, const uint8_t*
             sc[nt][e] = (key < lim) ? sc[nt][e] * a.scale_log2 : -INFINITY;
           }
       } else {
+        float z[8];
 #pragma unroll
-        for (int nt = 0; nt < 2; ++nt) {
+        for (int e = 0; e < 8; ++e) z[e] = sc[e >> 2][e & 3] * a.scale_log2;
+        if (a.rules.cap > 0.f) cap_scores(a.rules, z);
+        // element e: key key0 + 8 (e / 4) + 2 c + e % 2, row A (e % 4 < 2) or B
+        if (a.rules.slopes != nullptr) {
+          const float dA = static_cast<float>(posA - key0 - 2 * c);
+          const float dB = static_cast<float>(posB - key0 - 2 * c);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[nt][e] *= a.scale_log2;
-          if (a.rules.cap > 0.f) cap_scores(a.rules, sc[nt]);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) {
-            const int key = key0 + 8 * nt + 2 * c + (e & 1);
-            const float far = fabsf(static_cast<float>((e < 2 ? posA : posB) - key));
-            const float z = fmaf(e < 2 ? -slopeA : -slopeB, far, sc[nt][e]);
-            const bool seen = key >= (e < 2 ? loA : loB) && key < (e < 2 ? limA : limB);
-            sc[nt][e] = seen ? z : -INFINITY;
+          for (int e = 0; e < 8; ++e) {
+            const float k = static_cast<float>(8 * (e >> 2) + (e & 1));
+            z[e] = (e & 2) ? fmaf(-slopeB, fabsf(dB - k), z[e])
+                           : fmaf(-slopeA, fabsf(dA - k), z[e]);
           }
         }
+        if (key0 < lo_most || key0 + TK > lim_least) {
+#pragma unroll
+          for (int e = 0; e < 8; ++e) {
+            const int key = key0 + 8 * (e >> 2) + 2 * c + (e & 1);
+            if (key < ((e & 2) ? loB : loA) || key >= ((e & 2) ? limB : limA)) z[e] = -INFINITY;
+          }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sc[e >> 2][e & 3] = z[e];
       }
 
       float tA = fmaxf(fmaxf(sc[0][0], sc[0][1]), fmaxf(sc[1][0], sc[1][1]));

@@ -54,22 +54,38 @@ __device__ __forceinline__ float tanh_near(float x, float u) {
   return q * x;
 }
 
-// N scores of every lane of a warp capped in place.
+// N scores (pairs of them) of every lane of a warp capped in place.
+template <int kDegree, int N>
+__device__ __forceinline__ void cap_near(const ScoreRules& r, float (&z)[N]) {
+  const uint64_t inv2 = pack2(r.inv_cap, r.inv_cap), cap2 = pack2(r.cap, r.cap);
+#pragma unroll
+  for (int i = 0; i < N; i += 2) {
+    const uint64_t x = mul2(pack2(z[i], z[i + 1]), inv2);
+    const uint64_t u = mul2(x, x);
+    uint64_t q = pack2(tanh_q<kDegree>(kDegree), tanh_q<kDegree>(kDegree));
+#pragma unroll
+    for (int k = kDegree - 1; k >= 0; --k)
+      q = fma2(q, u, pack2(tanh_q<kDegree>(k), tanh_q<kDegree>(k)));
+    unpack2(mul2(mul2(x, cap2), q), z[i], z[i + 1]);
+  }
+}
 template <int N>
 __device__ __forceinline__ void cap_scores(const ScoreRules& r, float (&z)[N]) {
-  float x[N];
-  bool far = false;
+  // the largest |score| decides; a NaN that is hidden later does not count
+  float big = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) {
-    x[i] = z[i] * r.inv_cap;
-    const float u = x[i] * x[i];
-    z[i] = tanh_near(x[i], u) * r.cap;
-    far = far || !(u <= kTanhSquare);
-  }
-  if (__any_sync(0xffffffffu, far)) {
+  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(z[i]));
+  big *= r.inv_cap;
+  if (!__any_sync(0xffffffffu, big * big > kTanhSmall)) {
+    cap_near<3>(r, z);
+  } else if (!__any_sync(0xffffffffu, big * big > kTanhSquare)) {
+    cap_near<5>(r, z);
+  } else {
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-      if (!(x[i] * x[i] <= kTanhSquare)) z[i] = tanh_far(x[i]) * r.cap;
+    for (int i = 0; i < N; ++i) {
+      const float x = z[i] * r.inv_cap, u = x * x;
+      z[i] = r.cap * (u <= kTanhSquare ? tanh_near(x, u) : tanh_far(x));
+    }
   }
 }
 
