@@ -403,22 +403,40 @@ __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* ba
 
 // --------------------------------------------------------------- softmax
 
-// add + cap * tanh(k v) of 32 raw scores, k = scale log2(e) / cap: two at a time by the
-// polynomial that the largest of the warp's scores allows, or one by one.
-template <int kDegree>
-__device__ __forceinline__ void cap_pairs(float (&v)[32], float k, float cap, float add) {
-  const uint64_t k2 = pack2(k, k), add2_ = pack2(add, add);
-  uint64_t c[kDegree + 1];                     // the cap is in the coefficients
+// add + cap * tanh(k v) of 32 raw scores, k = scale / softcap: two at a time by the polynomial
+// that the largest of the warp's scores allows, or one by one.  Degree 3 has k and the
+// cap in its coefficients, v R(v^2): five packed instructions a pair.  That holds for
+// kSmallestK <= k <= kLargestK, where cap k^7, the last of them, neither under- nor overflows
+// (caps are 2^-20 .. 2^20 of the scores' own); another k takes degree 5.
+constexpr float kSmallestK = 0x1p-16f, kLargestK = 0x1p14f;
+
+__device__ __forceinline__ void cap_pairs_3(float (&v)[32], float k, float cap, float add) {
+  uint64_t c[4];
+  float f = cap * k;
 #pragma unroll
-  for (int i = 0; i <= kDegree; ++i)
-    c[i] = pack2(cap * tanh_q<kDegree>(i), cap * tanh_q<kDegree>(i));
+  for (int i = 0; i < 4; ++i) {
+    c[i] = pack2(f * tanh_q<3>(i), f * tanh_q<3>(i));
+    f *= k * k;
+  }
+  const uint64_t add2_ = pack2(add, add);
+#pragma unroll
+  for (int e = 0; e < 32; e += 2) {
+    const uint64_t x = pack2(v[e], v[e + 1]), u = mul2(x, x);
+    unpack2(fma2(x, fma2(fma2(fma2(c[3], u, c[2]), u, c[1]), u, c[0]), add2_), v[e], v[e + 1]);
+  }
+}
+__device__ __forceinline__ void cap_pairs_5(float (&v)[32], float k, float cap, float add) {
+  const uint64_t k2 = pack2(k, k), add2_ = pack2(add, add);
+  uint64_t c[6];                               // the cap is in the coefficients
+#pragma unroll
+  for (int i = 0; i < 6; ++i) c[i] = pack2(cap * tanh_q<5>(i), cap * tanh_q<5>(i));
 #pragma unroll
   for (int e = 0; e < 32; e += 2) {
     const uint64_t x = mul2(pack2(v[e], v[e + 1]), k2);
     const uint64_t u = mul2(x, x);
-    uint64_t q = c[kDegree];
+    uint64_t q = c[5];
 #pragma unroll
-    for (int i = kDegree - 1; i >= 0; --i) q = fma2(q, u, c[i]);
+    for (int i = 4; i >= 0; --i) q = fma2(q, u, c[i]);
     unpack2(fma2(x, q, add2_), v[e], v[e + 1]);
   }
 }
@@ -429,10 +447,11 @@ __device__ __forceinline__ void cap_chunk(float (&v)[32], float k, float cap, fl
   for (int e = 0; e < 32; e += 2)
     b4[(e >> 1) & 3] = max3(b4[(e >> 1) & 3], fabsf(v[e]), fabsf(v[e + 1]));
   const float big = max3(b4[0], b4[1], fmaxf(b4[2], b4[3])) * k;
-  if (!__any_sync(0xffffffffu, big * big > kTanhSmall)) {
-    cap_pairs<3>(v, k, cap, add);
+  const float small = k >= kSmallestK && k <= kLargestK ? kTanhSmall : -1.f;
+  if (!__any_sync(0xffffffffu, big * big > small)) {
+    cap_pairs_3(v, k, cap, add);
   } else if (!__any_sync(0xffffffffu, big * big > kTanhSquare)) {
-    cap_pairs<5>(v, k, cap, add);
+    cap_pairs_5(v, k, cap, add);
   } else {
 #pragma unroll
     for (int e = 0; e < 32; ++e) {

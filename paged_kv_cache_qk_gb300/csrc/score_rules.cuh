@@ -12,7 +12,7 @@
 //
 // tanh without cancellation: x Q(x^2), Q fitted to tanh(x) / x at Chebyshev nodes: of
 // degree 5 up to |x| = 0.75 (largest relative error 3.0e-8, 1.0e-7 evaluated in fp32), of
-// degree 3 up to 0.35 (3.5e-8, 9.1e-8), which takes no special-function unit; beyond,
+// degree 3 up to 0.5 (5.5e-7, 5.9e-7), which takes no special-function unit; beyond,
 // 1 - 2 / (1 + e^2x), whose absolute error of ~1.2e-7 is relative there.  The units'
 // exponentials and reciprocals are what the softmax itself is short of, so a warp computes
 // the last form only where one of its scores is that large.
@@ -24,13 +24,13 @@
 namespace pkvqk {
 
 constexpr float kTanhSquare = 0.5625f;         // x^2 up to which the polynomials serve:
-constexpr float kTanhSmall = 0.1225f;          // of degree 3, above it of degree 5
+constexpr float kTanhSmall = 0.25f;            // of degree 3, above it of degree 5
 
 // Coefficient i of the polynomial of the given degree.
 template <int kDegree>
 __device__ __forceinline__ constexpr float tanh_q(int i) {
   if (kDegree == 3)
-    return i == 0 ? 0.99999994f : i == 1 ? -0.33332425f : i == 2 ? 0.13295884f : -0.04896282f;
+    return i == 0 ? 0.999999464f : i == 1 ? -0.333263755f : i == 2 ? 0.131909117f : -0.0444185808f;
   return i == 0   ? 1.0f
          : i == 1 ? -0.33332968f
          : i == 2 ? 0.13325515f
