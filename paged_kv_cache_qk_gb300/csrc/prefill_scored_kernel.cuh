@@ -21,6 +21,11 @@
 // memory, not through Q's shared memory.  A CTA a place, and this: 16 ragged prompts of
 // documents 72 and 62 us, fresh 4 x 2048 under a cap 86 and 84, 19 x 512 in a window of 4096
 // 353 and 352.  With every SM's places fixed beforehand in place of taken: 78, 82, 351.
+// (Since then the cap costs less: 62, 82, 297.)
+//
+// Key tiles of 64 with two score buffers a row tile, so that the next scores are there when
+// a row tile's warps are done with the last, were slower: the scores of 64 keys cost the tensor
+// core as much as those of 128 (19 x 512 in a window 352 -> 391 us, fresh 4 x 2048 83 -> 96).
 //
 // Every barrier runs on from place to place: a role counts its uses.  Tile B's barriers
 // count only the places that have a tile B.
@@ -47,6 +52,13 @@ constexpr int kRuleIntervals = 1, kRuleCap = 2, kRuleBias = 4, kRuleBounded = 8;
 // to 2^46 fit an fp32 sum.  (In the decode kernel, which waits for HBM, the same gained
 // nothing: 64 x 8192 300.9 -> 300.2 us, and its registers cost the mma tiles 5 %.)
 constexpr float kBoundedCap = 80.f;
+
+// How far (log2) scores may rise above a row's reference before it follows them.  P reaches
+// 2^32 then, which bf16 holds as well as 1 and fp32 sums of 2^20 of them with values up to
+// 2^74 too, and weights down to 2^-126 of the largest keep their bits.  Once a row has seen a
+// tile its reference hardly ever moves: 19 x 512 tokens in a window of 4096 whose scores have a
+// deviation of 3 took 287 us with 2^8, and take 244 so.
+constexpr float kScoredRise = 32.f;
 
 constexpr int kJobs = 2;                       // places whose facts are held at once
 
@@ -565,7 +577,7 @@ __device__ __forceinline__ float scored_half_tile(uint32_t scol, uint32_t pcol, 
     float mt = max3(m4[0], m4[1], fmaxf(m4[2], m4[3]));
     if (kRules == kRuleIntervals) mt *= sl2;
     else mt += shift;
-    const bool grow = mt > m_ref + kRescaleLog2;
+    const bool grow = mt > m_ref + kScoredRise;
     if (__any_sync(0xffffffffu, grow)) {
       const float m_new = grow ? ceilf(mt) : m_ref;
       const float f = grow ? pow2_int(m_ref - m_new) : 1.f;
