@@ -422,10 +422,11 @@ PKVQK_API pkvqk_status pkvqk_paged_decode(
  * on are read, and splits are counted from the page of that key: block-table entries
  * before it may hold anything, and max_seq_len_hint bounds the keys from there to the
  * sequence's end (a window bounds them too, without a hint); give
- * pkvqk_choose_num_splits such spans in place of lengths.  Slots past seq_lens[b] and before the first
- * visible key may hold anything, NaN included.  A V that is not finite, of a key between
- * them, may make NaN of any row of its sequence and kv head.
- * A row with no visible key outputs 0 and lse = -inf.
+ * pkvqk_choose_num_splits such spans in place of lengths.  Slots past seq_lens[b] and
+ * before the first visible key may hold anything, NaN included.  A V between them that is
+ * not finite, or of a magnitude of 2^46 and more, may make NaN or infinities of any row of
+ * its sequence and kv head.  A row with no visible key outputs 0 and lse = -inf; a row
+ * with a NaN score is NaN, lse included.
  */
 PKVQK_API pkvqk_status pkvqk_paged_decode_scored(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,
