@@ -709,8 +709,9 @@ def norm_rope_append_axes(q, k, v, positions, freq_axes, slot_mapping, gamma_q, 
     Tv, Hv, vs, vh = _heads(t, v, "v")
     if (To, Ho) != (T, Hq) or Tk != T or Tv != T or Hk != Hv or Hk != k_cache.shape[2]:
         raise ValueError("q, q_out, k and v must agree in tokens, and k, v and the cache in heads")
-    if positions.dtype is not t["i64"] or positions.dim() != 2 or positions.shape[1] != T \
-            or (T > 1 and positions.stride(1) != 1):
+    shape, ps = positions.shape, positions.stride()
+    if positions.dtype is not t["i64"] or len(shape) != 2 or shape[1] != T \
+            or (T > 1 and ps[1] != 1):
         raise ValueError("positions must be int64 [axes, tokens], the tokens contiguous")
     if len(freq_axes) != 64:
         raise ValueError("freq_axes must be 64 bytes")
@@ -719,7 +720,7 @@ def norm_rope_append_axes(q, k, v, positions, freq_axes, slot_mapping, gamma_q, 
         raise ValueError(f"rope_table must be contiguous and hold {table_positions} positions")
     check(_append_axes(
         q.data_ptr(), qs, qh, q_out.data_ptr(), os_, oh, k.data_ptr(), ks, kh,
-        v.data_ptr(), vs, vh, positions.data_ptr(), positions.stride(0), positions.shape[0],
+        v.data_ptr(), vs, vh, positions.data_ptr(), ps[0], shape[0],
         bytes(freq_axes), _ints(slot_mapping, t["i64"], T, "slot_mapping"),
         _gains(t, gamma_q, "gamma_q"), _gains(t, gamma_k, "gamma_k"), theta, eps, T, Hq,
         k_cache.data_ptr(), v_cache.data_ptr(), _pack_layout(t, k_cache, v_cache),
@@ -737,6 +738,8 @@ _paged_prefill_varlen_scored = _fast("pkvqk_paged_prefill_varlen_scored",
 
 
 def _pack_rules(t, softcap, window, slopes, first_keys, prefix_lens, rows, batch, heads):
+    if slopes is None and first_keys is None and prefix_lens is None:
+        return _RULES_PACK.pack(softcap, window, 0, 0, 0)
     return _RULES_PACK.pack(
         softcap, window,
         0 if slopes is None else _ints(slopes, t["f32"], heads, "slopes"),
@@ -813,10 +816,11 @@ def paged_prefill_varlen_scored(q, cu_seqlens_q, max_q_len, k_cache, v_cache, bl
 
 def _rows_of(x, batch, rows, vocab, name):
     """Strides of a [batch, >= rows, vocab] view whose rows are contiguous."""
-    if x.dim() != 3 or x.shape[0] != batch or x.shape[1] < rows or x.shape[2] != vocab \
-            or (vocab > 1 and x.stride(2) != 1):
+    shape, st = x.shape, x.stride()
+    if len(shape) != 3 or shape[0] != batch or shape[1] < rows or shape[2] != vocab \
+            or (vocab > 1 and st[2] != 1):
         raise ValueError(f"{name} must be [batch, drafts, vocab], the vocabulary contiguous")
-    return x.stride(0), x.stride(1)
+    return st[0], st[1]
 
 
 def verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, tokens, num_accepted, *,
