@@ -162,7 +162,8 @@ def kernel_src_hash():
     import hashlib
     csrc = os.path.join(ROOT, "paged_kv_cache_qk_gb300", "csrc")
     parts = []
-    for f in ("decode.cu", "decode_schedule.cuh", "device_common.cuh", "kernels.h", "api.cu"):
+    for f in ("decode_kernel.cuh", "decode.cu", "decode_schedule.cuh", "score_rules.cuh",
+              "device_common.cuh", "kernels.h", "api.cu"):
         with open(os.path.join(csrc, f), "rb") as fh:
             parts.append(hashlib.sha256(fh.read()).hexdigest())
     return hashlib.sha256("".join(parts).encode()).hexdigest()[:16]
