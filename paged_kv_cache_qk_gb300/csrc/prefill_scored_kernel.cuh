@@ -21,7 +21,7 @@
 // memory, not through Q's shared memory.  A CTA a place, and this: 16 ragged prompts of
 // documents 72 and 62 us, fresh 4 x 2048 under a cap 86 and 84, 19 x 512 in a window of 4096
 // 353 and 352.  With every SM's places fixed beforehand in place of taken: 78, 82, 351.
-// (Since then the cap costs less: 62, 82, 297.)
+// (Since then the cap costs less: 62, 79, 286.)
 //
 // Key tiles of 64 with two score buffers a row tile, so that the next scores are there when
 // a row tile's warps are done with the last, were slower: the scores of 64 keys cost the tensor
@@ -177,6 +177,7 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
   const int oob = static_cast<int>(a.num_blocks);   // past the extent: TMA fills zeros
   Job cur, nxt;
   int asked = 0;                               // answers had
+  bool due = false;                            // one is on its way
   bool ok = true;
   // page id of box `lane` of a place's key tile i, when the box holds a visible key; loaded
   // ahead of its use
@@ -196,9 +197,11 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
     while (true) {
       if (lane == 0) ask_next(bars);
       __syncwarp();
+      due = true;
       ok = mbar_wait(&bars->next_full, asked & 1);
       ok = __all_sync(0xffffffffu, ok);
       if (!ok) return false;
+      due = false;
       ++asked;
       const bool got = read_next(bars, bx, by);
       __syncwarp();
@@ -314,6 +317,7 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
   if (!ok && lane == 0) {
     bars->abort = 1;
     report(a.status_flags, kFlagTimeout);
+    if (due) mbar_wait(&bars->next_full, asked & 1);       // it lands before the CTA leaves
   }
   __syncwarp();
   *issued_out = issued;
@@ -415,60 +419,45 @@ __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* ba
 
 // --------------------------------------------------------------- softmax
 
-// add + cap * tanh(k v) of 32 raw scores, k = scale / softcap: two at a time by the polynomial
-// that the largest of the warp's scores allows, or one by one.  Degree 3 has k and the
-// cap in its coefficients, v R(v^2): five packed instructions a pair.  That holds for
-// kSmallestK <= k <= kLargestK, where cap k^7, the last of them, neither under- nor overflows
-// (caps are 2^-20 .. 2^20 of the scores' own); another k takes degree 5.
+// add + cap * tanh(k v) of 32 raw scores, k = scale / softcap, in packed pairs.  The polynomial
+// has the cap in its coefficients and, for kSmallestK <= k <= kLargestK, k too: v R(v^2) is
+// then five instructions a pair (cap k^7, the last coefficient, neither under- nor overflows:
+// caps are 2^-20 .. 2^20 of the scores' own); another k is multiplied first.
 constexpr float kSmallestK = 0x1p-16f, kLargestK = 0x1p14f;
 
-__device__ __forceinline__ void cap_pairs_3(float (&v)[32], float k, float cap, float add) {
-  uint64_t c[4];
-  float f = cap * k;
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    c[i] = pack2(f * tanh_q<3>(i), f * tanh_q<3>(i));
-    f *= k * k;
-  }
-  const uint64_t add2_ = pack2(add, add);
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    const uint64_t x = pack2(v[e], v[e + 1]), u = mul2(x, x);
-    unpack2(fma2(x, fma2(fma2(fma2(c[3], u, c[2]), u, c[1]), u, c[0]), add2_), v[e], v[e + 1]);
-  }
-}
-__device__ __forceinline__ void cap_pairs_5(float (&v)[32], float k, float cap, float add) {
-  const uint64_t k2 = pack2(k, k), add2_ = pack2(add, add);
-  uint64_t c[6];                               // the cap is in the coefficients
-#pragma unroll
-  for (int i = 0; i < 6; ++i) c[i] = pack2(cap * tanh_q<5>(i), cap * tanh_q<5>(i));
-#pragma unroll
-  for (int e = 0; e < 32; e += 2) {
-    const uint64_t x = mul2(pack2(v[e], v[e + 1]), k2);
-    const uint64_t u = mul2(x, x);
-    uint64_t q = c[5];
-#pragma unroll
-    for (int i = 4; i >= 0; --i) q = fma2(q, u, c[i]);
-    unpack2(fma2(x, q, add2_), v[e], v[e + 1]);
-  }
-}
 __device__ __forceinline__ void cap_chunk(float (&v)[32], float k, float cap, float add) {
-  // the largest |v| decides; a NaN that is masked later does not count
+  // the largest |v| decides what is computed; a NaN that is masked later does not count
   float b4[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
   for (int e = 0; e < 32; e += 2)
     b4[(e >> 1) & 3] = max3(b4[(e >> 1) & 3], fabsf(v[e]), fabsf(v[e + 1]));
   const float big = max3(b4[0], b4[1], fmaxf(b4[2], b4[3])) * k;
-  const float small = k >= kSmallestK && k <= kLargestK ? kTanhSmall : -1.f;
-  if (!__any_sync(0xffffffffu, big * big > small)) {
-    cap_pairs_3(v, k, cap, add);
-  } else if (!__any_sync(0xffffffffu, big * big > kTanhSquare)) {
-    cap_pairs_5(v, k, cap, add);
-  } else {
+  const bool folded = k >= kSmallestK && k <= kLargestK;
+  const float inner = folded ? k : 1.f;
+  uint64_t c[4];
+  float f = cap * inner;
 #pragma unroll
-    for (int e = 0; e < 32; ++e) {
-      const float x = v[e] * k, u = x * x;
-      v[e] = fmaf(cap, u <= kTanhSquare ? tanh_near(x, u) : tanh_far(x), add);
+  for (int i = 0; i < 4; ++i) {
+    c[i] = pack2(f * tanh_q(i), f * tanh_q(i));
+    f *= inner * inner;
+  }
+  const uint64_t add2_ = pack2(add, add);
+  auto near = [&](uint64_t x) {
+    const uint64_t u = mul2(x, x);
+    return fma2(x, fma2(fma2(fma2(c[3], u, c[2]), u, c[1]), u, c[0]), add2_);
+  };
+  if (folded && !__any_sync(0xffffffffu, big * big > kTanhSquare)) {
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) unpack2(near(pack2(v[e], v[e + 1])), v[e], v[e + 1]);
+  } else {
+    const float outer = folded ? 1.f : k;      // exact where k is folded: the same bits
+    const uint64_t outer2 = pack2(outer, outer);
+#pragma unroll
+    for (int e = 0; e < 32; e += 2) {
+      const float x0 = v[e] * k, x1 = v[e + 1] * k;
+      unpack2(near(mul2(pack2(v[e], v[e + 1]), outer2)), v[e], v[e + 1]);
+      if (!(x0 * x0 <= kTanhSquare)) v[e] = fmaf(cap, tanh_far(x0), add);
+      if (!(x1 * x1 <= kTanhSquare)) v[e + 1] = fmaf(cap, tanh_far(x1), add);
     }
   }
 }

@@ -10,12 +10,12 @@
 // interval of keys.  Scores are kept in units of log2(e), so that the softmax's 2^x takes
 // them as they are.
 //
-// tanh without cancellation: x Q(x^2), Q fitted to tanh(x) / x at Chebyshev nodes: of
-// degree 5 up to |x| = 0.75 (largest relative error 3.0e-8, 1.0e-7 evaluated in fp32), of
-// degree 3 up to 0.5 (5.5e-7, 5.9e-7), which takes no special-function unit; beyond,
-// 1 - 2 / (1 + e^2x), whose absolute error of ~1.2e-7 is relative there.  The units'
-// exponentials and reciprocals are what the softmax itself is short of, so a warp computes
-// the last form only where one of its scores is that large.
+// tanh without cancellation: up to |x| = 0.5 x Q(x^2), Q of degree 3 fitted to tanh(x) / x at
+// Chebyshev nodes (largest relative error 5.5e-7, 5.9e-7 evaluated in fp32), which takes no
+// special-function unit; beyond, 1 - 2 / (1 + e^2x), whose absolute error of ~1.2e-7 is
+// 2.6e-7 of the value at most there.  A score's own size decides which it gets, so that no
+// row's bits depend on another's; a warp computes the second form only where one of its
+// scores needs it (exponentials and reciprocals are what the softmax itself is short of).
 #pragma once
 
 #include "device_common.cuh"
@@ -23,20 +23,9 @@
 
 namespace pkvqk {
 
-constexpr float kTanhSquare = 0.5625f;         // x^2 up to which the polynomials serve:
-constexpr float kTanhSmall = 0.25f;            // of degree 3, above it of degree 5
-
-// Coefficient i of the polynomial of the given degree.
-template <int kDegree>
+constexpr float kTanhSquare = 0.25f;           // x^2 up to which the polynomial serves
 __device__ __forceinline__ constexpr float tanh_q(int i) {
-  if (kDegree == 3)
-    return i == 0 ? 0.999999464f : i == 1 ? -0.333263755f : i == 2 ? 0.131909117f : -0.0444185808f;
-  return i == 0   ? 1.0f
-         : i == 1 ? -0.33332968f
-         : i == 2 ? 0.13325515f
-         : i == 3 ? -0.05334982f
-         : i == 4 ? 0.019593786f
-                  : -0.004723952f;
+  return i == 0 ? 0.99999946f : i == 1 ? -0.33326375f : i == 2 ? 0.13190912f : -0.04441858f;
 }
 
 // 1 - 2 / (1 + e^(2 x)), e^(2 x) = 2^(2 log2(e) x)
@@ -47,44 +36,30 @@ __device__ __forceinline__ float tanh_far(float x) {
   return fmaf(-2.f, r, 1.f);
 }
 
-__device__ __forceinline__ float tanh_near(float x, float u) {
-  float q = tanh_q<5>(5);
-#pragma unroll
-  for (int i = 4; i >= 0; --i) q = fmaf(q, u, tanh_q<5>(i));
-  return q * x;
-}
-
 // N scores (pairs of them) of every lane of a warp capped in place.
-template <int kDegree, int N>
-__device__ __forceinline__ void cap_near(const ScoreRules& r, float (&z)[N]) {
+template <int N>
+__device__ __forceinline__ void cap_scores(const ScoreRules& r, float (&z)[N]) {
+  // the largest |score| decides what is computed; a NaN that is hidden later does not count
+  float big = 0.f;
+#pragma unroll
+  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(z[i]));
+  big *= r.inv_cap;
+  const bool far = __any_sync(0xffffffffu, big * big > kTanhSquare);
   const uint64_t inv2 = pack2(r.inv_cap, r.inv_cap), cap2 = pack2(r.cap, r.cap);
 #pragma unroll
   for (int i = 0; i < N; i += 2) {
     const uint64_t x = mul2(pack2(z[i], z[i + 1]), inv2);
     const uint64_t u = mul2(x, x);
-    uint64_t q = pack2(tanh_q<kDegree>(kDegree), tanh_q<kDegree>(kDegree));
+    uint64_t q = pack2(tanh_q(3), tanh_q(3));
 #pragma unroll
-    for (int k = kDegree - 1; k >= 0; --k)
-      q = fma2(q, u, pack2(tanh_q<kDegree>(k), tanh_q<kDegree>(k)));
+    for (int k = 2; k >= 0; --k) q = fma2(q, u, pack2(tanh_q(k), tanh_q(k)));
     unpack2(mul2(mul2(x, cap2), q), z[i], z[i + 1]);
-  }
-}
-template <int N>
-__device__ __forceinline__ void cap_scores(const ScoreRules& r, float (&z)[N]) {
-  // the largest |score| decides; a NaN that is hidden later does not count
-  float big = 0.f;
-#pragma unroll
-  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(z[i]));
-  big *= r.inv_cap;
-  if (!__any_sync(0xffffffffu, big * big > kTanhSmall)) {
-    cap_near<3>(r, z);
-  } else if (!__any_sync(0xffffffffu, big * big > kTanhSquare)) {
-    cap_near<5>(r, z);
-  } else {
-#pragma unroll
-    for (int i = 0; i < N; ++i) {
-      const float x = z[i] * r.inv_cap, u = x * x;
-      z[i] = r.cap * (u <= kTanhSquare ? tanh_near(x, u) : tanh_far(x));
+    if (far) {
+      float x0, x1, u0, u1;
+      unpack2(x, x0, x1);
+      unpack2(u, u0, u1);
+      if (!(u0 <= kTanhSquare)) z[i] = r.cap * tanh_far(x0);
+      if (!(u1 <= kTanhSquare)) z[i + 1] = r.cap * tanh_far(x1);
     }
   }
 }

@@ -450,6 +450,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
       s_bad_token = bad_token;
     }
   }
+  __syncwarp();
   cluster_wait();
   __syncthreads();
   const int j = s_kept, n = s_drafts;
