@@ -157,6 +157,7 @@ __device__ void consume_simt(const DecodeArgs& a, const Plan* plan, const uint8_
   const int kg = lane >> 3;        // key group: key 4*q4 + kg of the tile
   const int p = lane & 7;          // 16-byte chunk p of each 64-dim half
 
+  const float factor = kScored ? score_factor(a.rules, a.scale_log2) : a.scale_log2;
   SegmentSourceOf<kScored> src;
   src.init(a, plan, TK);
   Segment seg;
@@ -179,7 +180,7 @@ __device__ void consume_simt(const DecodeArgs& a, const Plan* plan, const uint8_
       unpack8(u1, qf[rr] + 8);
 #pragma unroll
       for (int j = 0; j < 16; ++j) {
-        qf[rr][j] *= a.scale_log2;
+        qf[rr][j] *= factor;
         acc[rr][j] = 0.f;
       }
       m[rr] = -INFINITY;
@@ -423,6 +424,7 @@ __device__ void consume_tc(const DecodeArgs& a, const Plan* plan, const uint8_t*
   const int mat = lane >> 3;       // which 8x8 matrix this lane addresses in ldmatrix.x4
   const int mrow = lane & 7;
 
+  const float factor = kScored ? score_factor(a.rules, a.scale_log2) : a.scale_log2;
   SegmentSourceOf<kScored> src;
   src.init(a, plan, TK);
   Segment seg;
@@ -526,7 +528,7 @@ __device__ void consume_tc(const DecodeArgs& a, const Plan* plan, const uint8_t*
       } else {
         float z[8];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) z[e] = sc[e >> 2][e & 3] * a.scale_log2;
+        for (int e = 0; e < 8; ++e) z[e] = sc[e >> 2][e & 3] * factor;
         if (a.rules.cap > 0.f) cap_scores(a.rules, z);
         // element e: key key0 + 8 (e / 4) + 2 c + e % 2, row A (e % 4 < 2) or B
         if (a.rules.slopes != nullptr) {

@@ -106,7 +106,7 @@ __device__ __forceinline__ void ask_next(ScoredBars* bars) {
 
 // The answer: whether there was one, and its place.
 __device__ __forceinline__ bool read_next(const ScoredBars* bars, int& bx, int& by) {
-  uint32_t x, y, z, got;
+  uint32_t x, y, z, got;                       // the grid has one z
   asm volatile(
       "{\n\t.reg .pred p;\n\t.reg .b128 r;\n\t"
       "ld.shared.b128 r, [%4];\n\t"
@@ -117,10 +117,9 @@ __device__ __forceinline__ bool read_next(const ScoredBars* bars, int& bx, int& 
       : "=r"(x), "=r"(y), "=r"(z), "=r"(got)
       : "r"(smem_addr(&bars->next))
       : "memory");
-  (void)z;
   bx = static_cast<int>(x);
   by = static_cast<int>(y);
-  return got != 0;
+  return got != 0 && z == 0;
 }
 
 // The place's rows and keys (one warp, all lanes); its tokens' first keys go to first_keys.

@@ -36,30 +36,37 @@ __device__ __forceinline__ float tanh_far(float x) {
   return fmaf(-2.f, r, 1.f);
 }
 
-// N scores (pairs of them) of every lane of a warp capped in place.
+// What raw scores are multiplied by: to log2 units, or to units of the cap.
+__device__ __forceinline__ float score_factor(const ScoreRules& r, float scale_log2) {
+  return r.cap > 0.f ? scale_log2 * r.inv_cap : scale_log2;
+}
+
+// N scores (pairs of them) of every lane of a warp, in units of the cap, to capped ones.
 template <int N>
-__device__ __forceinline__ void cap_scores(const ScoreRules& r, float (&z)[N]) {
+__device__ __forceinline__ void cap_scores(const ScoreRules& r, float (&x)[N]) {
   // the largest |score| decides what is computed; a NaN that is hidden later does not count
   float big = 0.f;
 #pragma unroll
-  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(z[i]));
-  big *= r.inv_cap;
+  for (int i = 0; i < N; ++i) big = fmaxf(big, fabsf(x[i]));
   const bool far = __any_sync(0xffffffffu, big * big > kTanhSquare);
-  const uint64_t inv2 = pack2(r.inv_cap, r.inv_cap), cap2 = pack2(r.cap, r.cap);
-#pragma unroll
-  for (int i = 0; i < N; i += 2) {
-    const uint64_t x = mul2(pack2(z[i], z[i + 1]), inv2);
-    const uint64_t u = mul2(x, x);
+  const uint64_t cap2 = pack2(r.cap, r.cap);
+  auto near = [&](uint64_t z) {
+    const uint64_t u = mul2(z, z);
     uint64_t q = pack2(tanh_q(3), tanh_q(3));
 #pragma unroll
     for (int k = 2; k >= 0; --k) q = fma2(q, u, pack2(tanh_q(k), tanh_q(k)));
-    unpack2(mul2(mul2(x, cap2), q), z[i], z[i + 1]);
-    if (far) {
-      float x0, x1, u0, u1;
-      unpack2(x, x0, x1);
-      unpack2(u, u0, u1);
-      if (!(u0 <= kTanhSquare)) z[i] = r.cap * tanh_far(x0);
-      if (!(u1 <= kTanhSquare)) z[i + 1] = r.cap * tanh_far(x1);
+    return mul2(mul2(z, cap2), q);
+  };
+  if (!far) {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) unpack2(near(pack2(x[i], x[i + 1])), x[i], x[i + 1]);
+  } else {
+#pragma unroll
+    for (int i = 0; i < N; i += 2) {
+      const float x0 = x[i], x1 = x[i + 1];
+      unpack2(near(pack2(x0, x1)), x[i], x[i + 1]);
+      if (!(x0 * x0 <= kTanhSquare)) x[i] = r.cap * tanh_far(x0);
+      if (!(x1 * x1 <= kTanhSquare)) x[i + 1] = r.cap * tanh_far(x1);
     }
   }
 }
