@@ -21,7 +21,14 @@
 // memory, not through Q's shared memory.  A CTA a place, and this: 16 ragged prompts of
 // documents 72 and 62 us, fresh 4 x 2048 under a cap 86 and 84, 19 x 512 in a window of 4096
 // 353 and 352.  With every SM's places fixed beforehand in place of taken: 78, 82, 351.
-// (Since then the cap costs less: 62, 79, 286.)
+// (Since then the cap costs less, and the code is smaller: 51, 71, 279.)
+//
+// Code.  The roles run different code at the same time, and a place's set-up and output run
+// once in dozens of microseconds: what they lose to fetching instructions is no small part.
+// So loops over a tile's chunks, the two row tiles and the output's halves are not unrolled,
+// and each product, each place's reading and, without a cap or a bias, each softmax exists
+// once.  Documents, fresh 4 x 2048 and the window above: 61.6, 79.3 and 285 us unrolled, 53.2,
+// 72.6 and 280 so; warps waited for instructions 1.9 cycles an instruction (documents).
 //
 // Key tiles of 64 with two score buffers a row tile, so that the next scores are there when
 // a row tile's warps are done with the last, were slower: the scores of 64 keys cost the tensor
@@ -174,7 +181,7 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
   const int lane = threadIdx.x & 31;
   const int bs = a.block_size, tbs = box_shift(bs), tb = 1 << tbs, ppt = kN >> tbs;
   const int oob = static_cast<int>(a.num_blocks);   // past the extent: TMA fills zeros
-  Job cur, nxt;
+  Job cur{};
   int asked = 0;                               // answers had
   bool due = false;                            // one is on its way
   bool ok = true;
@@ -188,23 +195,27 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
     return i < w.ntiles && box_visible(w, i) ? __ldg(bt + (w.k0 + i * kN + lane * tb) / bs) : oob;
   };
   int jobs = 0, it = 0, issued = 0;            // places handed out, key tiles asked for
-  // the next place that has rows; false: none is left, or a wait gave up.  Its
-  // first keys' slot is that of the place before the current one, whose rows have left it
-  // once job_empty says so.
+  // the next place that has rows, the CTA's own first; false: none is left, or a wait gave
+  // up.  Its first keys' slot is that of the place before the current one, whose rows have left
+  // it once job_empty says so.
+  bool own = true;
   auto next_place = [&](Job& job) {
-    int bx, by;
+    int bx = blockIdx.x, by = blockIdx.y;
     while (true) {
-      if (lane == 0) ask_next(bars);
-      __syncwarp();
-      due = true;
-      ok = mbar_wait(&bars->next_full, asked & 1);
-      ok = __all_sync(0xffffffffu, ok);
-      if (!ok) return false;
-      due = false;
-      ++asked;
-      const bool got = read_next(bars, bx, by);
-      __syncwarp();
-      if (!got) return false;
+      if (!own) {
+        if (lane == 0) ask_next(bars);
+        __syncwarp();
+        due = true;
+        ok = mbar_wait(&bars->next_full, asked & 1);
+        ok = __all_sync(0xffffffffu, ok);
+        if (!ok) return false;
+        due = false;
+        ++asked;
+        const bool got = read_next(bars, bx, by);
+        __syncwarp();
+        if (!got) return false;
+      }
+      own = false;
       if (jobs >= kJobs) {
         ok = mbar_wait(&bars->job_empty[jobs % kJobs], (jobs / kJobs - 1) & 1);
         ok = __all_sync(0xffffffffu, ok);
@@ -213,9 +224,6 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
       if (make_job(a, bx, by, first_keys + (jobs % kJobs) * kJobTokens, job)) return true;
     }
   };
-  bool have = make_job(a, blockIdx.x, blockIdx.y, first_keys, cur);
-  if (!have) have = next_place(cur);
-  int id_first = have ? page_id(cur.w, 0) : oob;
   int q_issued[2] = {0, 0};
   auto wait_here = [&](uint64_t* bar, uint32_t parity) {
     bool w = true;
@@ -234,13 +242,15 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
     ++q_issued[x];
     return true;
   };
-  while (ok && have) {
+#pragma unroll 1
+  while (true) {
+    // The next place is asked for only here, while the row tiles still work on what the ring
+    // holds: places are few, and one that is taken early waits while another SM could have
+    // it (16 ragged prompts 68 us asked for at the third key tile, 62 here, with CTAs as they were).
+    if (!next_place(cur)) break;
     const Work& w = cur.w;
+    const int id_first = page_id(w, 0);
     const int slot = jobs % kJobs;
-    if (jobs >= kJobs && !wait_here(&bars->job_empty[slot], (jobs / kJobs - 1) & 1)) {
-      ok = false;
-      break;
-    }
     cur.first_tile = it;
     if (lane == 0) {
       bars->job[slot] = cur;
@@ -297,12 +307,6 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
       issued = it + 1;
     }
     if (!ok) break;
-    // The next place is asked for only here, while the row tiles still work on what the ring
-    // holds: places are few, and one that is taken early waits while another SM could have
-    // it (16 ragged prompts 68 us asked for at the third key tile, 62 here).
-    have = next_place(nxt);
-    if (have) id_first = page_id(nxt.w, 0);
-    cur = nxt;
   }
   // no place any more: a job without a row tile ends the other roles
   if (ok) {
@@ -340,7 +344,7 @@ __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* ba
   uint32_t v_step[kN / 16];
 #pragma unroll
   for (int ks = 0; ks < kN / 16; ++ks) v_step[ks] = v_step_offset(ks, tbs) >> 4;
-  uint32_t p_uses[2] = {0, 0}, q_uses[2] = {0, 0};
+  uint32_t p_uses = 0, q_uses = 0;             // bit x: parity of tile x's next use
   bool ok = true;
   for (int jobs = 0; ok; ++jobs) {
     const int slot = jobs % kJobs;
@@ -378,33 +382,25 @@ __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* ba
       if (i == n - 1) tc5::commit(&bars->pv_done[x]);
       if (x == last) tc5::commit(&bars->empty_v[s]);
     };
-    auto wait_q = [&](int x) { return mbar_wait(&bars->q_full[x], q_uses[x]++ & 1); };
-    auto wait_p = [&](int x) { return mbar_wait(&bars->p_full[x], p_uses[x]++ & 1); };
-    ok = wait_q(0) && mbar_wait(&bars->full_k[it0 & 1], (it0 >> 1) & 1);
-    if (!ok) break;
-    tc5::fence_after_sync();
-    mma_s(0, 0);
-    if (has_b) {
-      ok = wait_q(1);
-      if (!ok) break;
-      tc5::fence_after_sync();
-      mma_s(1, 0);
-    }
-    for (int i = 0; i < n && ok; ++i) {
+    auto wait_use = [&](uint64_t* bar, uint32_t& uses, int x) {
+      const uint32_t parity = uses >> x & 1;
+      uses ^= 1u << x;
+      return mbar_wait(bar + x, parity);
+    };
+    // turn i of row tile x: its product with key tile i, then the scores of key tile i + 1;
+    // turn -1: the first scores
+#pragma unroll 1
+    for (int i = -1; i < n && ok; ++i) {
       const int it = it0 + i;
-      ok = mbar_wait(&bars->full_v[it & 1], (it >> 1) & 1);
+      if (i >= 0) ok = mbar_wait(&bars->full_v[it & 1], (it >> 1) & 1);
       if (ok && i + 1 < n) ok = mbar_wait(&bars->full_k[(it + 1) & 1], ((it + 1) >> 1) & 1);
-      if (ok) ok = wait_p(0);
-      if (!ok) break;
-      tc5::fence_after_sync();
-      mma_pv(0, i);
-      if (i + 1 < n) mma_s(0, i + 1);
-      if (has_b) {
-        ok = wait_p(1);
+#pragma unroll 1
+      for (int x = 0; x <= last && ok; ++x) {
+        ok = i < 0 ? wait_use(bars->q_full, q_uses, x) : wait_use(bars->p_full, p_uses, x);
         if (!ok) break;
         tc5::fence_after_sync();
-        mma_pv(1, i);
-        if (i + 1 < n) mma_s(1, i + 1);
+        if (i >= 0) mma_pv(x, i);
+        if (i + 1 < n) mma_s(x, i + 1);
       }
     }
   }
@@ -493,7 +489,7 @@ __device__ __forceinline__ float bounded_half_tile(uint32_t scol, uint32_t pcol,
   uint64_t acc[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) acc[j] = pack2(0.f, 0.f);
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     float v[32];
     tc5::tmem_ld32(scol + c * 32, v);
@@ -526,7 +522,7 @@ __device__ __forceinline__ float scored_half_tile(uint32_t scol, uint32_t pcol, 
                                                   float slope, int at, float& m_ref,
                                                   Publish&& publish) {
   float psum = 0.f;
-#pragma unroll
+#pragma unroll 1
   for (int c = 0; c < 2; ++c) {
     float v[32];
     tc5::tmem_ld32(scol + c * 32, v);
@@ -614,6 +610,28 @@ __device__ __forceinline__ void store_words(void* to, const uint32_t (&v)[8]) {
   }
 }
 
+// 64 bytes of each lane's row (none where `to` is null).  A lane's own bytes in its own row
+// leave the SM a sector at a time; two lanes exchange 32 bytes and write their rows one after
+// the other, 64 bytes together (16 ragged prompts of documents 53.3 -> 51.3 us, fresh 4 x 2048
+// 72.9 -> 71.2; four lanes and 128 bytes, with three times the exchanges: 52.0, 72.0).
+__device__ __forceinline__ void store_rows64(uint32_t (&v)[16], uint8_t* to) {
+  const bool odd = (threadIdx.x & 1) != 0;
+  uint32_t w[2][8];
+#pragma unroll
+  for (int k = 0; k < 8; ++k) {
+    const uint32_t got = __shfl_xor_sync(0xffffffffu, odd ? v[k] : v[8 + k], 1);
+    w[0][k] = odd ? got : v[k];                // of the even lane's row
+    w[1][k] = odd ? v[8 + k] : got;            // of the odd lane's
+  }
+  const unsigned long long mine = reinterpret_cast<unsigned long long>(to);
+  const unsigned long long other = __shfl_xor_sync(0xffffffffu, mine, 1);
+#pragma unroll
+  for (int p = 0; p < 2; ++p) {
+    uint8_t* row = reinterpret_cast<uint8_t*>((p != 0) == odd ? mine : other);
+    if (row != nullptr) store_words(row + (odd ? 32 : 0), w[p]);
+  }
+}
+
 // This thread's half of an output row of tile x: O / l for dims 64h .. 64h + 63 (bf16, or
 // the fp32 partial of the split), and the log-sum-exp (half 0).  Every lane of the warp
 // takes part in the loads from tensor memory.
@@ -641,25 +659,21 @@ __device__ __forceinline__ void write_scored_rows(const PrefillArgs& a, const Wo
     }
 #pragma unroll
     for (int e = 0; e < 32; ++e) o[e] = have_o ? o[e] * inv : 0.f;
-    if (!valid) continue;
     if (split) {
-      float* to = a.ws_o + prow * kHeadDim + d0 + c * 32;
-#pragma unroll
-      for (int e = 0; e < 32; e += 8) {
-        uint32_t v[8];
-#pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = __float_as_uint(o[e + k]);
-        store_words(to + e, v);
-      }
-    } else {
-      __nv_bfloat16* to = a.out + row * kHeadDim + d0 + c * 32;
+      uint8_t* to = reinterpret_cast<uint8_t*>(a.ws_o + prow * kHeadDim + d0 + c * 32);
 #pragma unroll
       for (int e = 0; e < 32; e += 16) {
-        uint32_t v[8];
+        uint32_t v[16];
 #pragma unroll
-        for (int k = 0; k < 8; ++k) v[k] = pack_bf16x2(o[e + 2 * k], o[e + 2 * k + 1]);
-        store_words(to + e, v);
+        for (int k = 0; k < 16; ++k) v[k] = __float_as_uint(o[e + k]);
+        store_rows64(v, valid ? to + e * 4 : nullptr);
       }
+    } else {
+      uint32_t v[16];
+#pragma unroll
+      for (int k = 0; k < 16; ++k) v[k] = pack_bf16x2(o[2 * k], o[2 * k + 1]);
+      store_rows64(v, valid ? reinterpret_cast<uint8_t*>(a.out + row * kHeadDim + d0 + c * 32)
+                            : nullptr);
     }
   }
   if (valid && half == 0) {
@@ -763,7 +777,7 @@ __device__ __forceinline__ bool softmax_place(const PrefillArgs& a, const Job& j
                    : bounded_half_tile<true>(s_cols, s_cols, half * (kN / 2), lo - kb, nvis, k,
                                              a.rules.cap, m_ref);
     } else {
-      psum = whole ? scored_half_tile<kRules, false>(s_cols, s_cols, half * (kN / 2), 0, nvis, sl2,
+      psum = kRules != kRuleIntervals && whole ? scored_half_tile<kRules, false>(s_cols, s_cols, half * (kN / 2), 0, nvis, sl2,
                                                      a.rules, slope, kb - pos, m_ref, publish)
                    : scored_half_tile<kRules, true>(s_cols, s_cols, half * (kN / 2), lo - kb, nvis,
                                                     sl2, a.rules, slope, kb - pos, m_ref, publish);
