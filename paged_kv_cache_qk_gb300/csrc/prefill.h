@@ -43,7 +43,7 @@ struct PrefillArgs {
   int32_t q_tma, o_tma;
   // set by launch_paged_prefill: the grid runs over (row tile descending,
   // sequence, kv head, split) instead of (sequence, split, kv head, row tile
-  // descending)
+  // descending); scored kernels: 2, over the row tiles that packed prompts have
   int32_t mt_major;
   int32_t group_shift;             // set by launch_paged_prefill: log2(group), or -1
   // 8-bit caches only

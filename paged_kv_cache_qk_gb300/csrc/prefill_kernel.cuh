@@ -230,8 +230,21 @@ struct Work {
   bool has_b;    // row tile B holds rows
 };
 
-// What the place (bx, by) in the grid and the row offsets say; L is the sequence's length
-// as read.
+// What the row offsets say of the place's sequence; L is its length as read.
+__device__ __forceinline__ void read_place(const PrefillArgs& a, Work& w) {
+  w.L = a.seq_lens[w.b];
+  if (a.cu_seqlens_q != nullptr) {
+    const long long c0 = a.cu_seqlens_q[w.b], c1 = a.cu_seqlens_q[w.b + 1];
+    w.q0 = c0;
+    w.q_len = static_cast<int>(max(0ll, min(c1 - c0, static_cast<long long>(a.q_len))));
+  } else {
+    w.q0 = static_cast<long long>(w.b) * a.q_len;
+    w.q_len = a.q_len;
+  }
+  w.rows = w.q_len * a.group;
+}
+
+// What the place (bx, by) in the grid and the row offsets say.
 __device__ __forceinline__ Work place_work(const PrefillArgs& a, int bx, int by) {
   Work w;
   if (a.mt_major) {
@@ -255,16 +268,7 @@ __device__ __forceinline__ Work place_work(const PrefillArgs& a, int bx, int by)
     w.j = x / a.num_kv_heads;
     w.b = by;
   }
-  w.L = a.seq_lens[w.b];
-  if (a.cu_seqlens_q != nullptr) {
-    const long long c0 = a.cu_seqlens_q[w.b], c1 = a.cu_seqlens_q[w.b + 1];
-    w.q0 = c0;
-    w.q_len = static_cast<int>(max(0ll, min(c1 - c0, static_cast<long long>(a.q_len))));
-  } else {
-    w.q0 = static_cast<long long>(w.b) * a.q_len;
-    w.q_len = a.q_len;
-  }
-  w.rows = w.q_len * a.group;
+  read_place(a, w);
   return w;
 }
 

@@ -3,6 +3,7 @@
 #include "prefill_order.h"
 #include "prefill_scored_kernel.cuh"
 
+#include <algorithm>
 #include <cstring>
 
 namespace pkvqk {
@@ -25,14 +26,21 @@ cudaError_t launch_rules(const CUtensorMap& kmap, const CUtensorMap& vmap,
   const long long gx = static_cast<long long>(a.m_tiles) * a.num_kv_heads * a.num_splits;
   a.mt_major = row_tile_major(a.cu_seqlens_q != nullptr || 2ll * a.q_len >= a.longest, gx,
                               a.batch) ? 1 : 0;
+  dim3 grid(static_cast<unsigned>(gx), a.batch);
+  if (a.mt_major && a.cu_seqlens_q != nullptr && a.batch <= kPackedBatch) {
+    // at most this many row tiles of all sequences hold rows
+    const long long tiles = (a.total_q * a.group + (2ll * kM - 1) * a.batch) / (2 * kM);
+    a.mt_major = kPackedMajor;
+    grid = dim3(static_cast<unsigned>(std::min<long long>(
+        tiles * a.num_kv_heads * a.num_splits, gx * a.batch)));
+  }
   a.group_shift = -1;
   if (a.group > 0 && (a.group & (a.group - 1)) == 0)
     for (int s = 0; s < 31; ++s)
       if ((1 << s) == a.group) a.group_shift = s;
   a.q_tma = encode_rows_map(&qmap, a.q, a.total_q, a.num_q_heads, a.q_stride_h * 2,
                             a.q_stride_t * 2, a.group) ? 1 : 0;
-  return launch_pdl(kern, dim3(static_cast<unsigned>(gx), a.batch), dim3(kThreads),
-                    kScoredSmemBytes, stream, kmap, vmap, qmap, a);
+  return launch_pdl(kern, grid, dim3(kThreads), kScoredSmemBytes, stream, kmap, vmap, qmap, a);
 }
 
 }  // namespace

@@ -129,12 +129,69 @@ __device__ __forceinline__ bool read_next(const ScoredBars* bars, int& bx, int& 
   return got != 0 && z == 0;
 }
 
+// Packed prompts of different lengths: the grid's places are those of the row tiles there
+// are, every sequence's last first, in place of batch times the longest sequence's.  Place
+// `x`'s sequence and row tile (one warp, all lanes); false: past the last.
+constexpr int kPackedBatch = 128;              // sequences whose row tiles a warp counts at once
+constexpr int kPackedMajor = 2;                // PrefillArgs::mt_major
+__device__ __forceinline__ bool packed_place(const PrefillArgs& a, int x, Work& w) {
+  const int lane = threadIdx.x & 31;
+  const int per = a.num_kv_heads * a.num_splits;
+  int rank = x / per;
+  x -= rank * per;
+  w.g = x / a.num_splits;
+  w.j = x - w.g * a.num_splits;
+  int tiles[kPackedBatch / 32];                // row tiles of sequences lane, lane + 32, ...
+#pragma unroll
+  for (int k = 0; k < kPackedBatch / 32; ++k) {
+    const int b = k * 32 + lane;
+    tiles[k] = 0;
+    if (b >= a.batch) continue;
+    const long long c0 = a.cu_seqlens_q[b];
+    const long long c1 = min(static_cast<long long>(a.cu_seqlens_q[b + 1]),
+                             static_cast<long long>(a.total_q));
+    const int n = static_cast<int>(max(0ll, min(c1 - c0, static_cast<long long>(a.q_len))));
+    if (n > 0) tiles[k] = (n * a.group - 1) / (2 * kM) + 1;
+  }
+  auto from = [&](int mt) {                    // row tiles mt and later of all sequences
+    int n = 0;
+#pragma unroll
+    for (int k = 0; k < kPackedBatch / 32; ++k) n += max(0, tiles[k] - mt);
+    return __reduce_add_sync(0xffffffffu, n);
+  };
+  if (rank >= from(0)) return false;
+  int lo = 0, hi = a.m_tiles;                  // from(lo) > rank >= from(hi)
+#pragma unroll 1
+  while (hi - lo > 1) {
+    const int mid = (lo + hi) / 2;
+    if (from(mid) > rank) lo = mid;
+    else hi = mid;
+  }
+  w.mt = lo;
+  rank -= from(hi);                            // among the sequences that have this row tile
+  w.b = 0;
+#pragma unroll
+  for (int k = 0; k < kPackedBatch / 32; ++k) {
+    const uint32_t have = __ballot_sync(0xffffffffu, tiles[k] > lo);
+    const bool me = tiles[k] > lo && __popc(have & ((1u << lane) - 1)) == rank;
+    const uint32_t at = __ballot_sync(0xffffffffu, me);
+    if (at != 0) w.b = k * 32 + __ffs(at) - 1;
+    rank -= __popc(have);                      // below 0 from the sequence found on
+  }
+  return true;
+}
+
 // The place's rows and keys (one warp, all lanes); its tokens' first keys go to first_keys.
-// False: it has no rows (varlen grids cover the longest sequence).
+// False: it has no rows.
 __device__ __forceinline__ bool make_job(const PrefillArgs& a, int bx, int by, int* first_keys,
                                          Job& job) {
   Work& w = job.w;
-  w = place_work(a, bx, by);
+  if (a.mt_major == kPackedMajor) {
+    if (!packed_place(a, bx, w)) return false;
+    read_place(a, w);
+  } else {
+    w = place_work(a, bx, by);
+  }
   const int row0 = w.mt * 2 * kM;
   if (row0 >= w.rows) return false;
   const int prefix = a.rules.prefix_lens != nullptr ? a.rules.prefix_lens[w.b] : 0;
