@@ -21,14 +21,15 @@
 // memory, not through Q's shared memory.  A CTA a place, and this: 16 ragged prompts of
 // documents 72 and 62 us, fresh 4 x 2048 under a cap 86 and 84, 19 x 512 in a window of 4096
 // 353 and 352.  With every SM's places fixed beforehand in place of taken: 78, 82, 351.
-// (Since then the cap costs less, and the code is smaller: 51, 71, 279.)
+// (Since then the cap costs less, and the code is smaller: 50, 69, 269.)
 //
 // Code.  The roles run different code at the same time, and a place's set-up and output run
 // once in dozens of microseconds: what they lose to fetching instructions is no small part.
-// So loops over a tile's chunks, the two row tiles and the output's halves are not unrolled,
-// and each product, each place's reading and, without a cap or a bias, each softmax exists
-// once.  Documents, fresh 4 x 2048 and the window above: 61.6, 79.3 and 285 us unrolled, 53.2,
-// 72.6 and 280 so; warps waited for instructions 1.9 cycles an instruction (documents).
+// So loops over a tile's chunks and the output's halves are not unrolled, and the first
+// scores' issue, each place's reading and, without a cap or a bias, each softmax exists once.
+// Documents, fresh 4 x 2048 and the window above: 61.6, 79.3 and 285 us unrolled, 53.2, 72.6
+// and 280 so; warps waited 1.9 cycles an instruction for instructions before (documents),
+// 0.6 since.
 //
 // Key tiles of 64 with two score buffers a row tile, so that the next scores are there when
 // a row tile's warps are done with the last, were slower: the scores of 64 keys cost the tensor
@@ -303,7 +304,7 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
   while (true) {
     // The next place is asked for only here, while the row tiles still work on what the ring
     // holds: places are few, and one that is taken early waits while another SM could have
-    // it (16 ragged prompts 68 us asked for at the third key tile, 62 here, with CTAs as they were).
+    // it (16 ragged prompts took 68 us asked for at the third key tile, 62 here).
     if (!next_place(cur)) break;
     const Work& w = cur.w;
     const int id_first = page_id(w, 0);
@@ -387,6 +388,18 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
 
 // ------------------------------------------------------------ MMA issue
 
+// One lane of a converged warp.
+__device__ __forceinline__ bool elected() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+               : "=r"(p));
+  return p != 0;
+}
+
+// The whole warp walks the loop and one elected lane issues: operands of the matrix
+// instructions are then uniform values, where a loop of one lane alone had each moved over
+// before its instruction (19 x 512 in a window of 4096 279 -> 269 us, without the cap 268 ->
+// 248; fresh 4 x 2048 70.5 -> 68.9).
 __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* bars,
                              uint32_t tmem) {
   constexpr uint32_t idesc_s = tc5::idesc_bf16_f32(kM, kN, false);
@@ -402,14 +415,16 @@ __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* ba
 #pragma unroll
   for (int ks = 0; ks < kN / 16; ++ks) v_step[ks] = v_step_offset(ks, tbs) >> 4;
   uint32_t p_uses = 0, q_uses = 0;             // bit x: parity of tile x's next use
+  const bool lead = elected();
   bool ok = true;
   for (int jobs = 0; ok; ++jobs) {
     const int slot = jobs % kJobs;
-    ok = mbar_wait(&bars->job_full[slot], (jobs / kJobs) & 1);
+    ok = warp_wait(&bars->job_full[slot], (jobs / kJobs) & 1);
     if (!ok) break;
     const int n = bars->job[slot].w.ntiles, it0 = bars->job[slot].first_tile;
     const bool has_b = bars->job[slot].w.has_b;
-    mbar_arrive(&bars->job_empty[slot]);
+    __syncwarp();
+    if (lead) mbar_arrive(&bars->job_empty[slot]);
     if (n < 0) break;
     if (n == 0) continue;
     const int last = has_b ? 1 : 0;            // the row tile that reads a stage last
@@ -442,26 +457,30 @@ __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* ba
     auto wait_use = [&](uint64_t* bar, uint32_t& uses, int x) {
       const uint32_t parity = uses >> x & 1;
       uses ^= 1u << x;
-      return mbar_wait(bar + x, parity);
+      return warp_wait(bar + x, parity);
     };
     // turn i of row tile x: its product with key tile i, then the scores of key tile i + 1;
     // turn -1: the first scores
 #pragma unroll 1
     for (int i = -1; i < n && ok; ++i) {
       const int it = it0 + i;
-      if (i >= 0) ok = mbar_wait(&bars->full_v[it & 1], (it >> 1) & 1);
-      if (ok && i + 1 < n) ok = mbar_wait(&bars->full_k[(it + 1) & 1], ((it + 1) >> 1) & 1);
-#pragma unroll 1
-      for (int x = 0; x <= last && ok; ++x) {
+      if (i >= 0) ok = warp_wait(&bars->full_v[it & 1], (it >> 1) & 1);
+      if (ok && i + 1 < n) ok = warp_wait(&bars->full_k[(it + 1) & 1], ((it + 1) >> 1) & 1);
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        if (x > last || !ok) break;
         ok = i < 0 ? wait_use(bars->q_full, q_uses, x) : wait_use(bars->p_full, p_uses, x);
         if (!ok) break;
         tc5::fence_after_sync();
-        if (i >= 0) mma_pv(x, i);
-        if (i + 1 < n) mma_s(x, i + 1);
+        if (lead) {
+          if (i >= 0) mma_pv(x, i);
+          if (i + 1 < n) mma_s(x, i + 1);
+        }
+        __syncwarp();
       }
     }
   }
-  if (!ok) {
+  if (!ok && lead) {
     bars->abort = 1;
     report(a.status_flags, kFlagTimeout);
     tc5::commit(&bars->drain);                 // everything issued so far ...
@@ -996,7 +1015,7 @@ scored_prefill_kernel(const __grid_constant__ CUtensorMap kmap,
     }
     __syncwarp();
   } else {
-    if ((threadIdx.x & 31) == 0) issue_places(a, smem, bars, tmem);
+    issue_places(a, smem, bars, tmem);
     __syncwarp();
   }
   tc5::fence_before_sync();
