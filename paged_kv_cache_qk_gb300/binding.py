@@ -5,8 +5,10 @@ and C arguments (integers for pointers, ints, floats); the short-named
 helpers (``norm_rope_append``, ``paged_decode``, ``paged_prefill``,
 ``lse_combine``) take torch
 tensors, read their data pointers and strides and call the C entry point on
-the current CUDA stream.  All computation happens in the library's kernels;
-if ``libpkvqk.so`` is missing or fails to load, importing this module raises.
+the current CUDA stream; for the calls with axes, score rules and drafts
+``torch_calls.so`` does that natively.  All computation happens in the library's
+kernels; if ``libpkvqk.so`` is missing or fails to load, importing this module
+raises.
 """
 
 from __future__ import annotations
@@ -453,21 +455,16 @@ _ROPE_ROW_BYTES = pkvqk_rope_table_bytes(1)
 def _q8_names():
     torch = _torch()
     _q8.update(formats={torch.float8_e4m3fn: Q8_E4M3, torch.int8: Q8_INT8},
-               probs={torch.float32: PROB_FP32, torch.bfloat16: PROB_BF16,
-                      torch.float16: PROB_FP16},
                bf16=torch.bfloat16, f32=torch.float32, i32=torch.int32, i64=torch.int64,
                raw_stream=torch._C._cuda_getCurrentRawStream)
     return _q8
 
 
-_STRUCTS = (ctypes.POINTER(Q8Cache), ctypes.POINTER(CacheLayout), ctypes.POINTER(ScoreRules))
-
-
 def _fast(name, args):
-    """The entry point with its structs passed as packed bytes."""
+    """The entry point with the cache passed as packed bytes."""
     f = _lib[name]
     f.restype = ctypes.c_int
-    f.argtypes = [ctypes.c_char_p if a in _STRUCTS else a for a in args]
+    f.argtypes = [ctypes.c_char_p if a is ctypes.POINTER(Q8Cache) else a for a in args]
     return f
 
 
@@ -656,23 +653,21 @@ def paged_prefill_varlen_q8(q, cu_seqlens_q, max_q_len, k_cache, v_cache, k_scal
         _raw_stream(t, stream, q)))
 
 
-# ------------------------------------------------- positions of several axes
+# ------------------------------------- axes, score rules and drafted tokens
+#
+# The host side of these calls (types, shapes, strides, the current stream) is native
+# (csrc/torch_calls.cpp): it took 9 us of a call from here, as long as the kernels of a small
+# decode step, and takes 1 there.
 
-_LAYOUT_PACK = struct.Struct("=q4i3q")         # pkvqk_cache_layout, no padding
-assert _LAYOUT_PACK.size == ctypes.sizeof(CacheLayout)
-_append_axes = _fast("pkvqk_norm_rope_append_axes", pkvqk_norm_rope_append_axes.argtypes)
+_native = None
 
 
-def _pack_layout(t, k_cache, v_cache):
-    shape, st = k_cache.shape, k_cache.stride()
-    if k_cache.dtype is not t["bf16"] or v_cache.dtype is not t["bf16"]:
-        raise ValueError("k_cache and v_cache must be bfloat16")
-    if v_cache.stride() != st or v_cache.shape != shape:
-        raise ValueError("k_cache and v_cache must share one layout")
-    nb, bs, hkv, d = shape
-    if st[3] != 1:
-        raise ValueError("head_dim must be the contiguous axis")
-    return _LAYOUT_PACK.pack(nb, bs, hkv, d, 0, st[0], st[1], st[2])
+def _native_calls():
+    global _native
+    _torch()                                   # the module binds to the torch that is loaded
+    from . import torch_calls
+    _native = torch_calls
+    return _native
 
 
 def rope_axes(sections, *, interleaved=False):
@@ -701,67 +696,13 @@ def norm_rope_append_axes(q, k, v, positions, freq_axes, slot_mapping, gamma_q, 
     """norm_rope_append with positions [axes, T] int64 and the axis of each frequency
     (rope_axes); q [T, Hq, D] is written to q_out (default: in place).  rope_table as for
     norm_rope_append_cached."""
-    t = _q8 or _q8_names()
-    q_out = q if q_out is None else q_out
-    T, Hq, qs, qh = _heads(t, q, "q")
-    To, Ho, os_, oh = _heads(t, q_out, "q_out")
-    Tk, Hk, ks, kh = _heads(t, k, "k")
-    Tv, Hv, vs, vh = _heads(t, v, "v")
-    if (To, Ho) != (T, Hq) or Tk != T or Tv != T or Hk != Hv or Hk != k_cache.shape[2]:
-        raise ValueError("q, q_out, k and v must agree in tokens, and k, v and the cache in heads")
-    shape, ps = positions.shape, positions.stride()
-    if positions.dtype is not t["i64"] or len(shape) != 2 or shape[1] != T \
-            or (T > 1 and ps[1] != 1):
-        raise ValueError("positions must be int64 [axes, tokens], the tokens contiguous")
-    if len(freq_axes) != 64:
-        raise ValueError("freq_axes must be 64 bytes")
-    if rope_table is not None and (not rope_table.is_contiguous()
-                                   or rope_table.nbytes < table_positions * _ROPE_ROW_BYTES):
-        raise ValueError(f"rope_table must be contiguous and hold {table_positions} positions")
-    check(_append_axes(
-        q.data_ptr(), qs, qh, q_out.data_ptr(), os_, oh, k.data_ptr(), ks, kh,
-        v.data_ptr(), vs, vh, positions.data_ptr(), ps[0], shape[0],
-        bytes(freq_axes), _ints(slot_mapping, t["i64"], T, "slot_mapping"),
-        _gains(t, gamma_q, "gamma_q"), _gains(t, gamma_k, "gamma_k"), theta, eps, T, Hq,
-        k_cache.data_ptr(), v_cache.data_ptr(), _pack_layout(t, k_cache, v_cache),
-        _ptr(rope_table), table_positions, _flags(t, status_flags), _raw_stream(t, stream, q)))
-
-
-# -------------------------------------------------------------- score rules
-
-_RULES_PACK = struct.Struct("=fi3Q")           # pkvqk_score_rules, no padding
-assert _RULES_PACK.size == ctypes.sizeof(ScoreRules)
-_paged_decode_scored = _fast("pkvqk_paged_decode_scored", pkvqk_paged_decode_scored.argtypes)
-_paged_prefill_scored = _fast("pkvqk_paged_prefill_scored", pkvqk_paged_prefill_scored.argtypes)
-_paged_prefill_varlen_scored = _fast("pkvqk_paged_prefill_varlen_scored",
-                                     pkvqk_paged_prefill_varlen_scored.argtypes)
-
-
-def _pack_rules(t, softcap, window, slopes, first_keys, prefix_lens, rows, batch, heads):
-    if slopes is None and first_keys is None and prefix_lens is None:
-        return _RULES_PACK.pack(softcap, window, 0, 0, 0)
-    return _RULES_PACK.pack(
-        softcap, window,
-        0 if slopes is None else _ints(slopes, t["f32"], heads, "slopes"),
-        0 if first_keys is None else _ints(first_keys, t["i32"], rows, "first_keys"),
-        0 if prefix_lens is None else _ints(prefix_lens, t["i32"], batch, "prefix_lens"))
-
-
-def _attend_scored(f, q, k_cache, v_cache, block_tables, seq_lens, out, q_len, num_splits,
-                   max_seq_len_hint, scale, rules, lse_out, workspace, status_flags, stream):
-    t = _q8 or _q8_names()
-    rows, Hq, qs, qh = _heads(t, q, "q")
-    batch = seq_lens.shape[0]
-    if q_len * batch != rows:
-        raise ValueError("q must hold q_len rows for each sequence of seq_lens")
-    table, width = _table(t, block_tables, batch)
-    o, lse = _results(t, out, lse_out, rows, Hq)
-    check(f(
-        q.data_ptr(), qs, qh, k_cache.data_ptr(), v_cache.data_ptr(),
-        _pack_layout(t, k_cache, v_cache), table, width,
-        _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, q_len, Hq, num_splits,
-        max_seq_len_hint, scale, _pack_rules(t, *rules, rows, batch, Hq), o, lse,
-        *_workspace(workspace), _flags(t, status_flags), _raw_stream(t, stream, q)))
+    if type(freq_axes) is not bytes:
+        if len(freq_axes) != 64:
+            raise ValueError("freq_axes must be 64 bytes")
+        freq_axes = bytes(freq_axes)
+    check((_native or _native_calls()).append_axes(
+        q, k, v, positions, freq_axes, slot_mapping, gamma_q, gamma_k, theta, eps, k_cache, v_cache,
+        q_out, rope_table, table_positions, status_flags, stream))
 
 
 def paged_decode_scored(q, k_cache, v_cache, block_tables, seq_lens, out, *, q_len=1,
@@ -775,10 +716,10 @@ def paged_decode_scored(q, k_cache, v_cache, block_tables, seq_lens, out, *, q_l
     per row of q: no key before it; prefix_lens int32 [B]: keys that every row of the
     sequence sees, also those before them.
     """
-    _attend_scored(_paged_decode_scored, q, k_cache, v_cache, block_tables, seq_lens, out, q_len,
-                   num_splits, max_seq_len_hint, scale,
-                   (softcap, window, slopes, first_keys, prefix_lens), lse_out, workspace,
-                   status_flags, stream)
+    check((_native or _native_calls()).decode_scored(
+        q, k_cache, v_cache, block_tables, seq_lens, out, q_len, softcap, window, slopes,
+        first_keys, prefix_lens, num_splits, max_seq_len_hint, scale, lse_out, workspace,
+        status_flags, stream))
 
 
 def paged_prefill_scored(q, k_cache, v_cache, block_tables, seq_lens, out, *, q_len, softcap=0.0,
@@ -786,10 +727,10 @@ def paged_prefill_scored(q, k_cache, v_cache, block_tables, seq_lens, out, *, q_
                          max_seq_len_hint=0, scale=0.0, lse_out=None, workspace=None,
                          status_flags=None, stream=None):
     """paged_prefill under score rules (see paged_decode_scored)."""
-    _attend_scored(_paged_prefill_scored, q, k_cache, v_cache, block_tables, seq_lens, out, q_len,
-                   num_splits, max_seq_len_hint, scale,
-                   (softcap, window, slopes, first_keys, prefix_lens), lse_out, workspace,
-                   status_flags, stream)
+    check((_native or _native_calls()).prefill_scored(
+        q, k_cache, v_cache, block_tables, seq_lens, out, q_len, softcap, window, slopes,
+        first_keys, prefix_lens, num_splits, max_seq_len_hint, scale, lse_out, workspace,
+        status_flags, stream))
 
 
 def paged_prefill_varlen_scored(q, cu_seqlens_q, max_q_len, k_cache, v_cache, block_tables,
@@ -798,29 +739,10 @@ def paged_prefill_varlen_scored(q, cu_seqlens_q, max_q_len, k_cache, v_cache, bl
                                 max_seq_len_hint=0, scale=0.0, lse_out=None, workspace=None,
                                 status_flags=None, stream=None):
     """paged_prefill_varlen under score rules (see paged_decode_scored)."""
-    t = _q8 or _q8_names()
-    total_q, Hq, qs, qh = _heads(t, q, "q")
-    batch = seq_lens.shape[0]
-    table, width = _table(t, block_tables, batch)
-    o, lse = _results(t, out, lse_out, total_q, Hq)
-    check(_paged_prefill_varlen_scored(
-        q.data_ptr(), qs, qh, _ints(cu_seqlens_q, t["i32"], batch + 1, "cu_seqlens_q"), max_q_len,
-        total_q, k_cache.data_ptr(), v_cache.data_ptr(), _pack_layout(t, k_cache, v_cache), table,
-        width, _ints(seq_lens, t["i32"], batch, "seq_lens"), batch, Hq, num_splits,
-        max_seq_len_hint, scale,
-        _pack_rules(t, softcap, window, slopes, first_keys, prefix_lens, total_q, batch, Hq), o,
-        lse, *_workspace(workspace), _flags(t, status_flags), _raw_stream(t, stream, q)))
-
-
-# ----------------------------------------------------------- drafted tokens
-
-def _rows_of(x, batch, rows, vocab, name):
-    """Strides of a [batch, >= rows, vocab] view whose rows are contiguous."""
-    shape, st = x.shape, x.stride()
-    if len(shape) != 3 or shape[0] != batch or shape[1] < rows or shape[2] != vocab \
-            or (vocab > 1 and st[2] != 1):
-        raise ValueError(f"{name} must be [batch, drafts, vocab], the vocabulary contiguous")
-    return st[0], st[1]
+    check((_native or _native_calls()).prefill_varlen_scored(
+        q, cu_seqlens_q, max_q_len, k_cache, v_cache, block_tables, seq_lens, out, softcap, window,
+        slopes, first_keys, prefix_lens, num_splits, max_seq_len_hint, scale, lse_out, workspace,
+        status_flags, stream))
 
 
 def verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, tokens, num_accepted, *,
@@ -832,27 +754,6 @@ def verify_drafts(target_probs, draft_probs, draft_tokens, uniforms, tokens, num
     uniforms fp32 [B, K + 1]; tokens int32 [B, K + 1] and num_accepted int32 [B] are written,
     and kept_lens int32 [B] from seq_lens int32 [B] where both are given.
     """
-    t = _q8 or _q8_names()
-    B, K = draft_tokens.shape
-    V = target_probs.shape[-1]
-    kind = t["probs"].get(target_probs.dtype)
-    if kind is None:
-        raise ValueError("target_probs must be float32, bfloat16 or float16")
-    pb, pt = _rows_of(target_probs, B, K + 1, V, "target_probs")
-    q, qb, qt = 0, 0, 0
-    if draft_probs is not None:
-        if draft_probs.dtype is not target_probs.dtype:
-            raise ValueError("draft_probs must have target_probs' type")
-        if K:                                  # without drafts none of it is read
-            qb, qt = _rows_of(draft_probs, B, K, V, "draft_probs")
-            q = draft_probs.data_ptr()
-    i32 = t["i32"]
-    check(pkvqk_verify_drafts(
-        target_probs.data_ptr(), pb, pt, q, qb, qt, kind,
-        _ints(draft_tokens, i32, B * K, "draft_tokens"),
-        0 if draft_lens is None else _ints(draft_lens, i32, B, "draft_lens"),
-        _ints(uniforms, t["f32"], B * (K + 1), "uniforms"), B, K, V,
-        _ints(tokens, i32, B * (K + 1), "tokens"), _ints(num_accepted, i32, B, "num_accepted"),
-        0 if seq_lens is None else _ints(seq_lens, i32, B, "seq_lens"),
-        0 if kept_lens is None else _ints(kept_lens, i32, B, "kept_lens"),
-        _flags(t, status_flags), _raw_stream(t, stream, target_probs)))
+    check((_native or _native_calls()).verify_drafts(
+        target_probs, draft_probs, draft_tokens, uniforms, tokens, num_accepted, draft_lens,
+        seq_lens, kept_lens, status_flags, stream))

@@ -1,26 +1,30 @@
-"""Build libpkvqk.so (the C-ABI library) in-tree with nvcc for sm_103a.
+"""Build libpkvqk.so (the C-ABI library) in-tree with nvcc for sm_103a, and torch_calls.so.
 
     python -m paged_kv_cache_qk_gb300.build [--verbose-ptxas]
 
 Each .cu under csrc/ is compiled in parallel to an object under _build/,
 then linked into paged_kv_cache_qk_gb300/libpkvqk.so (CUDA runtime linked
 statically, no libcuda link: the TMA encoder is fetched through the runtime's
-driver entry-point query).
+driver entry-point query).  csrc/torch_calls.cpp, the binding's native part, becomes
+paged_kv_cache_qk_gb300/torch_calls.so with the host compiler, against the installed torch.
 """
 
 from __future__ import annotations
 
 import argparse
+import importlib.util
 import os
 import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libpkvqk.so")
+CALLS = os.path.join(PKG, "torch_calls.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 SOURCES = ["api.cu", "norm_rope_append.cu", "decode.cu", "combine.cu", "decode_static_ws.cu",
            "prefill.cu", "norm_rope_append_q8.cu", "decode_q8.cu", "verify_drafts.cu",
@@ -34,13 +38,30 @@ def nvcc() -> str:
     return cand
 
 
+def cxx() -> str:
+    found = shutil.which("g++") or shutil.which("c++")
+    if found is None:
+        raise RuntimeError("no C++ compiler found")
+    return found
+
+
+def torch_dir() -> str:
+    spec = importlib.util.find_spec("torch")   # its headers are wanted, not the module
+    if spec is None:
+        raise RuntimeError("torch not found")
+    return os.path.dirname(spec.origin)
+
+
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    deps.append(os.path.join(ROOT, "include", "pkvqk.h"))
-    if not force and os.path.exists(LIB):
-        t = os.path.getmtime(LIB)
+    calls_src = os.path.join(CSRC, "torch_calls.cpp")
+    torch = torch_dir()
+    deps += [os.path.join(ROOT, "include", "pkvqk.h"), calls_src,
+             os.path.join(torch, "version.py")]
+    if not force and os.path.exists(LIB) and os.path.exists(CALLS):
+        t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
         if all(os.path.getmtime(d) < t for d in deps) and os.path.getmtime(__file__) < t:
             return LIB
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
@@ -54,6 +75,14 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         objs.append(o)
         procs.append((s, subprocess.Popen([nvcc(), *flags, "-c", s, "-o", o],
                                           stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    calls_obj = os.path.join(BUILD, "torch_calls.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    procs.append((calls_src, subprocess.Popen(
+        [cxx(), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", *("-I" + i for i in include),
+         "-c", calls_src, "-o", calls_obj], stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for s, p in procs:
         out, _ = p.communicate()
@@ -63,7 +92,7 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         if p.returncode != 0:
             failed.append(s)
     if failed:
-        raise RuntimeError("nvcc failed for: " + ", ".join(failed))
+        raise RuntimeError("compilation failed for: " + ", ".join(failed))
     tmp = LIB + ".tmp"
     r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs],
                        stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
@@ -71,6 +100,15 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
         sys.stderr.write(r.stdout.decode(errors="replace"))
         raise RuntimeError("link failed")
     os.replace(tmp, LIB)
+    tmp = CALLS + ".tmp"
+    r = subprocess.run(
+        [cxx(), "-shared", "-o", tmp, calls_obj, "-L" + os.path.join(torch, "lib"),
+         "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libpkvqk.so",
+         "-Wl,-rpath,$ORIGIN"], stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    if r.returncode != 0:
+        sys.stderr.write(r.stdout.decode(errors="replace"))
+        raise RuntimeError("link failed")
+    os.replace(tmp, CALLS)
     return LIB
 
 
