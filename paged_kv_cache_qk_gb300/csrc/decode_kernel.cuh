@@ -665,11 +665,13 @@ __device__ void prefetch_before_wait(const CUtensorMap* kmap, const CUtensorMap*
   long long k1 = (j == a.num_splits - 1) ? L : min(L, k0 + chunk);
   if constexpr (kScored) {
     // the span of a window alone (first_keys may be the previous kernel's to write)
-    const long long lo = min(static_cast<long long>(window_start(
-                                 a.rules, static_cast<int>(min(L, 0x7fffffffll)) - a.q_len)), L);
-    const long long base = lo / a.block_size * a.block_size;
-    k0 = max(k0 + base, lo & ~static_cast<long long>(TK - 1));
-    k1 = (j == a.num_splits - 1) ? L : min(L, base + (j + 1) * chunk);
+    if (a.rules.window > 0) {
+      const int len = static_cast<int>(L);     // the table's slots fit an int
+      const int lo = min(window_start(a.rules, len - a.q_len), len);
+      const long long base = lo / a.block_size * a.block_size;
+      k0 = max(k0 + base, static_cast<long long>(lo & ~(TK - 1)));
+      k1 = (j == a.num_splits - 1) ? L : min(L, base + (j + 1) * chunk);
+    }
   }
   const long long key = k0 + static_cast<long long>(lane) * TK;
   if (key >= k1) return;

@@ -45,6 +45,7 @@ __device__ __forceinline__ PageSpan page_span(const DecodeArgs& a, int b, int L)
   if constexpr (!kScored) {
     return {0, 0, P};
   } else {
+    if (a.rules.window == 0 && a.rules.first_keys == nullptr) return {0, 0, P};
     const int p = L - a.q_len;                 // position of the sequence's first row
     int lo = window_start(a.rules, p);
     if (a.rules.first_keys != nullptr) {

@@ -77,13 +77,14 @@ struct Interval {
   int lo, hi;
 };
 __device__ __forceinline__ int window_start(const ScoreRules& r, int p) {
-  return r.window > 0 ? static_cast<int>(max(0ll, static_cast<long long>(p) - r.window + 1)) : 0;
+  return r.window > 0 && p >= r.window ? p - r.window + 1 : 0;
 }
 __device__ __forceinline__ int prefix_end(const ScoreRules& r, int b, int L) {
   return r.prefix_lens != nullptr ? min(r.prefix_lens[b], L) : 0;
 }
 __device__ __forceinline__ Interval visible_keys(const ScoreRules& r, int b, long long row, int p,
                                                  int L) {
+  if (r.window == 0 && r.first_keys == nullptr && r.prefix_lens == nullptr) return {0, p + 1};
   Interval v;
   v.lo = window_start(r, p);
   if (r.first_keys != nullptr) v.lo = max(v.lo, r.first_keys[row]);
