@@ -12,6 +12,7 @@ paged_kv_cache_qk_gb300/torch_calls.so with the host compiler, against the insta
 from __future__ import annotations
 
 import argparse
+import fcntl
 import importlib.util
 import os
 import shutil
@@ -54,6 +55,12 @@ def torch_dir() -> str:
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
     os.makedirs(BUILD, exist_ok=True)
+    with open(os.path.join(BUILD, "lock"), "w") as lock:
+        fcntl.flock(lock, fcntl.LOCK_EX)       # processes that build at the same time
+        return _build(verbose_ptxas, force)
+
+
+def _build(verbose_ptxas: bool, force: bool) -> str:
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
     deps = srcs + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
     calls_src = os.path.join(CSRC, "torch_calls.cpp")
