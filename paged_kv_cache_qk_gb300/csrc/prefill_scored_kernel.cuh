@@ -197,23 +197,26 @@ __device__ __forceinline__ bool make_job(const PrefillArgs& a, int bx, int by, i
   if (row0 >= w.rows) return false;
   const int prefix = a.rules.prefix_lens != nullptr ? a.rules.prefix_lens[w.b] : 0;
   const int t0 = div_group(a, row0), t1 = div_group(a, min(row0 + 2 * kM, w.rows) - 1);
-  int first = 0;
-  if (a.rules.first_keys != nullptr) {
-    first = INT_MAX;                           // the least of the rows'
-    for (int t = t0 + static_cast<int>(threadIdx.x & 31); t <= t1; t += 32) {
-      const long long row = w.q0 + t;
-      const int key = row >= 0 && row < a.total_q ? a.rules.first_keys[row] : INT_MAX;
-      first_keys[t - t0] = key;
-      first = min(first, key);
-    }
-    first = __reduce_min_sync(0xffffffffu, first);
-  }
   const long long cap = static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
   const long long L = min(static_cast<long long>(max(w.L, 0)), cap);
   w.L = static_cast<int>(L);
   w.has_b = row0 + kM < w.rows;
   const int p0 = w.L - w.q_len;                // position of the sequence's first new token
-  job.key_begin = min(w.L, max(window_start(a.rules, p0 + t0), first));
+  // The first key that any of the rows sees.  A row's bound is the later of its window's
+  // start and its first key, and the least of these bounds may lie behind both the earliest
+  // window's start and the least first key.
+  int first = window_start(a.rules, p0 + t0);
+  if (a.rules.first_keys != nullptr) {
+    first = INT_MAX;
+    for (int t = t0 + static_cast<int>(threadIdx.x & 31); t <= t1; t += 32) {
+      const long long row = w.q0 + t;
+      const int key = row >= 0 && row < a.total_q ? a.rules.first_keys[row] : INT_MAX;
+      first_keys[t - t0] = key;
+      first = min(first, max(window_start(a.rules, p0 + t), key));
+    }
+    first = __reduce_min_sync(0xffffffffu, first);
+  }
+  job.key_begin = min(w.L, first);
   // splits are counted from the page of the first key
   const long long base = job.key_begin / a.block_size * a.block_size;
   const long long chunk_keys = static_cast<long long>(a.chunk_pages) * a.block_size;
