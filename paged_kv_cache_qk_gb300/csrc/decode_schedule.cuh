@@ -49,11 +49,14 @@ __device__ __forceinline__ PageSpan page_span(const DecodeArgs& a, int b, int L)
     const int p = L - a.q_len;                 // position of the sequence's first row
     int lo = window_start(a.rules, p);
     if (a.rules.first_keys != nullptr) {
-      int least = L;
-      for (int t = 0; t < a.q_len; ++t)
-        least = min(least, max(window_start(a.rules, p + t),
-                               a.rules.first_keys[static_cast<long long>(b) * a.q_len + t]));
-      lo = max(least, 0);
+      // the first key that a row sees; a row that sees none has no say
+      const int past = prefix_end(a.rules, b, L);
+      lo = L;
+      for (int t = 0; t < a.q_len; ++t) {
+        const int key = max(window_start(a.rules, p + t),
+                            a.rules.first_keys[static_cast<long long>(b) * a.q_len + t]);
+        if (key < max(p + t + 1, past)) lo = min(lo, key);
+      }
     }
     lo = min(lo, L);
     const int first_page = lo < L ? lo / a.block_size : P;

@@ -195,16 +195,16 @@ __device__ __forceinline__ bool make_job(const PrefillArgs& a, int bx, int by, i
   }
   const int row0 = w.mt * 2 * kM;
   if (row0 >= w.rows) return false;
-  const int prefix = a.rules.prefix_lens != nullptr ? a.rules.prefix_lens[w.b] : 0;
   const int t0 = div_group(a, row0), t1 = div_group(a, min(row0 + 2 * kM, w.rows) - 1);
   const long long cap = static_cast<long long>(a.max_blocks_per_seq) * a.block_size;
   const long long L = min(static_cast<long long>(max(w.L, 0)), cap);
   w.L = static_cast<int>(L);
   w.has_b = row0 + kM < w.rows;
+  job.prefix_end = prefix_end(a.rules, w.b, w.L);
   const int p0 = w.L - w.q_len;                // position of the sequence's first new token
   // The first key that any of the rows sees.  A row's bound is the later of its window's
   // start and its first key, and the least of these bounds may lie behind both the earliest
-  // window's start and the least first key.
+  // window's start and the least first key.  A row that sees no key has no say.
   int first = window_start(a.rules, p0 + t0);
   if (a.rules.first_keys != nullptr) {
     first = INT_MAX;
@@ -212,7 +212,8 @@ __device__ __forceinline__ bool make_job(const PrefillArgs& a, int bx, int by, i
       const long long row = w.q0 + t;
       const int key = row >= 0 && row < a.total_q ? a.rules.first_keys[row] : INT_MAX;
       first_keys[t - t0] = key;
-      first = min(first, max(window_start(a.rules, p0 + t), key));
+      const int lo = max(window_start(a.rules, p0 + t), key);
+      if (lo < max(p0 + t + 1, job.prefix_end)) first = min(first, lo);
     }
     first = __reduce_min_sync(0xffffffffu, first);
   }
@@ -225,7 +226,6 @@ __device__ __forceinline__ bool make_job(const PrefillArgs& a, int bx, int by, i
   w.k1 = (w.j == a.num_splits - 1) ? w.L
                                    : static_cast<int>(min(L, base + (w.j + 1) * chunk_keys));
   job.token0 = t0;
-  job.prefix_end = min(prefix, w.L);
   const int end = max(p0 + t1 + 1, job.prefix_end);
   w.key_end = max(w.k0, min(w.k1, end));
   if (w.key_end <= job.key_begin) w.key_end = w.k0;          // nothing to see

@@ -5,6 +5,7 @@ between a row's own bound and that key.
 Bounds: those of test_gpu_scored_attention, whose Case is used.
 """
 
+import numpy as np
 import pytest
 import torch
 
@@ -76,3 +77,45 @@ def test_rows_that_see_nothing_under_a_window(lib, which, Hq, Hkv, T):
     want = _bury(c, first, window)
     assert all(f == n - T + 2 - window for f, n in zip(want, lens))
     _check(lib, c, which, first, window=window)
+
+
+@pytest.mark.parametrize("which,Hq,Hkv,T", CALLS)
+def test_rows_that_see_nothing_without_a_window(lib, which, Hq, Hkv, T):
+    """The first rows' bounds lie behind them and before every visible key."""
+    lens = [T + 100, T + 300, T + 517]
+    c = Case(Hq, Hkv, BS, lens, T, 97)
+    first = []
+    for n in lens:
+        # row t stands at n - T + t: the last row alone sees a key, its own
+        first += [n - T + t + 1 for t in range(T - 1)] + [n - 1]
+    want = _bury(c, first)
+    assert want == [n - 1 for n in lens]
+    _check(lib, c, which, first)
+
+
+@pytest.mark.parametrize("which,Hq,Hkv,T", CALLS)
+def test_sequences_of_rows_that_see_nothing(lib, which, Hq, Hkv, T):
+    """One sequence without a visible key between two that have them."""
+    lens = [T + 100, T + 300, T + 17]
+    c = Case(Hq, Hkv, BS, lens, T, 98)
+    first = [5] * T + list(range(301, T + 301)) + [0] * T
+    want = _bury(c, first)
+    assert want == [5, T + 300, 0]
+    _check(lib, c, which, first)
+
+
+@pytest.mark.parametrize("seed", range(6))
+@pytest.mark.parametrize("which,Hq,Hkv,T", CALLS)
+def test_any_first_keys(lib, which, Hq, Hkv, T, seed):
+    """Windows, first keys before, on and past their rows, and prefixes, at random."""
+    rng = np.random.default_rng(100 * seed + T)
+    lens = [int(rng.integers(T, T + 400)) for _ in range(4)]
+    c = Case(Hq, Hkv, BS, lens, T, 99)
+    window = int(rng.integers(1, 200)) if seed % 2 else 0
+    prefix = [int(rng.integers(-3, n + 9)) for n in lens] if seed % 3 == 0 else None
+    first = []
+    for n in lens:
+        low = int(rng.integers(0, n))          # no row of the sequence sees a key before it
+        first += [int(rng.integers(low, n + 3)) for _ in range(T)]
+    _bury(c, first, window, prefix)
+    _check(lib, c, which, first, prefix, window=window)
