@@ -11,7 +11,8 @@
 // What decides a border must not depend on the order of a sum: u_i q_i(x_i) is formed
 // in float64, where it is exact, and weights are summed as integers, multiples of
 // 2^-44 (exact for every fp32 probability of 2^-20 and more, off by at most 2^-45
-// below; the sum of 2^20 - 1 weights of at most 1 fits 64 bits).
+// below; the sum of 2^20 - 1 weights of at most 1 fits 64 bits), and their sum is multiplied
+// by u_K in integers too (part_of).
 //
 // A sequence is a cluster of CTAs.  Each finds j by itself (one warp: two dependent
 // gathers), then sums its slice of the vocabulary, a contiguous part a warp, and
@@ -294,6 +295,21 @@ __device__ __forceinline__ unsigned long long warp_scan(unsigned long long v) {
   return v;
 }
 
+// The whole part of u total, not rounded: u is m 2^-e with 24 bits of m, and the product's up to
+// 88 bits are formed in two halves (fp32 weights give sums of 45 bits and more, so that a
+// float64 product would round).  Below 0 and NaN u counts as 0, from 1 on as just below 1.
+__device__ __forceinline__ unsigned long long part_of(float u, unsigned long long total) {
+  if (!(u > 0.f)) return 0;
+  if (u >= 1.f) return total - 1;
+  const uint32_t bits = __float_as_uint(u);
+  const int exponent = static_cast<int>(bits >> 23);         // 0 .. 126; 0: subnormal
+  const unsigned long long m = (bits & 0x7fffffu) | (exponent > 0 ? 0x800000u : 0u);
+  const int e = 150 - max(exponent, 1);                      // 24 .. 149
+  const unsigned long long lo = m * total, hi = __umul64hi(m, total);
+  if (e < 64) return hi << (64 - e) | lo >> e;               // hi < 2^24
+  return e < 128 ? hi >> (e - 64) : 0;
+}
+
 // The first element of [begin, end) at which `before` and the weights so far pass t
 // (one warp, all lanes; the caller knows that there is one).  sums, run: sum_part's.
 template <typename T, bool kVec, bool kBoth>
@@ -437,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
   pdl_launch_dependents();
   pdl_wait();
   // what the end needs, on its way from the start
-  float u = a.uniforms[static_cast<int64_t>(b) * (a.max_drafts + 1) + a.max_drafts];
+  const float u = a.uniforms[static_cast<int64_t>(b) * (a.max_drafts + 1) + a.max_drafts];
   const int seq_len = a.kept_lens != nullptr && rank == 0 ? a.seq_lens[b] : 0;
   if (warp == 0) {
     bool bad_token = false;
@@ -507,10 +523,7 @@ __global__ void __launch_bounds__(kThreads, kCtasPerSm) verify_drafts_kernel(con
 
   int32_t* tokens = a.tokens + static_cast<int64_t>(b) * (a.max_drafts + 1);
   if (total != 0) {
-    u = fminf(fmaxf(u, 0.f), 1.f);             // NaN: 0
-    const double at = static_cast<double>(u) * static_cast<double>(total);
-    const unsigned long long t =
-        at >= static_cast<double>(total) ? total - 1 : min(total - 1, static_cast<unsigned long long>(at));
+    const unsigned long long t = part_of(u, total);
     for (int k = 0; k < warp; ++k) before += warp_sums[k];
     if (t >= before && t - before < warp_sums[warp]) {
       const int v =
