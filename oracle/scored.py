@@ -103,10 +103,12 @@ def verify_drafts(target, draft, tokens, uniforms, lens=None):
     K = K1 - 1
     out, accepted = np.full((B, K1), -1, np.int64), np.zeros(B, np.int64)
 
-    def units(row):
+    def counted(x):                            # above 1 as 1, NaN and negative ones as 0
         with np.errstate(invalid="ignore"):
-            row = np.where(row > 0, np.minimum(row, 1.0), 0.0)     # NaN: 0
-        return np.rint(np.ldexp(row, DRAFT_UNIT)).astype(np.int64)
+            return np.where(x > 0, np.minimum(x, 1.0), 0.0)
+
+    def units(row):
+        return np.rint(np.ldexp(counted(row), DRAFT_UNIT)).astype(np.int64)
 
     for b in range(B):
         n = K if lens is None else min(max(int(lens[b]), 0), K)
@@ -115,9 +117,9 @@ def verify_drafts(target, draft, tokens, uniforms, lens=None):
             x = int(tokens[b, j])
             if not 0 <= x < V:
                 break
-            qx = 1.0 if draft is None else float(draft[b, j, x])
-            px, u = float(target[b, j, x]), float(uniforms[b, j])
-            if not all(np.isfinite((qx, px, u))):
+            qx = 1.0 if draft is None else float(counted(draft[b, j, x]))
+            px, u = float(counted(target[b, j, x])), float(uniforms[b, j])
+            if not np.isfinite(u):
                 if not u * qx < px:
                     break
             elif not Fraction(u) * Fraction(qx) < Fraction(px):

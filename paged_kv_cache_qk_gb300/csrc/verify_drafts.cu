@@ -400,8 +400,10 @@ __device__ __forceinline__ int kept_drafts(const VerifyArgs& a, int b, int& n, i
     bool keep = false;
     const bool known = x >= 0 && x < a.vocab;
     if (i < n && known) {
-      const float px = value_at(p + i * a.target_stride_t + x);
-      const float qx = a.draft != nullptr ? value_at(q + i * a.draft_stride_t + x) : 1.f;
+      // as the draw counts them: NaN and below 0 as 0, above 1 as 1
+      const float px = __saturatef(value_at(p + i * a.target_stride_t + x));
+      const float qx =
+          a.draft != nullptr ? __saturatef(value_at(q + i * a.draft_stride_t + x)) : 1.f;
       keep = static_cast<double>(u) * qx < px;
     }
     const unsigned refused = __ballot_sync(0xffffffffu, !keep);

@@ -1,12 +1,14 @@
-"""pkvqk_verify_drafts where a rounding would show: every output equals the oracle's
-whole-number verdict.
+"""pkvqk_verify_drafts where a rounding, or a value that is no probability, would show:
+every output equals the oracle's whole-number verdict.
 """
 
 import numpy as np
 import pytest
 import torch
 
-from tests.test_gpu_verify_drafts import _check
+import oracle
+from tests.test_gpu_verify_drafts import TYPES, _check, _run
+from tests.test_oracle_verify_values import JUDGED
 
 pytestmark = pytest.mark.gpu
 
@@ -57,3 +59,28 @@ def test_uniforms_of_every_size(lib, V):
     p = torch.stack([r for r in rows for _ in u])
     tokens = _draw(lib, p, u * len(rows))
     assert (tokens[len(u):2 * len(u)] == 0).all()
+
+
+def _accept(lib, dtype, cases):
+    """cases: (u, q of the draft, p of it); every sequence drafts token 2 of 9."""
+    B, V = len(cases), 9
+    p = torch.full((B, 2, V), 0.0625)
+    q = torch.full((B, 1, V), 0.0625)
+    u = torch.full((B, 2), 0.5)
+    for b, (ub, qb, pb) in enumerate(cases):
+        p[b, 0, 2], q[b, 0, 2], u[b, 0] = pb, qb, ub
+    drafts = torch.full((B, 1), 2, dtype=torch.int32, device="cuda")
+    args = (p.to(TYPES[dtype]).cuda(), q.to(TYPES[dtype]).cuda(), drafts, u.cuda())
+    tokens, n, _, _ = _run(lib, *args)
+    ref, ref_n = oracle.verify_drafts(args[0].double().cpu().numpy(),
+                                      args[1].double().cpu().numpy(), drafts.cpu().numpy(),
+                                      args[3].cpu().numpy())
+    assert np.array_equal(tokens, ref) and np.array_equal(n, ref_n)
+    return n.tolist()
+
+
+@pytest.mark.parametrize("dtype", ["fp32", "bf16", "fp16"])
+def test_values_that_are_no_probabilities_decide_as_what_they_count_as(lib, dtype):
+    """Above 1 counts as 1, NaN and negative values as 0, also where a draft is judged."""
+    cases = [c[:3] for c in JUDGED]
+    assert _accept(lib, dtype, cases) == [kept for *_, kept in JUDGED]
