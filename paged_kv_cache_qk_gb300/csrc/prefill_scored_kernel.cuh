@@ -313,6 +313,7 @@ __device__ void produce_places(const PrefillArgs& a, const CUtensorMap* kmap,
     const int id_first = page_id(w, 0);
     const int slot = jobs % kJobs;
     cur.first_tile = it;
+    __syncwarp();                              // every lane's first keys are written
     if (lane == 0) {
       bars->job[slot] = cur;
       mbar_arrive(&bars->job_full[slot]);
