@@ -5,13 +5,16 @@
 Each .cu under csrc/ is compiled in parallel to an object under _build/,
 then linked into paged_kv_cache_qk_gb300/libpkvqk.so (CUDA runtime linked
 statically, no libcuda link: the TMA encoder is fetched through the runtime's
-driver entry-point query).  csrc/torch_calls.cpp, the binding's native part, becomes
+driver entry-point query).  Beside it csrc/torch_calls.cpp, the binding's native part, becomes
 paged_kv_cache_qk_gb300/torch_calls.so with the host compiler, against the installed torch.
+The library needs nvcc alone: without torch torch_calls.so is left out (its calls take
+tensors), and where it cannot be built the library is there before that is raised.
 """
 
 from __future__ import annotations
 
 import argparse
+import concurrent.futures
 import fcntl
 import importlib.util
 import os
@@ -46,11 +49,9 @@ def cxx() -> str:
     return found
 
 
-def torch_dir() -> str:
+def torch_dir() -> str | None:
     spec = importlib.util.find_spec("torch")   # its headers are wanted, not the module
-    if spec is None:
-        raise RuntimeError("torch not found")
-    return os.path.dirname(spec.origin)
+    return None if spec is None else os.path.dirname(spec.origin)
 
 
 def build(verbose_ptxas: bool = False, force: bool = False) -> str:
@@ -61,16 +62,34 @@ def build(verbose_ptxas: bool = False, force: bool = False) -> str:
 
 
 def _build(verbose_ptxas: bool, force: bool) -> str:
+    header = os.path.join(ROOT, "include", "pkvqk.h")
     srcs = [os.path.join(CSRC, s) for s in SOURCES]
-    deps = srcs + [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".h", ".cuh"))]
-    calls_src = os.path.join(CSRC, "torch_calls.cpp")
+    deps = [header, __file__] + srcs + [os.path.join(CSRC, f) for f in os.listdir(CSRC)
+                                        if f.endswith((".h", ".cuh"))]
     torch = torch_dir()
-    deps += [os.path.join(ROOT, "include", "pkvqk.h"), calls_src,
-             os.path.join(torch, "version.py")]
-    if not force and os.path.exists(LIB) and os.path.exists(CALLS):
-        t = min(os.path.getmtime(LIB), os.path.getmtime(CALLS))
-        if all(os.path.getmtime(d) < t for d in deps) and os.path.getmtime(__file__) < t:
-            return LIB
+    with concurrent.futures.ThreadPoolExecutor(1) as pool:
+        calls = None
+        if torch is not None:
+            calls_src = os.path.join(CSRC, "torch_calls.cpp")
+            calls_deps = [header, __file__, calls_src, os.path.join(torch, "version.py")]
+            if force or _stale(CALLS, calls_deps):
+                calls = pool.submit(_compile_calls, calls_src, torch)
+        if force or _stale(LIB, deps):
+            _link([nvcc(), *ARCH, "-shared"], LIB, _compile_library(srcs, verbose_ptxas))
+        if calls is not None:                  # links with the library
+            _link([cxx(), "-shared"], CALLS,
+                  [calls.result(), "-L" + os.path.join(torch, "lib"), "-ltorch_python",
+                   "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libpkvqk.so",
+                   "-Wl,-rpath,$ORIGIN"])
+    return LIB
+
+
+def _stale(out: str, deps: list) -> bool:
+    return not os.path.exists(out) or any(os.path.getmtime(d) >= os.path.getmtime(out)
+                                          for d in deps)
+
+
+def _compile_library(srcs: list, verbose_ptxas: bool) -> list:
     flags = ARCH + ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC,-O2,-fvisibility=hidden",
                     "-I", os.path.join(ROOT, "include"), "--expt-relaxed-constexpr"]
     if verbose_ptxas:
@@ -82,14 +101,6 @@ def _build(verbose_ptxas: bool, force: bool) -> str:
         objs.append(o)
         procs.append((s, subprocess.Popen([nvcc(), *flags, "-c", s, "-o", o],
                                           stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    calls_obj = os.path.join(BUILD, "torch_calls.o")
-    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
-    include = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
-               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
-               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
-    procs.append((calls_src, subprocess.Popen(
-        [cxx(), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", *("-I" + i for i in include),
-         "-c", calls_src, "-o", calls_obj], stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
     failed = []
     for s, p in procs:
         out, _ = p.communicate()
@@ -100,23 +111,31 @@ def _build(verbose_ptxas: bool, force: bool) -> str:
             failed.append(s)
     if failed:
         raise RuntimeError("compilation failed for: " + ", ".join(failed))
-    tmp = LIB + ".tmp"
-    r = subprocess.run([nvcc(), *ARCH, "-shared", "-o", tmp, *objs],
-                       stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
+    return objs
+
+
+def _compile_calls(src: str, torch: str) -> str:
+    obj = os.path.join(BUILD, "torch_calls.o")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(nvcc())))
+    include = [os.path.join(ROOT, "include"), os.path.join(torch, "include"),
+               os.path.join(torch, "include", "torch", "csrc", "api", "include"),
+               sysconfig.get_paths()["include"], os.path.join(cuda, "include")]
+    _run([cxx(), "-std=c++17", "-O2", "-fPIC", "-fvisibility=hidden", *("-I" + i for i in include),
+          "-c", src, "-o", obj], "compilation failed for: " + src)
+    return obj
+
+
+def _link(command: list, out: str, inputs: list) -> None:
+    tmp = out + ".tmp"
+    _run([*command, "-o", tmp, *inputs], "link failed: " + os.path.basename(out))
+    os.replace(tmp, out)
+
+
+def _run(command: list, failure: str) -> None:
+    r = subprocess.run(command, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
     if r.returncode != 0:
         sys.stderr.write(r.stdout.decode(errors="replace"))
-        raise RuntimeError("link failed")
-    os.replace(tmp, LIB)
-    tmp = CALLS + ".tmp"
-    r = subprocess.run(
-        [cxx(), "-shared", "-o", tmp, calls_obj, "-L" + os.path.join(torch, "lib"),
-         "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libpkvqk.so",
-         "-Wl,-rpath,$ORIGIN"], stdout=subprocess.PIPE, stderr=subprocess.STDOUT)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout.decode(errors="replace"))
-        raise RuntimeError("link failed")
-    os.replace(tmp, CALLS)
-    return LIB
+        raise RuntimeError(failure)
 
 
 def main():
