@@ -54,6 +54,12 @@ float float32(PyObject* o) {
   if (x == -1.0 && PyErr_Occurred()) throw PythonRaised{};
   return static_cast<float>(x);
 }
+// The same where the entry takes 0 as a word of its own: what fp32 only has as 0 is refused.
+float float32_or_0(PyObject* o, const char* name) {
+  const float x = float32(o);
+  if (x == 0.f && PyFloat_AsDouble(o) != 0.0) refuse(std::string(name) + " is out of range");
+  return x;
+}
 
 template <typename T = void>
 T* data(const at::Tensor& x) {
@@ -264,14 +270,14 @@ Attention attention(PyObject* q, int64_t q_len, PyObject* const* x, PyObject* co
   t.c = caches(x[0], x[1]);
   t.seq_lens = values<int32_t>(x[3], at::kInt, batch, "seq_lens");
   t.batch = count32(batch, "batch");
-  t.rules.softcap = float32(r[0]);
+  t.rules.softcap = float32_or_0(r[0], "softcap");
   t.rules.window = int32(r[1], "window");
   t.rules.slopes = values_or_none<float>(r[2], at::kFloat, t.q.heads, "slopes");
   t.rules.first_keys = values_or_none<int32_t>(r[3], at::kInt, t.q.tokens, "first_keys");
   t.rules.prefix_lens = values_or_none<int32_t>(r[4], at::kInt, batch, "prefix_lens");
   t.splits = int32(r[5], "num_splits");
   t.hint = int32(r[6], "max_seq_len_hint");
-  t.scale = float32(r[7]);
+  t.scale = float32_or_0(r[7], "scale");
   t.workspace = nullptr;
   t.workspace_bytes = 0;
   if (r[9] != Py_None) {
