@@ -71,8 +71,10 @@ def _build(verbose_ptxas: bool, force: bool) -> str:
         calls = None
         if torch is not None:
             calls_src = os.path.join(CSRC, "torch_calls.cpp")
-            calls_deps = [header, __file__, calls_src, os.path.join(torch, "version.py")]
-            if force or _stale(CALLS, calls_deps):
+            with open(os.path.join(torch, "version.py")) as f:
+                against = f"{sysconfig.get_config_var('SOABI')}\n{torch}\n{f.read()}"
+            # another torch may be older than what was built against this one
+            if force or _stale(CALLS, [header, __file__, calls_src]) or _read(_stamp()) != against:
                 calls = pool.submit(_compile_calls, calls_src, torch)
         if force or _stale(LIB, deps):
             _link([nvcc(), *ARCH, "-shared"], LIB, _compile_library(srcs, verbose_ptxas))
@@ -81,7 +83,20 @@ def _build(verbose_ptxas: bool, force: bool) -> str:
                   [calls.result(), "-L" + os.path.join(torch, "lib"), "-ltorch_python",
                    "-ltorch_cpu", "-lc10", "-lc10_cuda", "-L" + PKG, "-l:libpkvqk.so",
                    "-Wl,-rpath,$ORIGIN"])
+            with open(_stamp(), "w") as f:
+                f.write(against)
     return LIB
+
+
+def _stamp() -> str:
+    return os.path.join(BUILD, "torch_calls.against")
+
+
+def _read(path: str) -> str | None:
+    if not os.path.exists(path):
+        return None
+    with open(path) as f:
+        return f.read()
 
 
 def _stale(out: str, deps: list) -> bool:

@@ -115,6 +115,24 @@ def test_each_is_built_from_its_own_sources(tree):
         tree.settle()
 
 
+def test_another_torch_needs_another_binding(tree):
+    """Also one whose files are older than what was built."""
+    b.build()
+    tree.calls()
+    (tree.tmp / "other").mkdir()
+    (tree.tmp / "other" / "version.py").write_text("")
+    os.utime(tree.tmp / "other" / "version.py", (1, 1))
+    tree.patch.setattr(b, "torch_dir", lambda: str(tree.tmp / "other"))
+    b.build()
+    assert tree.calls() == (["cxx"], 2)
+    b.build()
+    assert tree.calls() == ([], 0)
+    (tree.tmp / "other" / "version.py").write_text("upgraded in place")
+    os.utime(tree.tmp / "other" / "version.py", (1, 1))
+    b.build()
+    assert tree.calls() == (["cxx"], 2)
+
+
 def test_torch_is_not_found_where_there_is_none(monkeypatch):
     monkeypatch.setattr(b.importlib.util, "find_spec", lambda name: None)
     assert b.torch_dir() is None
