@@ -145,9 +145,14 @@ typedef struct pkvqk_q8_cache {
  *     lo = max(0, p - window + 1 (where window > 0), first_keys[row])
  *     hi = max(p + 1, min(prefix_lens[b], seq_len))
  * So a window keeps the last `window` keys of a row, its own among them; first_keys
- * gives each token row the first key of its document (or of what is not padding); a
- * prefix is seen whole by every row of the sequence, also by those inside it, unless the
- * window or the document hides it.
+ * gives each token row the first key of its document (or of what is not padding); the
+ * keys of a prefix are seen by every row of the sequence, also by those before them, from
+ * the row's lo on.
+ * first_keys bounds a row from below alone: what keeps a row from the documents after its
+ * own is that they lie behind it, and a prefix lifts that.  With documents a prefix is the
+ * first document's and must not reach past its end; a longer one shows the rows of every
+ * document that it reaches past the keys of the next, and none of this is checked.  (Up to
+ * that end it changes nothing for later documents: they stay causal.)
  */
 typedef struct pkvqk_score_rules {
   float softcap;                     /* 0 (none) or 2^-20 .. 2^20 */
@@ -422,11 +427,11 @@ PKVQK_API pkvqk_status pkvqk_paged_decode(
  * on are read, and splits are counted from the page of that key: block-table entries
  * before it may hold anything, and max_seq_len_hint bounds the keys from there to the
  * sequence's end (a window bounds them too, without a hint); give
- * pkvqk_choose_num_splits such spans in place of lengths.  Slots past seq_lens[b] and
- * before the first visible key may hold anything, NaN included.  A V between them that is
- * not finite, or of a magnitude of 2^46 and more, may make NaN or infinities of any row of
- * its sequence and kv head.  A row with no visible key outputs 0 and lse = -inf; a row
- * with a NaN score is NaN, lse included.
+ * pkvqk_choose_num_splits such spans in place of lengths.  The first visible key is that of
+ * the rows that see any.  Slots past seq_lens[b] and before the first visible key may hold
+ * anything, NaN included.  A V between them that is not finite, or of a magnitude of 2^46
+ * and more, may make NaN or infinities of any row of its sequence and kv head.  A row with
+ * no visible key outputs 0 and lse = -inf; a row with a NaN score is NaN, lse included.
  */
 PKVQK_API pkvqk_status pkvqk_paged_decode_scored(
     const void* q, int64_t q_stride_t, int64_t q_stride_h,
@@ -560,12 +565,13 @@ typedef enum pkvqk_prob_type {
  *   kept_lens[b] = seq_lens[b] - (n - j): the keys that stay, where seq_lens[b] counts
  *   the cached tokens of the verify step; what the cache holds past them is free
  * so that with independent u, uniform in [0, 1), the tokens are distributed as the
- * target's own.  The sums are exact: probabilities count as multiples of 2^-44, to the
- * nearest.  Probabilities above 1 count as 1, NaN and negative ones as 0 (reported by
- * PKVQK_FLAG_BAD_VALUE where y's rows hold them); a row without any weight gives
- * y = -1 and the same flag.  A draft outside [0, vocab_size) is not accepted, takes no
- * weight away where draft_probs is NULL, and is reported by PKVQK_FLAG_BAD_TOKEN.
- * u_{max_drafts} counts as its nearest value in [0, 1); NaN as 0.
+ * target's own.  For y probabilities count as multiples of 2^-44, to the nearest; sums of
+ * them and u times the sum are exact.  Probabilities above 1 count as 1, NaN and negative
+ * ones as 0, where drafts are judged and where y is drawn (reported by PKVQK_FLAG_BAD_VALUE
+ * where y's rows hold them); a row without any weight gives y = -1 and the same flag.  A
+ * draft outside [0, vocab_size) is not accepted, takes no weight away where draft_probs is
+ * NULL, and is reported by PKVQK_FLAG_BAD_TOKEN.  u_{max_drafts} below 0 and NaN counts as
+ * 0, from 1 on as just below 1; the other u_i are compared as they are.
  *
  *   target_probs  device, row (b, i) of vocab_size values at
  *                 b*target_stride_b + i*target_stride_t elements, i <= max_drafts

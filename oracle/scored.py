@@ -44,7 +44,11 @@ def norm_rope_append_axes(q, k, v, positions, freq_axes, slot_mapping, gamma_q, 
 
 
 def visible(p, seq_len, window=0, first_key=0, prefix_len=0):
-    """Keys [lo, hi) that a row at position p of a sequence of seq_len keys sees."""
+    """Keys [lo, hi) that a row at position p of a sequence of seq_len keys sees.
+
+    first_key bounds from below alone: of the documents after a row's own the causal bound
+    p + 1 keeps it, which a prefix_len past its document's end lifts.
+    """
     lo = max(0, first_key, p - window + 1 if window > 0 else 0)
     hi = max(p + 1, min(prefix_len, seq_len))
     return lo, max(lo, hi)

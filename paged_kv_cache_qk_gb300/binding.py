@@ -714,7 +714,8 @@ def paged_decode_scored(q, k_cache, v_cache, block_tables, seq_lens, out, *, q_l
     softcap c > 0: s -> c tanh(s / c); slopes fp32 [Hq]: s - slope |p - n| for the row at
     position p and key n; window w > 0: only the last w keys of a row; first_keys int32, one
     per row of q: no key before it; prefix_lens int32 [B]: keys that every row of the
-    sequence sees, also those before them.
+    sequence sees, also those before them (from their first key on; with documents a prefix
+    must end inside the first, or rows see later ones).
     """
     check((_native or _native_calls()).decode_scored(
         q, k_cache, v_cache, block_tables, seq_lens, out, q_len, softcap, window, slopes,

@@ -57,7 +57,8 @@ constexpr int kRuleIntervals = 1, kRuleCap = 2, kRuleBias = 4, kRuleBounded = 8;
 // Capped scores without a bias lie in [-cap, cap].  Up to this cap (log2 units: 55.4 of the
 // scores' own) one reference serves every row, cap / 4: weights 2^(s - cap / 4) stay between
 // 2^-100 and 2^60, where fp32 and bf16 keep all their bits, and 2^20 of them with values up
-// to 2^46 fit an fp32 sum.  (In the decode kernel, which waits for HBM, the same gained
+// to 2^46 fit an fp32 sum; their products with values of 2^-26 and more are normal numbers.
+// (In the decode kernel, which waits for HBM, the same gained
 // nothing: 64 x 8192 300.9 -> 300.2 us, and its registers cost the mma tiles 5 %.)
 constexpr float kBoundedCap = 80.f;
 
@@ -496,8 +497,10 @@ __device__ void issue_places(const PrefillArgs& a, uint8_t* smem, ScoredBars* ba
 
 // add + cap * tanh(k v) of 32 raw scores, k = scale / softcap, in packed pairs.  The polynomial
 // has the cap in its coefficients and, for kSmallestK <= k <= kLargestK, k too: v R(v^2) is
-// then five instructions a pair (cap k^7, the last coefficient, neither under- nor overflows:
-// caps are 2^-20 .. 2^20 of the scores' own); another k is multiplied first.
+// then five instructions a pair; another k is multiplied first.  (Caps are 2^-20 .. 2^20 of
+// the scores' own: the last coefficient, 0.044 cap k^7, does not overflow, and at the smallest
+// of both is 2^-136, a subnormal of 13 bits.  Its term is at most 2^-10 of the value, which
+// then loses 2^-24.)
 constexpr float kSmallestK = 0x1p-16f, kLargestK = 0x1p14f;
 
 __device__ __forceinline__ void cap_chunk(float (&v)[32], float k, float cap, float add) {
