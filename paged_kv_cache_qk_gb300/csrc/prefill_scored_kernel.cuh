@@ -58,8 +58,8 @@ constexpr int kRuleIntervals = 1, kRuleCap = 2, kRuleBias = 4, kRuleBounded = 8;
 // scores' own) one reference serves every row, cap / 4: weights 2^(s - cap / 4) stay between
 // 2^-100 and 2^60, where fp32 and bf16 keep all their bits, and 2^20 of them with values up
 // to 2^46 fit an fp32 sum; their products with values of 2^-26 and more are normal numbers.
-// (In the decode kernel, which waits for HBM, the same gained
-// nothing: 64 x 8192 300.9 -> 300.2 us, and its registers cost the mma tiles 5 %.)
+// (In the decode kernel, which waits for HBM, the same gained nothing: 64 x 8192 300.9 ->
+// 300.2 us, and its registers cost the mma tiles 5 %.)
 constexpr float kBoundedCap = 80.f;
 
 // How far (log2) scores may rise above a row's reference before it follows them.  P reaches

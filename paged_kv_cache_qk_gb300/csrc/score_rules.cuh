@@ -8,8 +8,8 @@
 //     hi = max(p + 1, min(prefix_len of the sequence, seq_len)):
 // every combination of a causal mask, a window, first keys and a prefix leaves a row one
 // interval of keys.  (Documents are first keys under the causal mask; a row's interval has no
-// end of its document, so a prefix is the first document's and ends inside it.)  Scores are kept in units of log2(e), so that the softmax's 2^x takes
-// them as they are.
+// end of its document, so a prefix is the first document's and ends inside it.)  Scores are
+// kept in units of log2(e), so that the softmax's 2^x takes them as they are.
 //
 // tanh without cancellation: up to |x| = 0.5 x Q(x^2), Q of degree 3 fitted to tanh(x) / x at
 // Chebyshev nodes (largest relative error 5.5e-7, 5.9e-7 evaluated in fp32), which takes no
